@@ -414,6 +414,119 @@ ssd_status ssd_chunked_bwd(const void *x, const float *dt, const float *A, const
                            float *dinit, const ssd_dims *dims, void *workspace,
                            size_t workspace_bytes, void *stream);
 
+/*
+ * The short causal convolution in front of the scan ("Optimizing Nemotron v3
+ * Super in TensorRT-LLM", section on CausalConv1d; the layer's in_proj ->
+ * causal conv1d -> SiLU -> scan order): per channel c of C = channels[0] +
+ * channels[1] + channels[2], with W taps,
+ *
+ *     pre_t = bias_c + sum_k weight[c][k] x_{t-(W-1)+k}
+ *     y_t   = pre_t, or pre_t / (1 + e^-pre_t) with silu
+ *
+ * where the W-1 tokens before the first come from init_state (NULL = zeros).
+ *
+ *   x          [Bt, T, C]       io dtype  in   a token's channels are
+ *              consecutive, tokens and sequences lie x_token_stride and
+ *              x_batch_stride elements apart (a slice of a projection's rows);
+ *              x needs the alignment of its elements only
+ *   weight     [C, W]           float32   in   W in {2, 3, 4}
+ *   bias       [C]              float32   in   NULL = none
+ *   init_state [Bt, W-1, C]     io dtype  in   the last W-1 inputs, oldest first
+ *   seq_lens   [Bt]             int32     in   NULL = T for every sequence.
+ *              Right-padded batches: tokens at or past a sequence's length
+ *              (clamped to [0, T]) are not read, their y is written as zero,
+ *              and final_state is that after the last token before it.
+ *   y[i]       [Bt, T, channels[i]]  io dtype  out  dense; y[i] may be NULL
+ *              where channels[i] = 0.  With {H P, G N, G N} these are x, B and
+ *              C of ssd_chunked_fwd.
+ *   final_state [Bt, W-1, C]    io dtype  out  NULL = not written; may equal
+ *              init_state
+ *
+ * channels[0] >= 1, channels[1] and channels[2] >= 0.  With T = 0 final_state
+ * receives init_state (or zeros) and x and y may be NULL; with Bt = 0 nothing
+ * is done.  Sums in float32, one rounding to the io dtype.
+ */
+typedef struct {
+    int64_t batch;           /* Bt >= 0 */
+    int64_t seqlen;          /* T >= 0 (ignored by the step) */
+    int64_t width;           /* W: 2, 3 or 4 taps */
+    int64_t channels[3];     /* the three output tensors' channels */
+    int64_t x_batch_stride;  /* elements between sequences of x (rows of x_t); >= 0 */
+    int64_t x_token_stride;  /* elements between tokens of x; >= 0 (ignored by the step) */
+    int32_t io_dtype;        /* an ssd_dtype */
+    int32_t silu;            /* nonzero: y = silu(pre) */
+} ssd_conv_dims;
+
+ssd_status ssd_conv1d_fwd(const void *x, const float *weight, const float *bias,
+                          const void *init_state, const int32_t *seq_lens, void *const y[3],
+                          void *final_state, const ssd_conv_dims *dims, void *stream);
+
+/*
+ * One token per sequence.  conv_state [num_slots, W-1, C] (io dtype, in/out)
+ * is a pool of states; slots [Bt] int32 names each sequence's state (NULL =
+ * sequence b has state b, and num_slots >= Bt is required).  A slot outside
+ * [0, num_slots) marks a padded row: its y is zero and no state is touched.
+ * A slot may be named once per call: with two rows on one slot that slot's
+ * state and the y of those rows are undefined.
+ *   x_t [Bt, C] at row stride x_batch_stride; y_t[i] [Bt, channels[i]] dense.
+ * Other arguments as for ssd_conv1d_fwd.
+ */
+ssd_status ssd_conv1d_step(void *conv_state, int64_t num_slots, const int32_t *slots,
+                           const void *x_t, const float *weight, const float *bias,
+                           void *const y_t[3], const ssd_conv_dims *dims, void *stream);
+
+/*
+ * Gradients of ssd_conv1d_fwd (without seq_lens) for the loss
+ * sum(dy . y) + sum(dfinal . final_state); float32 whatever the io dtype.
+ *   dy[i]   [Bt, T, channels[i]]  float32  in   (the dx, dB, dC of ssd_chunked_bwd)
+ *   dfinal  [Bt, W-1, C]          float32  in   NULL = 0
+ *   dx      [Bt, T, C]            float32  out  dense
+ *   dweight [C, W], dbias [C]     float32  out  dbias NULL = not written
+ *   dinit   [Bt, W-1, C]          float32  out  NULL = not written
+ * workspace: ssd_conv1d_bwd_workspace_size(dims) bytes, 16-byte aligned.  With
+ * Bt = 0, dweight and dbias are zero.  No atomics: reruns are bitwise
+ * identical.
+ */
+size_t ssd_conv1d_bwd_workspace_size(const ssd_conv_dims *dims);
+ssd_status ssd_conv1d_bwd(const void *x, const float *weight, const float *bias,
+                          const void *init_state, const float *const dy[3], const float *dfinal,
+                          float *dx, float *dweight, float *dbias, float *dinit,
+                          const ssd_conv_dims *dims, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * Recurrent states in a slot pool at 8 bits per element: snapshots of prompt
+ * prefixes, and sequences swapped out.  A state is `size` consecutive float32
+ * (H P N of the SSD scan, Dm N of the selective scan); size must be a multiple
+ * of 8.  Each block of SSD_CACHE_BLOCK consecutive elements (the last one may
+ * be shorter) has one float32 scale:
+ *     scale = max|v| / q,  code = v q / max|v| rounded to the nearest code,
+ *     ties to even;  q = 127 (SSD_CACHE_INT8) or 448 (SSD_CACHE_FP8, e4m3)
+ * and reads back as code * scale.  A block whose largest magnitude is below
+ * 2^-100 is stored as zeros.  A block that holds an infinity or a NaN reads
+ * back as NaN.
+ *
+ *   codes  [num_slots, size]                     8-bit   scales 16-byte aligned
+ *   scales [num_slots, ceil(size / SSD_CACHE_BLOCK)]  float32
+ *   slots  [n] int32: state i lives in slot slots[i]
+ *
+ * ssd_cache_write stores state [n, size]; a slot outside [0, num_slots) skips
+ * that state (padded rows), slots not named keep their contents, and a slot
+ * may be named once per call (two states on one slot leave it undefined).
+ * ssd_cache_read writes state [n, size]; a slot may be named any number of
+ * times, and one outside [0, num_slots) reads as zeros (a new sequence).
+ * n = 0 does nothing.
+ */
+#define SSD_CACHE_BLOCK 64
+typedef enum { SSD_CACHE_INT8 = 0, SSD_CACHE_FP8 = 1 } ssd_cache_format;
+
+ssd_status ssd_cache_write(const float *state, int64_t n, int64_t size, const int32_t *slots,
+                           int64_t num_slots, void *codes, float *scales, int32_t format,
+                           void *stream);
+ssd_status ssd_cache_read(const void *codes, const float *scales, int64_t n, int64_t size,
+                          const int32_t *slots, int64_t num_slots, float *state, int32_t format,
+                          void *stream);
+
 /* Static text for a status code. */
 const char *ssd_status_string(ssd_status status);
 

@@ -1,0 +1,52 @@
+// Host-side launchers of the operators around the layer scan: the short causal
+// convolution, the per-channel selective scan and the 8-bit state cache
+// (internal to libssd.so).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ssd {
+
+struct ConvArgs {
+    const void *x;             // io dtype, rows at the strides below
+    const float *weight;       // [C, W]
+    const float *bias;         // [C] or NULL
+    const void *init;          // [Bt, W-1, C] io dtype or NULL (fwd, bwd)
+    const int32_t *lens;       // [Bt] or NULL (fwd)
+    void *y[3];                // dense [Bt, T, ch[i]] io dtype (fwd, step)
+    void *fin;                 // [Bt, W-1, C] io dtype or NULL (fwd)
+    const int32_t *slots;      // [Bt] or NULL (step)
+    void *state;               // [nslots, W-1, C] io dtype (step)
+    int64_t nslots;
+    const float *dy[3];        // dense [Bt, T, ch[i]] float32 (bwd)
+    const float *dfinal;       // [Bt, W-1, C] or NULL (bwd)
+    float *dx, *dweight, *dbias, *dinit;   // bwd outputs; dbias, dinit may be NULL
+    float *part;               // bwd workspace
+    int64_t Bt, T, sxb, sxt;   // batch and token strides of x, in elements
+    int64_t C;                 // channels: the sum of ch
+    int64_t ch[3];
+    int W;
+    bool silu, bf16;
+};
+hipError_t launch_conv1d_fwd(const ConvArgs &a, hipStream_t st);
+hipError_t launch_conv1d_step(const ConvArgs &a, hipStream_t st);
+hipError_t launch_conv1d_bwd(const ConvArgs &a, hipStream_t st);
+size_t conv1d_bwd_workspace(const ConvArgs &a);
+// false: more workgroups or 32-bit positions than one launch holds
+bool conv1d_fits(const ConvArgs &a);
+
+struct CacheArgs {
+    int64_t n, size, nslots;
+    const int32_t *slots;   // [n], or NULL: state i in slot i
+    void *codes;            // [nslots, size] 8-bit
+    float *scales;          // [nslots, ceil(size / 64)]
+    const float *src;       // write: [n, size]
+    float *dst;             // read: [n, size]
+    bool fp8;               // e4m3 codes (else int8)
+};
+hipError_t launch_cache_write(const CacheArgs &a, hipStream_t st);
+hipError_t launch_cache_read(const CacheArgs &a, hipStream_t st);
+
+}  // namespace ssd

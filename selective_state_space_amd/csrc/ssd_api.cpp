@@ -20,6 +20,7 @@
 #include <mutex>
 
 #include "../../include/ssd.h"
+#include "host_check.h"
 #include "ssd_launch.h"
 
 // The workspace of ssd_chunked_fwd_noalloc: a file-scope device array, one
@@ -31,6 +32,18 @@ static __device__ __align__(256) unsigned char scratch[SSD_NOALLOC_SCRATCH_BYTES
 namespace {
 
 thread_local char g_detail[512] = "";
+
+bool debug_sync() {
+    static const int on = [] {
+        const char *e = getenv("SSD_DEBUG_SYNC");
+        return (e && e[0] && e[0] != '0') ? 1 : 0;
+    }();
+    return on != 0;
+}
+
+}  // namespace
+
+namespace ssd {
 
 ssd_status fail(ssd_status st, const char *fmt, ...) {
     va_list ap;
@@ -45,21 +58,28 @@ ssd_status ok() {
     return SSD_OK;
 }
 
-bool debug_sync() {
-    static const int on = [] {
-        const char *e = getenv("SSD_DEBUG_SYNC");
-        return (e && e[0] && e[0] != '0') ? 1 : 0;
-    }();
-    return on != 0;
+ssd_status hip_result(hipError_t e, const char *what, hipStream_t st) {
+    if (e == hipSuccess && debug_sync()) {
+        e = hipStreamSynchronize(st);
+        if (e == hipSuccess) e = hipGetLastError();
+    }
+    if (e != hipSuccess) return fail(SSD_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+    return SSD_OK;
 }
 
-constexpr int64_t kMaxDim = int64_t(1) << 30;
-constexpr uint64_t kMaxGrid = (uint64_t(1) << 31) - 1;
+}  // namespace ssd
+
+namespace {
+
+using ssd::align256;
+using ssd::fail;
+using ssd::hip_result;
+using ssd::kMaxDim;
+using ssd::kMaxGrid;
+using ssd::misaligned;
+using ssd::ok;
+
 constexpr int64_t kMaxTokensPerStep = int64_t(1) << 16;   // ssd_decode_multi's K
-
-bool misaligned(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u); }
-
-size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Validates dims (and chunk_size when L > 0) and fills `s`.
 ssd_status check_dims(const ssd_dims *d, int64_t L, bool need_seq, ssd::Shape *s) {
@@ -154,16 +174,6 @@ ssd_status check_ws(const ssd::Shape &s, void *ws, size_t bytes, Ws *w) {
     return SSD_OK;
 }
 
-#define REQUIRE_PTR(p)                                                          \
-    do {                                                                        \
-        if (!(p)) return fail(SSD_ERR_NULL, "%s is NULL", #p);                  \
-        if (misaligned(p)) return fail(SSD_ERR_ALIGN, "%s is not 16-byte aligned", #p); \
-    } while (0)
-#define OPTIONAL_PTR(p)                                                         \
-    do {                                                                        \
-        if (misaligned(p)) return fail(SSD_ERR_ALIGN, "%s is not 16-byte aligned", #p); \
-    } while (0)
-
 // The optional layer interface: pointers 16-byte aligned.  Also records in
 // the shape whether y is stored in the io dtype (bf16 io only: for fp32 io
 // the io dtype is float32 already).
@@ -175,15 +185,6 @@ ssd_status check_opts(const ssd_layer_opts *o, ssd::Shape *s) {
     if (misaligned(o->dt_bias)) return fail(SSD_ERR_ALIGN, "dt_bias is not 16-byte aligned");
     if (misaligned(o->z)) return fail(SSD_ERR_ALIGN, "z is not 16-byte aligned");
     s->ybf16 = s->bf16 && o->y_io_dtype != 0;
-    return SSD_OK;
-}
-
-ssd_status hip_result(hipError_t e, const char *what, hipStream_t st) {
-    if (e == hipSuccess && debug_sync()) {
-        e = hipStreamSynchronize(st);
-        if (e == hipSuccess) e = hipGetLastError();
-    }
-    if (e != hipSuccess) return fail(SSD_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
     return SSD_OK;
 }
 

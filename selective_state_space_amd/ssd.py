@@ -21,6 +21,10 @@ The functions carry the C names:
   draft-tree parents;
 * :func:`ssd_decode_step_lp` -- the decode step on a 16-bit state;
 * :func:`ssd_chunked_bwd` -- every gradient of the chunked forward;
+* :func:`ssd_conv1d_fwd`, :func:`ssd_conv1d_step`, :func:`ssd_conv1d_bwd` -- the
+  short causal convolution in front of the scan;
+* :func:`ssd_cache_write`, :func:`ssd_cache_read` -- recurrent states in a slot
+  pool at 8 bits per element;
 * :func:`ssd_chunked_fwd_workspace_size`, :func:`ssd_chunked_fwd_workspace_layout`,
   :func:`ssd_chunked_bwd_workspace_size`, :func:`fwd_path` and
   :func:`set_path_override` (which path the forward takes, and a switch for
@@ -77,6 +81,17 @@ class LayerOpts(ctypes.Structure):
                 ("y_io_dtype", ctypes.c_int32), ("z", ctypes.c_void_p)]
 
 
+class ConvDims(ctypes.Structure):
+    """ssd_conv_dims."""
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("channels", ctypes.c_int64 * 3), ("x_batch_stride", ctypes.c_int64),
+                ("x_token_stride", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("silu", ctypes.c_int32)]
+
+
+CACHE_BLOCK = 64   # SSD_CACHE_BLOCK
+CACHE_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}   # ssd_cache_format by the codes' dtype
+
 _lib = None
 
 
@@ -90,6 +105,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                            "selective_state_space_amd.build` -- there is no fallback" % path)
     lib = ctypes.CDLL(path)
     vp, i64, sz, dp = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(Dims)
+    cdp = ctypes.POINTER(ConvDims)
     st = ctypes.c_int
     sig = {
         "ssd_chunked_fwd": ([vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, dp, vp, sz, vp], st),
@@ -116,6 +132,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                              vp, dp, vp, sz, vp], st),
         "ssd_decode_step_lp": ([vp, ctypes.POINTER(StateFormat), vp, vp, vp, vp, vp, vp, vp,
                                 ctypes.POINTER(LayerOpts), dp, vp], st),
+        "ssd_conv1d_fwd": ([vp, vp, vp, vp, vp, vp, vp, cdp, vp], st),
+        "ssd_conv1d_step": ([vp, i64, vp, vp, vp, vp, vp, cdp, vp], st),
+        "ssd_conv1d_bwd_workspace_size": ([cdp], sz),
+        "ssd_conv1d_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, cdp, vp, sz, vp], st),
+        "ssd_cache_write": ([vp, i64, i64, vp, i64, vp, vp, ctypes.c_int32, vp], st),
+        "ssd_cache_read": ([vp, vp, i64, i64, vp, i64, vp, ctypes.c_int32, vp], st),
         "ssd_status_string": ([st], ctypes.c_char_p),
         "ssd_last_error_detail": ([], ctypes.c_char_p),
         "ssd_version": ([], ctypes.c_int),
@@ -559,3 +581,203 @@ def ssd_chunked_bwd(x, dt, A, B, C, D, chunk_size, dy, init_state=None, dfinal=N
         _ptr(out["dB"]), _ptr(out["dC"]), _ptr(out["dD"]), _ptr(out["dinit"]),
         ctypes.byref(a.dims), _ptr(workspace), workspace.numel(), _stream(dev)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# The operators around the scan.
+
+def _on_gpu(t: torch.Tensor, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device.type != "cuda":
+        raise ValueError("tensors must live on a GPU device, got %s" % t.device)
+    return t.device
+
+
+def _call(fn: str, dev: torch.device, *args):
+    """One library call on dev's current stream, with dev the current device."""
+    f = getattr(load_library(), fn)
+    if torch.cuda.current_device() == dev.index:
+        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        _check(fn, st)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _opt(t, name, dtype, shape, device):
+    return None if t is None else _need(t, name, dtype, shape, device)
+
+
+def _parts3(ts):
+    return (ctypes.c_void_p * 3)(*[_addr(t) if t is not None and t.numel() else None for t in ts])
+
+
+def _conv_args(x, weight, bias, splits, silu, tokens: int):
+    """(dims, x, weight, bias, splits) of a convolution call; x [Bt, T, C] (tokens = 1)
+    or [Bt, C] (tokens = 0) keeps its strides as long as its channels are consecutive."""
+    dev = _on_gpu(x, "x")
+    io = _io_code(x.dtype)
+    if x.dim() != 2 + tokens:
+        raise ValueError("x must be %s" % ("[Bt,T,C]" if tokens else "[Bt,C]"))
+    C = x.shape[-1]
+    if weight.dim() != 2:
+        raise ValueError("weight must be [C,W]")
+    weight = _need(weight, "weight", torch.float32, (C, weight.shape[1]), dev)
+    bias = _opt(bias, "bias", torch.float32, (C,), dev)
+    splits = (C,) if splits is None else tuple(int(c) for c in splits)
+    if not 1 <= len(splits) <= 3 or sum(splits) != C or min(splits) < 0:
+        raise ValueError("splits %s must be one to three channel counts that sum to %d"
+                         % (splits, C))
+    if C > 1 and x.stride(-1) != 1 or min(x.stride()) < 0:
+        x = x.contiguous()
+    dims = ConvDims(x.shape[0], x.shape[1] if tokens else 1, weight.shape[1],
+                    (ctypes.c_int64 * 3)(*(splits + (0, 0))[:3]), x.stride(0),
+                    x.stride(1) if tokens else 0, io, 1 if silu else 0)
+    return dims, x, weight, bias, splits, dev
+
+
+def _outs(y, name, dtype, shapes, dev):
+    if y is None:
+        return tuple([torch.empty(s, dtype=dtype, device=dev) for s in shapes])
+    if len(y) != len(shapes):
+        raise ValueError("%s must hold %d tensors" % (name, len(shapes)))
+    return tuple([_need_out(t, "%s[%d]" % (name, i), dtype, s, dev)
+                  for i, (t, s) in enumerate(zip(y, shapes))])
+
+
+def ssd_conv1d_fwd(x, weight, bias=None, silu: bool = True, splits=None, init_state=None,
+                   final_state=None, want_final: bool = True, seq_lens=None, y=None):
+    """Short causal convolution of a prompt.  Returns (tuple of outputs, final_state or None).
+
+    x [Bt,T,C] (float32 or bfloat16; its channels consecutive, its rows at any
+    stride: a slice of a projection is read in place), weight [C,W] f32 with W
+    2, 3 or 4, bias [C] f32 or None.  ``splits``: one to three channel counts
+    that sum to C, one dense output [Bt,T,splits[i]] each (None = one output).
+    init_state [Bt,W-1,C] holds the inputs before the first token, oldest first
+    (None = zeros); ``final_state`` may be the same tensor.  ``seq_lens`` [Bt]
+    int32: outputs past a sequence's length are zero and its final state is
+    that at its length.
+    """
+    dims, x, weight, bias, splits, dev = _conv_args(x, weight, bias, splits, silu, 1)
+    Bt, T, C = x.shape
+    W = weight.shape[1]
+    init_state = _opt(init_state, "init_state", x.dtype, (Bt, W - 1, C), dev)
+    seq_lens = _opt(seq_lens, "seq_lens", torch.int32, (Bt,), dev)
+    if final_state is not None:
+        final_state = _need_out(final_state, "final_state", x.dtype, (Bt, W - 1, C), dev)
+    elif want_final:
+        final_state = torch.empty((Bt, W - 1, C), dtype=x.dtype, device=dev)
+    y = _outs(y, "y", x.dtype, [(Bt, T, c) for c in splits], dev)
+    _call("ssd_conv1d_fwd", dev, _addr(x), _addr(weight), _addr(bias), _addr(init_state),
+          _addr(seq_lens), _parts3(y + (None,) * (3 - len(y))), _addr(final_state),
+          ctypes.byref(dims))
+    return y, final_state
+
+
+def ssd_conv1d_step(conv_state, x_t, weight, bias=None, silu: bool = True, splits=None,
+                    slots=None, y_t=None):
+    """One token of the convolution per sequence; returns the tuple of outputs [Bt,splits[i]].
+
+    conv_state [num_slots,W-1,C] (x_t's dtype, updated in place) and slots [Bt]
+    int32 (None = sequence b has state b): a slot outside the pool marks a
+    padded row (output zero, no state touched); a slot may be named once.
+    x_t [Bt,C] may be a slice of wider rows.
+    """
+    dims, x_t, weight, bias, splits, dev = _conv_args(x_t, weight, bias, splits, silu, 0)
+    Bt, C = x_t.shape
+    if conv_state.dim() != 3:
+        raise ValueError("conv_state must be [num_slots,W-1,C]")
+    conv_state = _need_out(conv_state, "conv_state", x_t.dtype,
+                           (conv_state.shape[0], weight.shape[1] - 1, C), dev)
+    slots = _opt(slots, "slots", torch.int32, (Bt,), dev)
+    y_t = _outs(y_t, "y_t", x_t.dtype, [(Bt, c) for c in splits], dev)
+    _call("ssd_conv1d_step", dev, _addr(conv_state), conv_state.shape[0], _addr(slots),
+          _addr(x_t), _addr(weight), _addr(bias), _parts3(y_t + (None,) * (3 - len(y_t))),
+          ctypes.byref(dims))
+    return y_t
+
+
+def ssd_conv1d_bwd_workspace_size(dims: ConvDims) -> int:
+    return int(load_library().ssd_conv1d_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def ssd_conv1d_bwd(x, weight, dy, bias=None, silu: bool = True, init_state=None, dfinal=None,
+                   want_dinit: bool = True, workspace=None):
+    """Gradients of ssd_conv1d_fwd (without seq_lens), float32: a dict of dx [Bt,T,C],
+    dweight [C,W], dbias [C] (None without bias) and dinit [Bt,W-1,C] (None unless
+    ``want_dinit``).  dy: one tensor or a tuple of one to three, [Bt,T,splits[i]] f32;
+    dfinal [Bt,W-1,C] f32 or None."""
+    dy = (dy,) if isinstance(dy, torch.Tensor) else tuple(dy)
+    dims, x, weight, bias, splits, dev = _conv_args(x, weight, bias, [d.shape[-1] for d in dy],
+                                                    silu, 1)
+    Bt, T, C = x.shape
+    W = weight.shape[1]
+    dy = tuple([_need(d, "dy[%d]" % i, torch.float32, (Bt, T, c), dev)
+                for i, (d, c) in enumerate(zip(dy, splits))])
+    init_state = _opt(init_state, "init_state", x.dtype, (Bt, W - 1, C), dev)
+    dfinal = _opt(dfinal, "dfinal", torch.float32, (Bt, W - 1, C), dev)
+    if workspace is None:
+        workspace = torch.empty(max(ssd_conv1d_bwd_workspace_size(dims), 16), dtype=torch.uint8,
+                                device=dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = dict(dx=torch.empty((Bt, T, C), **f32), dweight=torch.empty((C, W), **f32),
+               dbias=None if bias is None else torch.empty((C,), **f32),
+               dinit=torch.empty((Bt, W - 1, C), **f32) if want_dinit else None)
+    _call("ssd_conv1d_bwd", dev, _addr(x), _addr(weight), _addr(bias), _addr(init_state),
+          _parts3(dy + (None,) * (3 - len(dy))), _addr(dfinal), _addr(out["dx"]),
+          _addr(out["dweight"]), _addr(out["dbias"]), _addr(out["dinit"]), ctypes.byref(dims),
+          _addr(workspace), workspace.numel() * workspace.element_size())
+    return out
+
+
+def _cache_pool(codes, scales):
+    dev = _on_gpu(codes, "codes")
+    if codes.dtype not in CACHE_FORMATS:
+        raise TypeError("codes must be int8 or float8_e4m3fn, got %s" % codes.dtype)
+    if codes.dim() != 2:
+        raise ValueError("codes must be [num_slots,size]")
+    nblk = -(-codes.shape[1] // CACHE_BLOCK)
+    codes = _need_out(codes, "codes", codes.dtype, tuple(codes.shape), dev)
+    scales = _need_out(scales, "scales", torch.float32, (codes.shape[0], nblk), dev)
+    return codes, scales, dev
+
+
+def ssd_cache_write(state, codes, scales, slots=None):
+    """Stores states at 8 bits: state [n,...] f32 (size = elements of one state, a multiple
+    of 8) into the rows ``slots`` [n] int32 of codes [num_slots,size] (int8 or
+    float8_e4m3fn) and scales [num_slots,ceil(size/64)] f32, in place.  A slot outside the
+    pool skips that state; a slot may be named once."""
+    codes, scales, dev = _cache_pool(codes, scales)
+    n, size = state.shape[0], codes.shape[1]
+    state = _need(state, "state", torch.float32, tuple(state.shape), dev)
+    if state.numel() != n * size:
+        raise ValueError("a state holds %d elements, the pool's rows %d"
+                         % (state.numel() // max(n, 1), size))
+    slots = _opt(slots, "slots", torch.int32, (n,), dev)
+    _call("ssd_cache_write", dev, _addr(state), n, size, _addr(slots), codes.shape[0],
+          _addr(codes), _addr(scales), CACHE_FORMATS[codes.dtype])
+
+
+def ssd_cache_read(codes, scales, slots=None, shape=None, state=None):
+    """Reads states back: returns state [n, *shape] f32 (shape None = [n,size]) from the rows
+    ``slots`` [n] int32 of the pool (None = every row).  A slot may be named several times;
+    one outside the pool reads as zeros."""
+    codes, scales, dev = _cache_pool(codes, scales)
+    size = codes.shape[1]
+    n = codes.shape[0] if slots is None else slots.shape[0]
+    slots = _opt(slots, "slots", torch.int32, (n,), dev)
+    full = (n, size) if shape is None else (n,) + tuple(shape)
+    state = (torch.empty(full, dtype=torch.float32, device=dev) if state is None
+             else _need_out(state, "state", torch.float32, full, dev))
+    if state.numel() != n * size:
+        raise ValueError("a state of shape %s does not hold the pool's %d elements"
+                         % (full[1:], size))
+    _call("ssd_cache_read", dev, _addr(codes), _addr(scales), n, size, _addr(slots),
+          codes.shape[0], _addr(state), CACHE_FORMATS[codes.dtype])
+    return state
