@@ -495,6 +495,95 @@ ssd_status ssd_conv1d_bwd(const void *x, const float *weight, const float *bias,
                           void *stream);
 
 /*
+ * The per-channel selective scan ("mamba-metal: running Mamba on Apple
+ * Silicon", the selective scan with a diagonal A per state element): each
+ * channel c of Dm has N states with their own decay rates, and B_t, C_t are
+ * shared by all channels,
+ *
+ *     d      = dt (+ dt_bias_c, then softplus, as the options say)
+ *     h[c,n] <- exp(d A[c,n]) h[c,n] + d x[c] B_t[n]
+ *     y[c]   = sum_n h[c,n] C_t[n] + D_c x[c]      (then y silu(z), with opts->z)
+ *
+ *   x, dt       [Bt, T, Dm]  io dtype  in
+ *   A           [Dm, N]      float32   in   natural-log decay rates (<= 0)
+ *   B, C        [Bt, T, N]   io dtype  in
+ *   D           [Dm]         float32   in
+ *   init_state  [Bt, Dm, N]  float32   in   NULL = zeros
+ *   seq_lens    [Bt]         int32     in   NULL = T for every sequence.
+ *               Right-padded batches: tokens at or past a sequence's length
+ *               (clamped to [0, T]) are not read, their y is written as zero,
+ *               and final_state is the state at the length.
+ *   y           [Bt, T, Dm]  float32   out  (io dtype with opts->y_io_dtype)
+ *   final_state [Bt, Dm, N]  float32   out  NULL = not written; may equal
+ *               init_state
+ *   opts        the layer options above: dt_bias [Dm] float32, dt_softplus,
+ *               y_io_dtype and the gate z [Bt, T, Dm] in the io dtype; may be
+ *               NULL
+ *
+ * Instantiated for N in {8, 16, 32, 64}.  workspace:
+ * ssd_selective_scan_workspace_size(dims) bytes (0 where sequences and
+ * channels alone fill the chip; workspace may then be NULL).  With T = 0
+ * final_state receives init_state (or zeros) and the token tensors may be
+ * NULL.  States and sums are float32.  Reruns are bitwise identical.
+ */
+typedef struct {
+    int64_t batch;     /* Bt >= 0 */
+    int64_t seqlen;    /* T >= 0 (ignored by the step) */
+    int64_t dim;       /* Dm >= 1 channels */
+    int64_t dstate;    /* N: 8, 16, 32 or 64 */
+    int32_t io_dtype;  /* an ssd_dtype */
+} ssd_scan_dims;
+
+size_t ssd_selective_scan_workspace_size(const ssd_scan_dims *dims);
+ssd_status ssd_selective_scan_fwd(const void *x, const void *dt, const float *A, const void *B,
+                                  const void *C, const float *D, const float *init_state,
+                                  const int32_t *seq_lens, void *y, float *final_state,
+                                  const ssd_layer_opts *opts, const ssd_scan_dims *dims,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token per sequence.  state [num_slots, Dm, N] (float32, in/out) is a
+ * pool of states; slots [Bt] int32 names each sequence's state (NULL =
+ * sequence b has state b, and num_slots >= Bt is required).  A slot outside
+ * [0, num_slots) marks a padded row: its y is zero and no state is touched.
+ * A slot may be named once per call: with two rows on one slot that slot's
+ * state and the y of those rows are undefined.
+ *   x_t, dt_t [Bt, Dm], B_t, C_t [Bt, N], y_t [Bt, Dm], opts->z [Bt, Dm].
+ */
+ssd_status ssd_selective_scan_step(float *state, int64_t num_slots, const int32_t *slots,
+                                   const void *x_t, const void *dt_t, const float *A,
+                                   const void *B_t, const void *C_t, const float *D, void *y_t,
+                                   const ssd_layer_opts *opts, const ssd_scan_dims *dims,
+                                   void *stream);
+
+/*
+ * Gradients of ssd_selective_scan_fwd (without seq_lens; with the options
+ * dt_bias, dt_softplus and z) for the loss sum(dy . y) + sum(dfinal .
+ * final_state); float32 whatever the io dtype.
+ *   dy       [Bt, T, Dm]  float32  in   (of the gated y where z is given)
+ *   dfinal   [Bt, Dm, N]  float32  in   NULL = 0
+ *   dx, ddt  [Bt, T, Dm]  float32  out  (ddt: of dt as passed)
+ *   dA       [Dm, N]      float32  out
+ *   dB, dC   [Bt, T, N]   float32  out
+ *   dD       [Dm]         float32  out
+ *   ddt_bias [Dm]         float32  out  NULL = not written
+ *   dz       [Bt, T, Dm]  float32  out  required with opts->z, else unused
+ *   dinit    [Bt, Dm, N]  float32  out  NULL = not written
+ * The states are recomputed.  workspace:
+ * ssd_selective_scan_bwd_workspace_size(dims) bytes, 16-byte aligned.  With no
+ * tokens dA, dD and ddt_bias are zero and dinit = dfinal.  No atomics: reruns
+ * are bitwise identical.
+ */
+size_t ssd_selective_scan_bwd_workspace_size(const ssd_scan_dims *dims);
+ssd_status ssd_selective_scan_bwd(const void *x, const void *dt, const float *A, const void *B,
+                                  const void *C, const float *D, const float *init_state,
+                                  const float *dy, const float *dfinal, float *dx, float *ddt,
+                                  float *dA, float *dB, float *dC, float *dD, float *ddt_bias,
+                                  float *dz, float *dinit, const ssd_layer_opts *opts,
+                                  const ssd_scan_dims *dims, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/*
  * Recurrent states in a slot pool at 8 bits per element: snapshots of prompt
  * prefixes, and sequences swapped out.  A state is `size` consecutive float32
  * (H P N of the SSD scan, Dm N of the selective scan); size must be a multiple

@@ -89,6 +89,59 @@ ssd_status check_slots(const int32_t *slots, int64_t num_slots, int64_t n) {
     return SSD_OK;
 }
 
+ssd_status check_scan(const ssd_scan_dims *d, bool need_seq, const ssd_layer_opts *o,
+                      ssd::SelArgs *a) {
+    if (!d) return fail(SSD_ERR_NULL, "dims is NULL");
+    if (d->batch < 0 || d->batch > kMaxDim)
+        return fail(SSD_ERR_SHAPE, "batch = %lld out of range [0, 2^30]", (long long)d->batch);
+    if (need_seq && (d->seqlen < 0 || d->seqlen > kMaxDim))
+        return fail(SSD_ERR_SHAPE, "seqlen = %lld out of range [0, 2^30]", (long long)d->seqlen);
+    if (d->dim < 1 || d->dim > (int64_t(1) << 24))
+        return fail(SSD_ERR_SHAPE, "dim = %lld out of range [1, 2^24]", (long long)d->dim);
+    if (d->dstate != 8 && d->dstate != 16 && d->dstate != 32 && d->dstate != 64)
+        return fail(SSD_ERR_UNSUPPORTED, "dstate = %lld; only 8, 16, 32 and 64 are instantiated",
+                    (long long)d->dstate);
+    ssd_status r = check_io(d->io_dtype);
+    if (r != SSD_OK) return r;
+    *a = ssd::SelArgs{};
+    a->Bt = d->batch;
+    a->T = need_seq ? d->seqlen : 1;
+    a->Dm = d->dim;
+    a->N = (int)d->dstate;
+    a->bf16 = d->io_dtype == SSD_BF16;
+    if (o) {
+        if (o->y_io_dtype != 0 && o->y_io_dtype != 1)
+            return fail(SSD_ERR_UNSUPPORTED, "ssd_layer_opts.y_io_dtype = %d; 0 or 1",
+                        (int)o->y_io_dtype);
+        if (misaligned(o->dt_bias)) return fail(SSD_ERR_ALIGN, "dt_bias is not 16-byte aligned");
+        if (misaligned(o->z)) return fail(SSD_ERR_ALIGN, "z is not 16-byte aligned");
+        a->dt_bias = o->dt_bias;
+        a->softplus = o->dt_softplus != 0;
+        a->ybf = a->bf16 && o->y_io_dtype != 0;
+        a->z = o->z;
+    }
+    if (!ssd::selective_scan_fits(*a))
+        return fail(SSD_ERR_SHAPE, "problem too large for one launch (batch %lld, seqlen %lld, "
+                    "dim %lld)", (long long)a->Bt, (long long)a->T, (long long)a->Dm);
+    return SSD_OK;
+}
+
+ssd_status check_workspace(void *workspace, size_t bytes, size_t need) {
+    if (need && !workspace)
+        return fail(SSD_ERR_NULL, "workspace is NULL (%zu bytes needed)", need);
+    OPTIONAL_PTR(workspace);
+    if (bytes < need)
+        return fail(SSD_ERR_WORKSPACE, "workspace_bytes = %zu < %zu required", bytes, need);
+    return SSD_OK;
+}
+
+// a pointer that is needed where there is something to read or write
+#define PTR_IF(cond, p)          \
+    do {                         \
+        if (cond) REQUIRE_PTR(p); \
+        else OPTIONAL_PTR(p);    \
+    } while (0)
+
 ssd_status check_cache(int64_t n, int64_t size, const int32_t *slots, int64_t num_slots,
                        int32_t format, ssd::CacheArgs *a) {
     if (n < 0 || n > kMaxDim)
@@ -190,12 +243,8 @@ ssd_status ssd_conv1d_bwd(const void *x, const float *weight, const float *bias,
     ssd_status r = check_conv(dims, true, &a);
     if (r != SSD_OK) return r;
     const bool tokens = a.Bt > 0 && a.T > 0;
-    if (tokens) {
-        if (!x) return fail(SSD_ERR_NULL, "x is NULL");
-        REQUIRE_PTR(dx);
-    } else {
-        OPTIONAL_PTR(dx);
-    }
+    if (tokens && !x) return fail(SSD_ERR_NULL, "x is NULL");
+    PTR_IF(tokens, dx);
     if (off_element(x, dims->io_dtype))
         return fail(SSD_ERR_ALIGN, "x is not aligned to its elements");
     REQUIRE_PTR(weight);
@@ -207,12 +256,8 @@ ssd_status ssd_conv1d_bwd(const void *x, const float *weight, const float *bias,
     OPTIONAL_PTR(dinit);
     if ((r = check_parts(reinterpret_cast<const void *const *>(dy), "dy", a, tokens)) != SSD_OK)
         return r;
-    const size_t need = ssd::conv1d_bwd_workspace(a);
-    if (need && !workspace) return fail(SSD_ERR_NULL, "workspace is NULL (%zu bytes needed)", need);
-    OPTIONAL_PTR(workspace);
-    if (workspace_bytes < need)
-        return fail(SSD_ERR_WORKSPACE, "workspace_bytes = %zu < %zu required", workspace_bytes,
-                    need);
+    if ((r = check_workspace(workspace, workspace_bytes, ssd::conv1d_bwd_workspace(a))) != SSD_OK)
+        return r;
     a.x = x;
     a.weight = weight;
     a.bias = bias;
@@ -230,21 +275,158 @@ ssd_status ssd_conv1d_bwd(const void *x, const float *weight, const float *bias,
     return ok();
 }
 
+size_t ssd_selective_scan_workspace_size(const ssd_scan_dims *dims) {
+    ssd::SelArgs a;
+    if (check_scan(dims, true, nullptr, &a) != SSD_OK) return 0;
+    return ssd::selective_scan_workspace(a);
+}
+
+ssd_status ssd_selective_scan_fwd(const void *x, const void *dt, const float *A, const void *B,
+                                  const void *C, const float *D, const float *init_state,
+                                  const int32_t *seq_lens, void *y, float *final_state,
+                                  const ssd_layer_opts *opts, const ssd_scan_dims *dims,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    ssd::SelArgs a;
+    ssd_status r = check_scan(dims, true, opts, &a);
+    if (r != SSD_OK) return r;
+    const bool tokens = a.Bt > 0 && a.T > 0;
+    PTR_IF(tokens, x);
+    PTR_IF(tokens, dt);
+    PTR_IF(a.Bt > 0, A);
+    PTR_IF(tokens, B);
+    PTR_IF(tokens, C);
+    PTR_IF(a.Bt > 0, D);
+    PTR_IF(tokens, y);
+    OPTIONAL_PTR(init_state);
+    OPTIONAL_PTR(seq_lens);
+    OPTIONAL_PTR(final_state);
+    if ((r = check_workspace(workspace, workspace_bytes, ssd::selective_scan_workspace(a))) !=
+        SSD_OK)
+        return r;
+    if (a.Bt == 0) return ok();
+    a.x = x;
+    a.dt = dt;
+    a.A = A;
+    a.B = B;
+    a.C = C;
+    a.D = D;
+    a.init = init_state;
+    a.lens = seq_lens;
+    a.y = y;
+    a.fin = final_state;
+    a.ws = workspace;
+    r = hip_result(ssd::launch_selective_scan(a, static_cast<hipStream_t>(stream)),
+                   "selective_scan_fwd", static_cast<hipStream_t>(stream));
+    if (r != SSD_OK) return r;
+    return ok();
+}
+
+ssd_status ssd_selective_scan_step(float *state, int64_t num_slots, const int32_t *slots,
+                                   const void *x_t, const void *dt_t, const float *A,
+                                   const void *B_t, const void *C_t, const float *D, void *y_t,
+                                   const ssd_layer_opts *opts, const ssd_scan_dims *dims,
+                                   void *stream) {
+    ssd::SelArgs a;
+    ssd_status r = check_scan(dims, false, opts, &a);
+    if (r != SSD_OK) return r;
+    if ((r = check_slots(slots, num_slots, a.Bt)) != SSD_OK) return r;
+    PTR_IF(a.Bt > 0, state);
+    PTR_IF(a.Bt > 0, x_t);
+    PTR_IF(a.Bt > 0, dt_t);
+    PTR_IF(a.Bt > 0, A);
+    PTR_IF(a.Bt > 0, B_t);
+    PTR_IF(a.Bt > 0, C_t);
+    PTR_IF(a.Bt > 0, D);
+    PTR_IF(a.Bt > 0, y_t);
+    if (a.Bt == 0) return ok();
+    a.state = state;
+    a.slots = slots;
+    a.nslots = num_slots;
+    a.x = x_t;
+    a.dt = dt_t;
+    a.A = A;
+    a.B = B_t;
+    a.C = C_t;
+    a.D = D;
+    a.y = y_t;
+    r = hip_result(ssd::launch_selective_step(a, static_cast<hipStream_t>(stream)),
+                   "selective_scan_step", static_cast<hipStream_t>(stream));
+    if (r != SSD_OK) return r;
+    return ok();
+}
+
+size_t ssd_selective_scan_bwd_workspace_size(const ssd_scan_dims *dims) {
+    ssd::SelArgs a;
+    if (check_scan(dims, true, nullptr, &a) != SSD_OK) return 0;
+    return ssd::selective_scan_bwd_workspace(a);
+}
+
+ssd_status ssd_selective_scan_bwd(const void *x, const void *dt, const float *A, const void *B,
+                                  const void *C, const float *D, const float *init_state,
+                                  const float *dy, const float *dfinal, float *dx, float *ddt,
+                                  float *dA, float *dB, float *dC, float *dD, float *ddt_bias,
+                                  float *dz, float *dinit, const ssd_layer_opts *opts,
+                                  const ssd_scan_dims *dims, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+    ssd::SelArgs a;
+    ssd_status r = check_scan(dims, true, opts, &a);
+    if (r != SSD_OK) return r;
+    const bool tokens = a.Bt > 0 && a.T > 0;
+    PTR_IF(tokens, x);
+    PTR_IF(tokens, dt);
+    PTR_IF(a.Bt > 0, A);
+    PTR_IF(tokens, B);
+    PTR_IF(tokens, C);
+    PTR_IF(a.Bt > 0, D);
+    PTR_IF(tokens, dy);
+    PTR_IF(tokens, dx);
+    PTR_IF(tokens, ddt);
+    REQUIRE_PTR(dA);
+    PTR_IF(tokens, dB);
+    PTR_IF(tokens, dC);
+    REQUIRE_PTR(dD);
+    PTR_IF(tokens && a.z, dz);
+    OPTIONAL_PTR(init_state);
+    OPTIONAL_PTR(dfinal);
+    OPTIONAL_PTR(ddt_bias);
+    OPTIONAL_PTR(dinit);
+    if ((r = check_workspace(workspace, workspace_bytes, ssd::selective_scan_bwd_workspace(a))) !=
+        SSD_OK)
+        return r;
+    a.x = x;
+    a.dt = dt;
+    a.A = A;
+    a.B = B;
+    a.C = C;
+    a.D = D;
+    a.init = init_state;
+    a.dy = dy;
+    a.dfinal = dfinal;
+    a.dx = dx;
+    a.ddt = ddt;
+    a.dA = dA;
+    a.dB = dB;
+    a.dC = dC;
+    a.dD = dD;
+    a.dbias = ddt_bias;
+    a.dz = dz;
+    a.dinit = dinit;
+    a.ws = workspace;
+    r = hip_result(ssd::launch_selective_scan_bwd(a, static_cast<hipStream_t>(stream)),
+                   "selective_scan_bwd", static_cast<hipStream_t>(stream));
+    if (r != SSD_OK) return r;
+    return ok();
+}
+
 ssd_status ssd_cache_write(const float *state, int64_t n, int64_t size, const int32_t *slots,
                            int64_t num_slots, void *codes, float *scales, int32_t format,
                            void *stream) {
     ssd::CacheArgs a{};
     ssd_status r = check_cache(n, size, slots, num_slots, format, &a);
     if (r != SSD_OK) return r;
-    if (n > 0) {
-        REQUIRE_PTR(state);
-        REQUIRE_PTR(codes);
-        REQUIRE_PTR(scales);
-    } else {
-        OPTIONAL_PTR(state);
-        OPTIONAL_PTR(codes);
-        OPTIONAL_PTR(scales);
-    }
+    PTR_IF(n > 0, state);
+    PTR_IF(n > 0, codes);
+    PTR_IF(n > 0, scales);
     if (n == 0) return ok();
     a.src = state;
     a.codes = codes;
@@ -261,15 +443,9 @@ ssd_status ssd_cache_read(const void *codes, const float *scales, int64_t n, int
     ssd::CacheArgs a{};
     ssd_status r = check_cache(n, size, slots, num_slots, format, &a);
     if (r != SSD_OK) return r;
-    if (n > 0) {
-        REQUIRE_PTR(state);
-        REQUIRE_PTR(codes);
-        REQUIRE_PTR(scales);
-    } else {
-        OPTIONAL_PTR(state);
-        OPTIONAL_PTR(codes);
-        OPTIONAL_PTR(scales);
-    }
+    PTR_IF(n > 0, state);
+    PTR_IF(n > 0, codes);
+    PTR_IF(n > 0, scales);
     if (n == 0) return ok();
     a.codes = const_cast<void *>(codes);
     a.scales = const_cast<float *>(scales);

@@ -49,4 +49,29 @@ struct CacheArgs {
 hipError_t launch_cache_write(const CacheArgs &a, hipStream_t st);
 hipError_t launch_cache_read(const CacheArgs &a, hipStream_t st);
 
+struct SelArgs {
+    const void *x, *dt, *B, *C, *z;   // [Bt, T, Dm] (B, C: [Bt, T, N]) io dtype; z NULL = no gate
+    const float *A, *D;               // [Dm, N], [Dm]
+    const float *dt_bias;             // [Dm] or NULL
+    const float *init;                // [Bt, Dm, N] or NULL
+    const int32_t *lens;              // [Bt] or NULL (fwd)
+    void *y;                          // [Bt, T, Dm] float32, or io dtype with ybf (fwd, step)
+    float *fin;                       // [Bt, Dm, N] or NULL (fwd)
+    float *state;                     // [nslots, Dm, N] (step)
+    const int32_t *slots;             // [Bt] or NULL (step)
+    int64_t nslots;
+    const float *dy, *dfinal;         // bwd
+    float *dx, *ddt, *dA, *dB, *dC, *dD, *dbias, *dz, *dinit;   // bwd; dbias, dz, dinit may be NULL
+    void *ws;
+    int64_t Bt, T, Dm;
+    int N;
+    bool softplus, bf16, ybf;
+};
+bool selective_scan_fits(const SelArgs &a);   // workgroups in one launch
+size_t selective_scan_workspace(const SelArgs &a);
+hipError_t launch_selective_scan(const SelArgs &a, hipStream_t st);
+hipError_t launch_selective_step(const SelArgs &a, hipStream_t st);
+size_t selective_scan_bwd_workspace(const SelArgs &a);
+hipError_t launch_selective_scan_bwd(const SelArgs &a, hipStream_t st);
+
 }  // namespace ssd

@@ -1,0 +1,242 @@
+// The per-channel selective scan: every channel c has its own decay rates
+// A[c][n], and with d = softplus(dt + bias_c)
+//
+//     h[n] <- exp(d A[c][n]) h[n] + d x B[n];   y = sum_n h[n] C[n] + D_c x,
+//
+// optionally y <- y silu(z).  ("mamba-metal: running Mamba on Apple Silicon",
+// the selective scan with a diagonal A per state element.)  The decay differs
+// for every (channel, state), so unlike the scalar-decay scan no part of it is
+// a matrix product: each state element costs an exponential and five vector
+// operations per token, 16 times more arithmetic per byte than memory needs,
+// and the kernels are bound by vector issue.
+//
+// A sequence is walked in order, tile by tile (see selective_scan.h for the
+// split over lanes).  Where sequences and channels alone do not fill the chip
+// the tokens are cut into segments as well: a first pass forms each segment's
+// end state from zero and its sum of d, a short one chains them (the decay of
+// a whole segment is exp(A sum d)), and the scan then starts every segment
+// from its true state.
+
+#include "selective_scan.h"
+
+namespace ssd {
+
+namespace {
+
+// seg [Bt][nseg][Dm][N]: end states from zero (all but the last) become the
+// states entering each segment.
+__global__ __launch_bounds__(256) void sel_chain_kernel(float *__restrict__ seg,
+                                                        const float *__restrict__ dsum,
+                                                        const float *__restrict__ A,
+                                                        const float *__restrict__ init,
+                                                        int64_t total, int32_t Dm, int32_t N,
+                                                        int32_t nseg) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // (b, c, n)
+    if (i >= total) return;
+    const int64_t per = (int64_t)Dm * N;
+    const int64_t b = i / per, cn = i % per;
+    const int64_t c = cn / N;
+    const float a2 = A[cn] * kLog2e;
+    float h = init ? init[i] : 0.f;
+    float *p = seg + b * nseg * per + cn;
+    const float *q = dsum + b * nseg * Dm + c;
+    for (int32_t k = 0; k < nseg; ++k) {
+        const bool more = k + 1 < nseg;
+        const float e = more ? p[k * per] : 0.f;
+        const float d = more ? q[(int64_t)k * Dm] : 0.f;
+        p[k * per] = h;
+        h = fmaf(fast_exp2(d * a2), h, e);
+    }
+}
+
+// One token per sequence: the state is read and written once, which is all
+// the traffic that counts.  A lane keeps its 4 decay rates for R sequences
+// (A is as large as one sequence's state).
+template <int N, typename Tio, typename Ty, bool GATE, int R>
+__global__ __launch_bounds__(256) void sel_step_kernel(
+    float *__restrict__ state, const int32_t *__restrict__ slots, int64_t nslots,
+    const Tio *__restrict__ x, const Tio *__restrict__ dt, const float *__restrict__ A,
+    const Tio *__restrict__ B, const Tio *__restrict__ C, const float *__restrict__ D,
+    const Tio *__restrict__ z, const float *__restrict__ dt_bias, Ty *__restrict__ y, int32_t Bt,
+    int32_t Dm, int32_t ncb, int32_t softplus) {
+    constexpr int S = SelSplit<N>::S, CPW = SelSplit<N>::CPW, CB = SelSplit<N>::CB;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t cb = blockIdx.x % (uint32_t)ncb;
+    const int64_t b0 = (int64_t)(blockIdx.x / (uint32_t)ncb) * R;
+    const int s = lane % S;
+    const int32_t c = cb * CB + wave * CPW + lane / S;
+    if (c >= Dm) return;
+    float4 hv[R], bv[R], cv[R];
+    float xv[R], dv[R], zv[R];
+    float *hp[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t b = b0 + r;
+        const int64_t slot = b < Bt ? (slots ? (int64_t)slots[b] : b) : -1;
+        hp[r] = slot >= 0 && slot < nslots ? state + (slot * Dm + c) * N + 4 * s : nullptr;
+        if (hp[r]) {
+            hv[r] = load_nt(hp[r]);
+            bv[r] = widen4(load_raw<false>(B + b * N + 4 * s, 4));
+            cv[r] = widen4(load_raw<false>(C + b * N + 4 * s, 4));
+            xv[r] = load1(x + b * Dm + c);
+            dv[r] = load1(dt + b * Dm + c);
+            if constexpr (GATE) zv[r] = load1(z + b * Dm + c);
+        }
+    }
+    const float4 av = *reinterpret_cast<const float4 *>(A + (int64_t)c * N + 4 * s);
+    const float bias = dt_bias ? dt_bias[c] : 0.f, Dc = D[c];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t b = b0 + r;
+        if (b >= Bt) break;
+        float out = 0.f;
+        if (hp[r]) {
+            float d = dv[r] + bias;
+            if (softplus) d = softplus_f(d);
+            const float u = d * xv[r], d2 = d * kLog2e;
+            float4 h = hv[r];
+            h.x = fmaf(fast_exp2(d2 * av.x), h.x, u * bv[r].x);
+            h.y = fmaf(fast_exp2(d2 * av.y), h.y, u * bv[r].y);
+            h.z = fmaf(fast_exp2(d2 * av.z), h.z, u * bv[r].z);
+            h.w = fmaf(fast_exp2(d2 * av.w), h.w, u * bv[r].w);
+            store_nt(hp[r], h);
+            out = chan_sum<S>(h.x * cv[r].x + h.y * cv[r].y + h.z * cv[r].z + h.w * cv[r].w);
+            out += Dc * xv[r];
+            if constexpr (GATE) out *= fast_silu(zv[r]);
+        }
+        if (s == 0) {
+            if constexpr (sizeof(Ty) == 2)
+                y[b * Dm + c] = (uint16_t)f32_to_bf16_bits(out);
+            else
+                y[b * Dm + c] = out;
+        }
+    }
+}
+
+struct Segs {
+    int64_t n, len;
+};
+// Segments of a sequence: one where sequences and channel blocks alone give 2
+// workgroups per CU (a second pass over the tokens costs more than the idle
+// lanes), else enough for 4, of at least 64 tokens each.
+Segs segments(const SelArgs &a) {
+    const int64_t blocks = a.Bt * chan_blocks(a);
+    const int64_t tile = a.N;
+    Segs s{1, cdiv64(a.T > 0 ? a.T : 1, tile) * tile};
+    if (blocks >= 512 || blocks == 0) return s;
+    int64_t n = cdiv64(1024, blocks);
+    n = n < a.T / 64 ? n : a.T / 64;
+    if (n < 2) return s;
+    s.len = cdiv64(cdiv64(a.T, n), tile) * tile;
+    s.n = cdiv64(a.T, s.len);
+    return s;
+}
+size_t seg_bytes(const SelArgs &a, const Segs &s) {
+    return s.n > 1 ? (size_t)(a.Bt * s.n * a.Dm * a.N) * sizeof(float) : 0;
+}
+
+// f(y type): bf16 where the caller asked for the io dtype and that is bf16
+template <typename F>
+void by_y(const SelArgs &a, F f) {
+    if (a.ybf)
+        f(uint16_t());
+    else
+        f(float());
+}
+
+}  // namespace
+
+bool selective_scan_fits(const SelArgs &a) {
+    // workgroups of the widest launch (segments of 16 tokens in the backward)
+    const double blocks = (double)a.Bt * (double)chan_blocks(a);
+    return blocks * 1024.0 < 0x1p31 && (double)a.Bt * (double)a.Dm * (double)a.N < 0x1p38 &&
+           (double)a.Bt * (double)a.T * (double)a.N < 0x1p38;
+}
+
+size_t selective_scan_workspace(const SelArgs &a) {
+    const Segs s = segments(a);
+    const size_t b = seg_bytes(a, s);
+    return b ? b + (size_t)(a.Bt * s.n * a.Dm) * sizeof(float) : 0;
+}
+
+hipError_t launch_selective_scan(const SelArgs &a, hipStream_t st) {
+    const Segs sg = segments(a);
+    SelGeom g;
+    g.T = a.T;
+    g.Bt = a.Bt;
+    g.Dm = (int32_t)a.Dm;
+    g.ncb = (int32_t)chan_blocks(a);
+    g.nseg = (int32_t)sg.n;
+    g.seg_len = sg.len;
+    g.softplus = a.softplus ? 1 : 0;
+    const bool rag = a.Dm % 4 != 0;
+    const float *start = a.init;
+    hipError_t e = hipSuccess;
+    if (sg.n > 1) {
+        float *seg = static_cast<float *>(a.ws);
+        float *dsum = seg + (size_t)(a.Bt * sg.n * a.Dm * a.N);
+        by_state(a, [&](auto n, auto io) {
+            typedef decltype(io) Tio;
+            by_flag(rag, [&](auto r) {
+                sel_scan_kernel<decltype(n)::value, Tio, float, false, decltype(r)::value, SCAN_END>
+                    <<<dim3((uint32_t)(a.Bt * (sg.n - 1) * g.ncb)), 256, 0, st>>>(
+                        (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B, nullptr,
+                        nullptr, nullptr, a.dt_bias, nullptr, a.lens, nullptr, seg, dsum,
+                        nullptr, nullptr, g);
+            });
+        });
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const int64_t total = a.Bt * a.Dm * a.N;
+        sel_chain_kernel<<<dim3((uint32_t)cdiv64(total, 256)), 256, 0, st>>>(
+            seg, dsum, a.A, a.init, total, (int32_t)a.Dm, (int32_t)a.N, (int32_t)sg.n);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        start = seg;
+    }
+    by_state(a, [&](auto n, auto io) {
+        typedef decltype(io) Tio;
+        by_flag(rag, [&](auto r) {
+            by_flag(a.z != nullptr, [&](auto gate) {
+                by_y(a, [&](auto yt) {
+                    typedef decltype(yt) Ty;
+                    if constexpr (sizeof(Ty) == 4 || sizeof(Tio) == 2)   // bf16 y only for bf16 io
+                        sel_scan_kernel<decltype(n)::value, Tio, Ty, decltype(gate)::value,
+                                        decltype(r)::value, SCAN_OUT>
+                            <<<dim3((uint32_t)(a.Bt * sg.n * g.ncb)), 256, 0, st>>>(
+                                (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B,
+                                (const Tio *)a.C, a.D, (const Tio *)a.z, a.dt_bias, start, a.lens,
+                                (Ty *)a.y, a.fin, nullptr, nullptr, nullptr, g);
+                });
+            });
+        });
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_selective_step(const SelArgs &a, hipStream_t st) {
+    const int64_t ncb = chan_blocks(a);
+    // 4 sequences per lane where that leaves 2 workgroups per CU
+    const bool four = a.Bt * ncb >= 4 * 512;
+    const dim3 grid((uint32_t)(ncb * cdiv64(a.Bt, four ? 4 : 1)));
+    by_state(a, [&](auto n, auto io) {
+        typedef decltype(io) Tio;
+        by_flag(a.z != nullptr, [&](auto gate) {
+            by_flag(four, [&](auto f) {
+                by_y(a, [&](auto yt) {
+                    typedef decltype(yt) Ty;
+                    if constexpr (sizeof(Ty) == 4 || sizeof(Tio) == 2)
+                        sel_step_kernel<decltype(n)::value, Tio, Ty, decltype(gate)::value,
+                                        decltype(f)::value ? 4 : 1><<<grid, 256, 0, st>>>(
+                            a.state, a.slots, a.nslots, (const Tio *)a.x, (const Tio *)a.dt, a.A,
+                            (const Tio *)a.B, (const Tio *)a.C, a.D, (const Tio *)a.z, a.dt_bias,
+                            (Ty *)a.y, (int32_t)a.Bt, (int32_t)a.Dm, (int32_t)ncb,
+                            a.softplus ? 1 : 0);
+                });
+            });
+        });
+    });
+    return hipGetLastError();
+}
+
+}  // namespace ssd

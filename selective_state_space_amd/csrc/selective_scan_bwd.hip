@@ -1,0 +1,668 @@
+// Gradients of the per-channel selective scan.  With a_t = exp(d_t A), the
+// states h_t of the forward, dyp = dy silu(z) (dy without a gate) and g the
+// adjoint of the state, g_T = dfinal and from the last token to the first
+//
+//     g      = (carried) + dyp_t C_t
+//     dC_t   = sum_c dyp h_t        dB_t = sum_c g d x
+//     gB     = sum_n g B_t          q = a_t g h_{t-1}   (per c, n)
+//     dx_t   = d gB + D dyp         dd_t = x gB + sum_n q A
+//     dA    += d q                  (carried) = a_t g
+//
+// and ddt = dd sigmoid(dt + bias) under softplus, dbias = sum ddt, dD = sum
+// dyp x, dz = dy (sum_n h C + D x) silu'(z).
+//
+// The states are not kept by the forward: a first pass scans again and writes
+// the state before every 16th token; the reverse pass then recomputes a
+// tile's 16 states into registers (4 per lane and token) and walks them
+// backwards, so every h_{t-1} is exact, never divided out.  Sums over n are
+// made on the S lanes of a channel.  Sums over channels (dB, dC: 8 values per
+// lane and token) halve the values with every lane distance (permlane32 and
+// permlane16 swaps), then rotate within a row; wavefronts are joined in LDS
+// and channel blocks by a last kernel.  Every sum has a fixed order.
+//
+// With several segments per sequence (few rows, see segments() of the forward)
+// the first pass starts each segment from zero and the reverse pass adds the
+// decayed entry state to its checkpoints; the adjoints entering the segments
+// come from a reverse pass without outputs and a chain over segments.
+
+#include "selective_scan.h"
+
+namespace ssd {
+
+namespace {
+
+constexpr int TB = 16;   // tokens of a backward tile, and between checkpoints
+
+template <int N>
+struct BTile {
+    static constexpr int VPR = SelSplit<N>::CB / 4;              // 4-channel vectors of a row
+    static constexpr int ITEMS = TB * VPR;                       // (token, vector) pairs
+    static constexpr int NI = (ITEMS + 255) / 256;               // of them per thread
+    static constexpr int ROWS = ITEMS < 256 ? ITEMS / VPR : 256 / VPR;
+    static constexpr int BC = TB * N / 4;                        // 4-element vectors of B (or C)
+    static constexpr int NBC = (2 * BC + 255) / 256;
+};
+
+// 8 values per lane summed over the channels of the wavefront: afterwards the
+// lanes of each half (0 = v[0..3], 1 = v[4..7]) and row parity hold the sums of
+// values 2 parity and 2 parity + 1 of their half for their lane s.
+__device__ __forceinline__ float add_swapped32(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
+                                                    false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float add_swapped16(float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false,
+                                                    false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+template <int S>
+__device__ __forceinline__ float row_sum(float v) {
+    if constexpr (S <= 8) v += dpp_mov<0x128>(v);   // row_ror:8
+    if constexpr (S <= 4) v += dpp_mov<0x124>(v);   // row_ror:4
+    if constexpr (S <= 2) v += dpp_mov<0x122>(v);   // row_ror:2
+    return v;
+}
+template <int S>
+__device__ __forceinline__ float2 channels_sum(const float (&v)[8]) {
+    float r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = add_swapped32(v[i], v[i + 4]);
+    return make_float2(row_sum<S>(add_swapped16(r[0], r[2])),
+                       row_sum<S>(add_swapped16(r[1], r[3])));
+}
+
+// silu(z) and its derivative
+__device__ __forceinline__ void silu_grad(float z, float &f, float &df) {
+    const float s = sigmoid_f(z);
+    f = z * s;
+    df = s * (1.f + z * (1.f - s));
+}
+
+// The adjoint leaving a segment at its first token, started from zero after
+// its last one (segments 1 .. nseg-1).
+template <int N, typename Tio, bool GATE, bool RAG>
+__global__ __launch_bounds__(256) void sel_adj_kernel(
+    const Tio *__restrict__ dt, const float *__restrict__ A, const Tio *__restrict__ C,
+    const Tio *__restrict__ z, const float *__restrict__ dt_bias, const float *__restrict__ dy,
+    float *__restrict__ adj, SelGeom g) {
+    constexpr int S = SelSplit<N>::S, CPW = SelSplit<N>::CPW, CB = SelSplit<N>::CB;
+    constexpr int VPR = BTile<N>::VPR, NI = BTile<N>::NI, ITEMS = BTile<N>::ITEMS;
+    constexpr int BC = BTile<N>::BC;
+    __shared__ __align__(16) float2 sdy[TB][CB];   // (d, dyp)
+    __shared__ __align__(16) float sc[TB][N];
+    const int tid = threadIdx.x;
+    const uint32_t cb = blockIdx.x % (uint32_t)g.ncb;
+    const uint32_t rest = blockIdx.x / (uint32_t)g.ncb;
+    const int64_t b = rest / (uint32_t)(g.nseg - 1);
+    const int32_t seg = 1 + rest % (uint32_t)(g.nseg - 1);
+    const int64_t t0 = seg * g.seg_len, t1 = min(g.T, t0 + g.seg_len);
+    const int sv = tid % VPR;
+    const int32_t ch0 = cb * CB + 4 * sv;
+    const int chn = min(4, g.Dm - ch0);
+    float bias[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bias[i] = dt_bias && i < chn ? dt_bias[ch0 + i] : 0.f;
+    const int lane = tid & 63, wave = tid >> 6;
+    const int s = lane % S, cl = wave * CPW + lane / S;
+    const int32_t c = cb * CB + cl;
+    float a2[4] = {}, car[4] = {};
+    if (c < g.Dm) {
+        const float4 av = *reinterpret_cast<const float4 *>(A + (int64_t)c * N + 4 * s);
+        a2[0] = av.x * kLog2e;
+        a2[1] = av.y * kLog2e;
+        a2[2] = av.z * kLog2e;
+        a2[3] = av.w * kLog2e;
+    }
+    const int64_t ntile = (t1 - t0 + TB - 1) / TB;
+    for (int64_t k = ntile - 1; k >= 0; --k) {
+        const int64_t tb = t0 + k * TB;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = tid + 256 * i, r = e / VPR;
+            const int64_t t = tb + r;
+            if (e < ITEMS) {
+                float d[4] = {}, p[4] = {};
+                if (t < t1 && chn > 0) {
+                    const int64_t o = (b * g.T + t) * g.Dm + ch0;
+                    const float4 dv = widen4(load_raw<RAG>(dt + o, chn));
+                    const float4 yv = widen4(load_raw<RAG>(dy + o, chn));
+                    float4 zv = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if constexpr (GATE) zv = widen4(load_raw<RAG>(z + o, chn));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float rw = (&dv.x)[j] + bias[j];
+                        d[j] = g.softplus ? softplus_f(rw) : rw;
+                        p[j] = (&yv.x)[j];
+                        if constexpr (GATE) p[j] *= fast_silu((&zv.x)[j]);
+                    }
+                }
+                float4 *w = reinterpret_cast<float4 *>(&sdy[r][4 * sv]);
+                w[0] = make_float4(d[0], p[0], d[1], p[1]);
+                w[1] = make_float4(d[2], p[2], d[3], p[3]);
+            }
+        }
+        for (int e = tid; e < BC; e += 256) {
+            const int64_t t = tb + e / (N / 4);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t < t1) v = widen4(load_raw<false>(C + (b * g.T + t) * N + 4 * (e % (N / 4)), 4));
+            reinterpret_cast<float4 *>(&sc[0][0])[e] = v;
+        }
+        lds_barrier();
+#pragma unroll
+        for (int t = TB - 1; t >= 0; --t) {
+            const float2 w = sdy[t][cl];
+            const float4 cv = *reinterpret_cast<const float4 *>(&sc[t][4 * s]);
+            car[0] = fast_exp2(w.x * a2[0]) * fmaf(w.y, cv.x, car[0]);
+            car[1] = fast_exp2(w.x * a2[1]) * fmaf(w.y, cv.y, car[1]);
+            car[2] = fast_exp2(w.x * a2[2]) * fmaf(w.y, cv.z, car[2]);
+            car[3] = fast_exp2(w.x * a2[3]) * fmaf(w.y, cv.w, car[3]);
+        }
+        lds_barrier();
+    }
+    if (c < g.Dm)
+        *reinterpret_cast<float4 *>(adj + (((b * g.nseg) + seg) * g.Dm + c) * N + 4 * s) =
+            make_float4(car[0], car[1], car[2], car[3]);
+}
+
+// Both chains over the segments: the states entering each (hseg, in place of
+// the end states) and the adjoints entering each from the right (adj).
+__global__ __launch_bounds__(256) void sel_chain_bwd_kernel(
+    float *__restrict__ hseg, float *__restrict__ adj, const float *__restrict__ dsum,
+    const float *__restrict__ A, const float *__restrict__ init,
+    const float *__restrict__ dfinal, int64_t total, int32_t Dm, int32_t N, int32_t nseg) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // (b, c, n)
+    if (i >= total) return;
+    const int64_t per = (int64_t)Dm * N;
+    const int64_t b = i / per, cn = i % per;
+    const float a2 = A[cn] * kLog2e;
+    const float *q = dsum + b * nseg * Dm + cn / N;
+    float *p = hseg + b * nseg * per + cn;
+    float h = init ? init[i] : 0.f;
+    for (int32_t k = 0; k < nseg; ++k) {
+        const float e = p[k * per];
+        p[k * per] = h;
+        h = fmaf(fast_exp2(q[(int64_t)k * Dm] * a2), h, e);
+    }
+    p = adj + b * nseg * per + cn;
+    float r = dfinal ? dfinal[i] : 0.f;
+    for (int32_t k = nseg - 1; k >= 0; --k) {
+        const float e = k > 0 ? p[k * per] : 0.f;
+        p[k * per] = r;
+        r = fmaf(fast_exp2(q[(int64_t)k * Dm] * a2), r, e);
+    }
+}
+
+template <int N, typename Tio, bool GATE, bool RAG>
+__global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
+    const Tio *__restrict__ x, const Tio *__restrict__ dt, const float *__restrict__ A,
+    const Tio *__restrict__ B, const Tio *__restrict__ C, const float *__restrict__ D,
+    const Tio *__restrict__ z, const float *__restrict__ dt_bias, const float *__restrict__ dy,
+    const float *__restrict__ right, const float *__restrict__ ckpt,
+    const float *__restrict__ cumd, const float *__restrict__ hseg, float *__restrict__ dx,
+    float *__restrict__ ddt, float *__restrict__ dz, float *__restrict__ dinit,
+    float *__restrict__ pbc, float *__restrict__ pA, float *__restrict__ pD,
+    float *__restrict__ pbias, SelGeom g) {
+    constexpr int S = SelSplit<N>::S, CPW = SelSplit<N>::CPW, CB = SelSplit<N>::CB;
+    constexpr int VPR = BTile<N>::VPR, NI = BTile<N>::NI, ITEMS = BTile<N>::ITEMS;
+    constexpr int BC = BTile<N>::BC, NBC = BTile<N>::NBC, ROWS = BTile<N>::ROWS;
+    __shared__ __align__(16) float2 sdu[TB][CB];          // (d, d x)
+    __shared__ __align__(16) float sdy[TB][CB];           // dyp
+    __shared__ __align__(16) float sbc[2][TB][N];
+    __shared__ __align__(16) float2 sgd[TB][CB];          // (gB, sum q a2)
+    __shared__ __align__(16) float sy[GATE ? TB : 1][GATE ? CB : 4];
+    __shared__ __align__(16) float sdbc[4][TB][2 * N];
+    const int tid = threadIdx.x;
+    const uint32_t cb = blockIdx.x % (uint32_t)g.ncb;
+    const uint32_t rest = blockIdx.x / (uint32_t)g.ncb;   // (b, segment)
+    const int64_t b = rest / (uint32_t)g.nseg;
+    const int32_t seg = rest % (uint32_t)g.nseg;
+    const int64_t t0 = seg * g.seg_len, t1 = min(g.T, t0 + g.seg_len);
+    const int64_t ntile = (t1 - t0 + TB - 1) / TB;
+
+    const int sv = tid % VPR;
+    const int32_t ch0 = cb * CB + 4 * sv;
+    const int chn = min(4, g.Dm - ch0);
+    float bias[4], Dv[4], accD[4] = {}, accb[4] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        bias[i] = dt_bias && i < chn ? dt_bias[ch0 + i] : 0.f;
+        Dv[i] = i < chn ? D[ch0 + i] : 0.f;
+    }
+    const int lane = tid & 63, wave = tid >> 6;
+    const int s = lane % S, cl = wave * CPW + lane / S;
+    const int32_t c = cb * CB + cl;
+    float a2[4] = {}, car[4] = {}, dA[4] = {};
+    float4 hs = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < g.Dm) {
+        const float4 av = *reinterpret_cast<const float4 *>(A + (int64_t)c * N + 4 * s);
+        a2[0] = av.x * kLog2e;
+        a2[1] = av.y * kLog2e;
+        a2[2] = av.z * kLog2e;
+        a2[3] = av.w * kLog2e;
+        const int64_t u = ((int64_t)rest * g.Dm + c) * N + 4 * s;
+        if (right) {   // [Bt][nseg][Dm][N]: with one segment dfinal
+            const float4 rv = *reinterpret_cast<const float4 *>(right + u);
+            car[0] = rv.x;
+            car[1] = rv.y;
+            car[2] = rv.z;
+            car[3] = rv.w;
+        }
+        if (g.nseg > 1) hs = *reinterpret_cast<const float4 *>(hseg + u);
+    }
+
+    struct Tok {
+        Raw4<Tio> x, dt, z;
+        Raw4<float> dy;
+    };
+    auto load_tok = [&](int64_t tb, int i) {
+        const int e = tid + 256 * i;
+        const int64_t t = tb + e / VPR;
+        Tok r;
+        zero_raw(r.x);
+        zero_raw(r.dt);
+        zero_raw(r.z);
+        zero_raw(r.dy);
+        if (e < ITEMS && tb >= t0 && t < t1 && chn > 0) {
+            const int64_t o = (b * g.T + t) * g.Dm + ch0;
+            r.x = load_raw<RAG>(x + o, chn);
+            r.dt = load_raw<RAG>(dt + o, chn);
+            r.dy = load_raw<RAG>(dy + o, chn);
+            if constexpr (GATE) r.z = load_raw<RAG>(z + o, chn);
+        }
+        return r;
+    };
+    auto load_bc = [&](int64_t tb, int k) {
+        const int e = tid + 256 * k;
+        Raw4<Tio> r;
+        zero_raw(r);
+        if (e < 2 * BC) {
+            const int o = e % BC;
+            const int64_t t = tb + o / (N / 4);
+            if (tb >= t0 && t < t1)
+                r = load_raw<false>((e / BC ? C : B) + (b * g.T + t) * N + 4 * (o % (N / 4)), 4);
+        }
+        return r;
+    };
+    auto load_h0 = [&](int64_t tb) {
+        float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < g.Dm && tb >= t0) {
+            const int64_t u = (b * ((g.T + 15) >> 4) + (tb >> 4)) * g.Dm + c;
+            h = *reinterpret_cast<const float4 *>(ckpt + u * N + 4 * s);
+            if (g.nseg > 1) {
+                const float cd = cumd[u];
+                h.x = fmaf(fast_exp2(cd * a2[0]), hs.x, h.x);
+                h.y = fmaf(fast_exp2(cd * a2[1]), hs.y, h.y);
+                h.z = fmaf(fast_exp2(cd * a2[2]), hs.z, h.z);
+                h.w = fmaf(fast_exp2(cd * a2[3]), hs.w, h.w);
+            }
+        }
+        return h;
+    };
+
+    int64_t tb = t0 + (ntile - 1) * TB;
+    Tok tok[NI];
+    Raw4<Tio> rbc[NBC];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) tok[i] = load_tok(tb, i);
+#pragma unroll
+    for (int k = 0; k < NBC; ++k) rbc[k] = load_bc(tb, k);
+    float4 h0 = load_h0(tb);
+
+    for (; tb >= t0; tb -= TB) {
+        // stage
+        float dkeep[NI][4];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = tid + 256 * i, r = e / VPR;
+            if (e < ITEMS) {
+                const float4 xv = widen4(tok[i].x), dv = widen4(tok[i].dt), yv = tok[i].dy.v;
+                const float4 zv = widen4(tok[i].z);
+                float u[4], p[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float rw = (&dv.x)[j] + bias[j];
+                    float d = g.softplus ? softplus_f(rw) : rw;
+                    if (tb + r >= t1) d = 0.f;
+                    dkeep[i][j] = d;
+                    u[j] = d * (&xv.x)[j];
+                    p[j] = (&yv.x)[j];
+                    if constexpr (GATE) p[j] *= fast_silu((&zv.x)[j]);
+                }
+                float4 *w = reinterpret_cast<float4 *>(&sdu[r][4 * sv]);
+                w[0] = make_float4(dkeep[i][0], u[0], dkeep[i][1], u[1]);
+                w[1] = make_float4(dkeep[i][2], u[2], dkeep[i][3], u[3]);
+                *reinterpret_cast<float4 *>(&sdy[r][4 * sv]) = make_float4(p[0], p[1], p[2], p[3]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NBC; ++k) {
+            const int e = tid + 256 * k;
+            if (e < 2 * BC) reinterpret_cast<float4 *>(&sbc[0][0][0])[e] = widen4(rbc[k]);
+        }
+        // the previous tile's loads, in flight during this one's arithmetic
+        const int64_t tp = tb - TB;
+        Tok ntok[NI];
+        Raw4<Tio> nbc[NBC];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) ntok[i] = load_tok(tp, i);
+#pragma unroll
+        for (int k = 0; k < NBC; ++k) nbc[k] = load_bc(tp, k);
+        lds_barrier();
+
+        // the tile's states
+        float H[TB][4];
+        float keep = 0.f;
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+            const float2 w = sdu[t][cl];
+            const float4 bv = *reinterpret_cast<const float4 *>(&sbc[0][t][4 * s]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float prev = t ? H[t ? t - 1 : 0][i] : (&h0.x)[i];
+                H[t][i] = fmaf(fast_exp2(w.x * a2[i]), prev, w.y * (&bv.x)[i]);
+            }
+            if constexpr (GATE) {
+                const float4 cv = *reinterpret_cast<const float4 *>(&sbc[1][t][4 * s]);
+                const float p = chan_sum<S>(H[t][0] * cv.x + H[t][1] * cv.y + H[t][2] * cv.z +
+                                            H[t][3] * cv.w);
+                if (s == t % S) keep = p;
+                if ((t + 1) % S == 0) sy[t - (S - 1) + s][cl] = keep;
+            }
+            // (keeps the scheduler from loading every token's operands at once)
+            if ((t & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+        // and backwards
+        float dAt[4] = {};
+        float2 kgd = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int t = TB - 1; t >= 0; --t) {
+            const float2 w = sdu[t][cl];
+            const float p = sdy[t][cl];
+            const float4 bv = *reinterpret_cast<const float4 *>(&sbc[0][t][4 * s]);
+            const float4 cv = *reinterpret_cast<const float4 *>(&sbc[1][t][4 * s]);
+            float v[8], gb = 0.f, qa = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float gi = fmaf(p, (&cv.x)[i], car[i]);
+                v[i] = gi * w.y;
+                v[4 + i] = p * H[t][i];
+                gb = fmaf(gi, (&bv.x)[i], gb);
+                car[i] = gi * fast_exp2(w.x * a2[i]);
+                const float q = car[i] * (t ? H[t ? t - 1 : 0][i] : (&h0.x)[i]);
+                qa = fmaf(q, a2[i], qa);
+                dAt[i] = fmaf(q, w.x, dAt[i]);
+            }
+            gb = chan_sum<S>(gb);
+            qa = chan_sum<S>(qa);
+            if (s == t % S) kgd = make_float2(gb, qa);
+            if (t % S == 0) sgd[t + s][cl] = kgd;
+            const float2 r = channels_sum<S>(v);
+            if ((lane & 15) < S)
+                *reinterpret_cast<float2 *>(
+                    &sdbc[wave][t][(lane >> 5) * N + 4 * s + 2 * ((lane >> 4) & 1)]) = r;
+            if ((t & 1) == 0) __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dA[i] += dAt[i];
+        h0 = load_h0(tp);
+        lds_barrier();
+
+        // per-channel outputs
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int e = tid + 256 * i, r = e / VPR;
+            const int64_t t = tb + r;
+            if (e < ITEMS && t < t1 && chn > 0) {
+                const float4 xv = widen4(tok[i].x), dv = widen4(tok[i].dt), yv = tok[i].dy.v;
+                const float4 zv = widen4(tok[i].z);
+                const float4 *w = reinterpret_cast<const float4 *>(&sgd[r][4 * sv]);
+                const float4 w0 = w[0], w1 = w[1];
+                const float gb[4] = {w0.x, w0.z, w1.x, w1.z}, qa[4] = {w0.y, w0.w, w1.y, w1.w};
+                float4 ys = make_float4(0.f, 0.f, 0.f, 0.f);
+                if constexpr (GATE) ys = *reinterpret_cast<const float4 *>(&sy[r][4 * sv]);
+                float ox[4], od[4], oz[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float xj = (&xv.x)[j], dyj = (&yv.x)[j];
+                    float p = dyj;
+                    if constexpr (GATE) {
+                        float f, df;
+                        silu_grad((&zv.x)[j], f, df);
+                        p *= f;
+                        oz[j] = dyj * ((&ys.x)[j] + Dv[j] * xj) * df;
+                    }
+                    ox[j] = fmaf(dkeep[i][j], gb[j], Dv[j] * p);
+                    float dd = fmaf(xj, gb[j], qa[j] * kLn2);
+                    const float rw = (&dv.x)[j] + bias[j];
+                    if (g.softplus && rw <= 20.f) dd *= sigmoid_f(rw);
+                    od[j] = dd;
+                    accD[j] = fmaf(p, xj, accD[j]);
+                    accb[j] += dd;
+                }
+                const int64_t o = (b * g.T + t) * g.Dm + ch0;
+                store4<RAG>(dx + o, make_float4(ox[0], ox[1], ox[2], ox[3]), chn);
+                store4<RAG>(ddt + o, make_float4(od[0], od[1], od[2], od[3]), chn);
+                if constexpr (GATE)
+                    store4<RAG>(dz + o, make_float4(oz[0], oz[1], oz[2], oz[3]), chn);
+            }
+        }
+        // dB and dC of this channel block
+        for (int e = tid; e < TB * N / 2; e += 256) {
+            const int r = e / (N / 2), o = 4 * (e % (N / 2));
+            if (tb + r < t1) {
+                float4 v[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    v[w] = *reinterpret_cast<const float4 *>(&sdbc[w][r][o]);
+                float4 q;
+                q.x = (v[0].x + v[1].x) + (v[2].x + v[3].x);
+                q.y = (v[0].y + v[1].y) + (v[2].y + v[3].y);
+                q.z = (v[0].z + v[1].z) + (v[2].z + v[3].z);
+                q.w = (v[0].w + v[1].w) + (v[2].w + v[3].w);
+                *reinterpret_cast<float4 *>(pbc + ((cb * g.Bt + b) * g.T + tb + r) * (2 * N) + o) =
+                    q;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) tok[i] = ntok[i];
+#pragma unroll
+        for (int k = 0; k < NBC; ++k) rbc[k] = nbc[k];
+    }
+
+    if (c < g.Dm) {
+        *reinterpret_cast<float4 *>(pA + ((int64_t)rest * g.Dm + c) * N + 4 * s) =
+            make_float4(dA[0], dA[1], dA[2], dA[3]);
+        if (dinit && seg == 0)
+            *reinterpret_cast<float4 *>(dinit + (b * g.Dm + c) * N + 4 * s) =
+                make_float4(car[0], car[1], car[2], car[3]);
+    }
+    // sums over this block's token rows
+    __syncthreads();
+    float(*red)[CB] = reinterpret_cast<float(*)[CB]>(&sdu[0][0]);   // [2 ROWS][CB]
+    if (tid < ROWS * VPR) {
+        const int r = tid / VPR;
+        *reinterpret_cast<float4 *>(&red[r][4 * sv]) =
+            make_float4(accD[0], accD[1], accD[2], accD[3]);
+        *reinterpret_cast<float4 *>(&red[ROWS + r][4 * sv]) =
+            make_float4(accb[0], accb[1], accb[2], accb[3]);
+    }
+    __syncthreads();
+    for (int e = tid; e < 2 * CB; e += 256) {
+        const int q = e / CB, o = e % CB;
+        const int32_t co = cb * CB + o;
+        if (co < g.Dm) {
+            float v = 0.f;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) v += red[q * ROWS + r][o];
+            (q ? pbias : pD)[(int64_t)rest * g.Dm + co] = v;
+        }
+    }
+}
+
+// out = sum over the partials, in order and in double.  A workgroup owns 64
+// outputs; its 4 wavefronts take every fourth partial.
+struct SumJob {
+    const float *part;
+    int64_t count, np;       // outputs, partials ([np][count])
+    float *out0, *out1;      // out1: the second half of every row of 2 half elements
+    int32_t half;            // 0: one output array
+    uint32_t blocks;
+};
+struct SumJobs {
+    SumJob j[4];
+};
+__global__ __launch_bounds__(256) void sel_sum_kernel(SumJobs jobs) {
+    __shared__ double red[4][64];
+    uint32_t blk = blockIdx.x;
+    int k = 0;
+    while (k < 3 && blk >= jobs.j[k].blocks) blk -= jobs.j[k++].blocks;
+    const SumJob &j = jobs.j[k];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t i = (int64_t)blk * 64 + lane;
+    double v = 0.0;
+    if (i < j.count) {
+#pragma unroll 8
+        for (int64_t p = wave; p < j.np; p += 4) v += (double)j.part[p * j.count + i];
+    }
+    red[wave][lane] = v;
+    __syncthreads();
+    if (wave == 0 && i < j.count) {
+        const float r = (float)((red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]));
+        if (j.half) {
+            const int64_t row = i / (2 * j.half);
+            const int32_t o = (int32_t)(i - row * 2 * j.half);
+            if (o < j.half)
+                j.out0[row * j.half + o] = r;
+            else
+                j.out1[row * j.half + o - j.half] = r;
+        } else if (j.out0) {
+            j.out0[i] = r;
+        }
+    }
+}
+
+struct BwdPlan {
+    int64_t nseg, seg_len;
+    // float offsets into the workspace
+    size_t ckpt, cumd, hseg, adj, dsum, pbc, pA, pD, pbias, total;
+};
+BwdPlan plan(const SelArgs &a) {
+    BwdPlan p;
+    const int64_t tile = a.N > TB ? a.N : TB;
+    const int64_t ncb = chan_blocks(a), blocks = a.Bt * ncb;
+    p.nseg = 1;
+    p.seg_len = cdiv64(a.T > 0 ? a.T : 1, tile) * tile;
+    if (blocks > 0 && blocks < 512) {
+        int64_t n = cdiv64(1024, blocks);
+        n = n < a.T / 64 ? n : a.T / 64;
+        if (n >= 2) {
+            p.seg_len = cdiv64(cdiv64(a.T, n), tile) * tile;
+            p.nseg = cdiv64(a.T, p.seg_len);
+        }
+    }
+    const size_t st = (size_t)a.Bt * a.Dm * a.N, ch = (size_t)a.Bt * a.Dm;
+    const size_t nt = (size_t)cdiv64(a.T, TB), ns = p.nseg;
+    size_t o = 0;
+    auto take = [&](size_t n) {
+        const size_t at = o;
+        o += (n + 63) & ~size_t(63);
+        return at;
+    };
+    p.ckpt = take(st * nt);
+    p.cumd = take(ns > 1 ? ch * nt : 0);
+    p.hseg = take(ns > 1 ? st * ns : 0);
+    p.adj = take(ns > 1 ? st * ns : 0);
+    p.dsum = take(ns > 1 ? ch * ns : 0);
+    p.pbc = take((size_t)ncb * a.Bt * a.T * 2 * a.N);
+    p.pA = take(st * ns);
+    p.pD = take(ch * ns);
+    p.pbias = take(ch * ns);
+    p.total = o;
+    return p;
+}
+
+}  // namespace
+
+size_t selective_scan_bwd_workspace(const SelArgs &a) {
+    return a.Bt > 0 ? plan(a).total * sizeof(float) : 0;
+}
+
+hipError_t launch_selective_scan_bwd(const SelArgs &a, hipStream_t st) {
+    const BwdPlan p = plan(a);
+    float *ws = static_cast<float *>(a.ws);
+    SelGeom g;
+    g.T = a.T;
+    g.Bt = a.Bt;
+    g.Dm = (int32_t)a.Dm;
+    g.ncb = (int32_t)chan_blocks(a);
+    g.nseg = (int32_t)p.nseg;
+    g.seg_len = p.seg_len;
+    g.softplus = a.softplus ? 1 : 0;
+    const bool rag = a.Dm % 4 != 0, split = p.nseg > 1;
+    const int64_t rows = a.Bt * p.nseg;
+    hipError_t e;
+    if (a.Bt > 0) {
+        by_state(a, [&](auto n, auto io) {
+            typedef decltype(io) Tio;
+            by_flag(rag, [&](auto r) {
+                sel_scan_kernel<decltype(n)::value, Tio, float, false, decltype(r)::value,
+                                SCAN_CKPT><<<dim3((uint32_t)(rows * g.ncb)), 256, 0, st>>>(
+                    (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B, nullptr, nullptr,
+                    nullptr, a.dt_bias, split ? nullptr : a.init, nullptr, nullptr, ws + p.hseg,
+                    ws + p.dsum, ws + p.ckpt, ws + p.cumd, g);
+            });
+        });
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (split) {
+            by_state(a, [&](auto n, auto io) {
+                typedef decltype(io) Tio;
+                by_flag(rag, [&](auto r) {
+                    by_flag(a.z != nullptr, [&](auto gate) {
+                        sel_adj_kernel<decltype(n)::value, Tio, decltype(gate)::value,
+                                       decltype(r)::value>
+                            <<<dim3((uint32_t)(a.Bt * (p.nseg - 1) * g.ncb)), 256, 0, st>>>(
+                                (const Tio *)a.dt, a.A, (const Tio *)a.C, (const Tio *)a.z,
+                                a.dt_bias, a.dy, ws + p.adj, g);
+                    });
+                });
+            });
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+            const int64_t total = a.Bt * a.Dm * a.N;
+            sel_chain_bwd_kernel<<<dim3((uint32_t)cdiv64(total, 256)), 256, 0, st>>>(
+                ws + p.hseg, ws + p.adj, ws + p.dsum, a.A, a.init, a.dfinal, total,
+                (int32_t)a.Dm, (int32_t)a.N, (int32_t)p.nseg);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+        by_state(a, [&](auto n, auto io) {
+            typedef decltype(io) Tio;
+            by_flag(rag, [&](auto r) {
+                by_flag(a.z != nullptr, [&](auto gate) {
+                    sel_bwd_kernel<decltype(n)::value, Tio, decltype(gate)::value,
+                                   decltype(r)::value>
+                        <<<dim3((uint32_t)(rows * g.ncb)), 256, 0, st>>>(
+                            (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B,
+                            (const Tio *)a.C, a.D, (const Tio *)a.z, a.dt_bias, a.dy,
+                            split ? ws + p.adj : a.dfinal, ws + p.ckpt, ws + p.cumd, ws + p.hseg,
+                            a.dx, a.ddt, a.dz, a.dinit, ws + p.pbc, ws + p.pA, ws + p.pD,
+                            ws + p.pbias, g);
+                });
+            });
+        });
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    SumJobs jobs;
+    auto job = [&](const float *part, int64_t count, int64_t np, float *o0, float *o1, int half) {
+        return SumJob{part, count, np, o0, o1, half, (uint32_t)cdiv64(count, 64)};
+    };
+    jobs.j[0] = job(ws + p.pbc, a.Bt * a.T * 2 * a.N, g.ncb, a.dB, a.dC, a.N);
+    jobs.j[1] = job(ws + p.pA, a.Dm * a.N, rows, a.dA, nullptr, 0);
+    jobs.j[2] = job(ws + p.pD, a.Dm, rows, a.dD, nullptr, 0);
+    jobs.j[3] = job(ws + p.pbias, a.Dm, rows, a.dbias, nullptr, 0);
+    uint32_t blocks = 0;
+    for (const SumJob &j : jobs.j) blocks += j.blocks;
+    sel_sum_kernel<<<dim3(blocks), 256, 0, st>>>(jobs);
+    return hipGetLastError();
+}
+
+}  // namespace ssd

@@ -23,6 +23,9 @@ The functions carry the C names:
 * :func:`ssd_chunked_bwd` -- every gradient of the chunked forward;
 * :func:`ssd_conv1d_fwd`, :func:`ssd_conv1d_step`, :func:`ssd_conv1d_bwd` -- the
   short causal convolution in front of the scan;
+* :func:`ssd_selective_scan_fwd`, :func:`ssd_selective_scan_step`,
+  :func:`ssd_selective_scan_bwd` -- the scan with a decay rate per channel and
+  state;
 * :func:`ssd_cache_write`, :func:`ssd_cache_read` -- recurrent states in a slot
   pool at 8 bits per element;
 * :func:`ssd_chunked_fwd_workspace_size`, :func:`ssd_chunked_fwd_workspace_layout`,
@@ -89,6 +92,12 @@ class ConvDims(ctypes.Structure):
                 ("silu", ctypes.c_int32)]
 
 
+class ScanDims(ctypes.Structure):
+    """ssd_scan_dims."""
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("io_dtype", ctypes.c_int32)]
+
+
 CACHE_BLOCK = 64   # SSD_CACHE_BLOCK
 CACHE_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}   # ssd_cache_format by the codes' dtype
 
@@ -105,7 +114,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                            "selective_state_space_amd.build` -- there is no fallback" % path)
     lib = ctypes.CDLL(path)
     vp, i64, sz, dp = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(Dims)
-    cdp = ctypes.POINTER(ConvDims)
+    cdp, sdp = ctypes.POINTER(ConvDims), ctypes.POINTER(ScanDims)
+    lop = ctypes.POINTER(LayerOpts)
     st = ctypes.c_int
     sig = {
         "ssd_chunked_fwd": ([vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, dp, vp, sz, vp], st),
@@ -136,6 +146,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "ssd_conv1d_step": ([vp, i64, vp, vp, vp, vp, vp, cdp, vp], st),
         "ssd_conv1d_bwd_workspace_size": ([cdp], sz),
         "ssd_conv1d_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, cdp, vp, sz, vp], st),
+        "ssd_selective_scan_workspace_size": ([sdp], sz),
+        "ssd_selective_scan_fwd": ([vp] * 10 + [lop, sdp, vp, sz, vp], st),
+        "ssd_selective_scan_step": ([vp, i64] + [vp] * 8 + [lop, sdp, vp], st),
+        "ssd_selective_scan_bwd_workspace_size": ([sdp], sz),
+        "ssd_selective_scan_bwd": ([vp] * 18 + [lop, sdp, vp, sz, vp], st),
         "ssd_cache_write": ([vp, i64, i64, vp, i64, vp, vp, ctypes.c_int32, vp], st),
         "ssd_cache_read": ([vp, vp, i64, i64, vp, i64, vp, ctypes.c_int32, vp], st),
         "ssd_status_string": ([st], ctypes.c_char_p),
@@ -610,8 +625,15 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _in(t, name, dtype, shape, device):
+    """An input the library can read: contiguous, and a copy where a view starts off a
+    16-byte boundary."""
+    t = _need(t, name, dtype, shape, device)
+    return t.clone() if t.data_ptr() & 15 else t
+
+
 def _opt(t, name, dtype, shape, device):
-    return None if t is None else _need(t, name, dtype, shape, device)
+    return None if t is None else _in(t, name, dtype, shape, device)
 
 
 def _parts3(ts):
@@ -628,7 +650,7 @@ def _conv_args(x, weight, bias, splits, silu, tokens: int):
     C = x.shape[-1]
     if weight.dim() != 2:
         raise ValueError("weight must be [C,W]")
-    weight = _need(weight, "weight", torch.float32, (C, weight.shape[1]), dev)
+    weight = _in(weight, "weight", torch.float32, (C, weight.shape[1]), dev)
     bias = _opt(bias, "bias", torch.float32, (C,), dev)
     splits = (C,) if splits is None else tuple(int(c) for c in splits)
     if not 1 <= len(splits) <= 3 or sum(splits) != C or min(splits) < 0:
@@ -718,7 +740,7 @@ def ssd_conv1d_bwd(x, weight, dy, bias=None, silu: bool = True, init_state=None,
                                                     silu, 1)
     Bt, T, C = x.shape
     W = weight.shape[1]
-    dy = tuple([_need(d, "dy[%d]" % i, torch.float32, (Bt, T, c), dev)
+    dy = tuple([_in(d, "dy[%d]" % i, torch.float32, (Bt, T, c), dev)
                 for i, (d, c) in enumerate(zip(dy, splits))])
     init_state = _opt(init_state, "init_state", x.dtype, (Bt, W - 1, C), dev)
     dfinal = _opt(dfinal, "dfinal", torch.float32, (Bt, W - 1, C), dev)
@@ -733,6 +755,143 @@ def ssd_conv1d_bwd(x, weight, dy, bias=None, silu: bool = True, init_state=None,
           _parts3(dy + (None,) * (3 - len(dy))), _addr(dfinal), _addr(out["dx"]),
           _addr(out["dweight"]), _addr(out["dbias"]), _addr(out["dinit"]), ctypes.byref(dims),
           _addr(workspace), workspace.numel() * workspace.element_size())
+    return out
+
+
+def _scan_layer(x, dt_bias, dt_softplus, z, zname, y_io_dtype, Dm, dev):
+    """(options or None, tensors to keep) of a selective-scan call."""
+    dt_bias = _opt(dt_bias, "dt_bias", torch.float32, (Dm,), dev)
+    z = _opt(z, zname, x.dtype, tuple(x.shape), dev)
+    if dt_bias is None and z is None and not dt_softplus and not y_io_dtype:
+        return None, None, None
+    return (LayerOpts(_addr(dt_bias), 1 if dt_softplus else 0, 1 if y_io_dtype else 0, _addr(z)),
+            dt_bias, z)
+
+
+def _scan_tokens(x, dt, A, B, C, D, names):
+    dev = _on_gpu(x, names[0])
+    lead, Dm = tuple(x.shape[:-1]), x.shape[-1]
+    if A.dim() != 2:
+        raise ValueError("A must be [Dm,N]")
+    N = A.shape[1]
+    return (dev, _in(x, names[0], x.dtype, lead + (Dm,), dev), _in(dt, names[1], x.dtype, lead + (Dm,), dev),
+            _in(A, "A", torch.float32, (Dm, N), dev),
+            _in(B, names[2], x.dtype, lead + (N,), dev),
+            _in(C, names[3], x.dtype, lead + (N,), dev),
+            _in(D, "D", torch.float32, (Dm,), dev))
+
+
+def ssd_selective_scan_workspace_size(dims: ScanDims) -> int:
+    return int(load_library().ssd_selective_scan_workspace_size(ctypes.byref(dims)))
+
+
+def ssd_selective_scan_fwd(x, dt, A, B, C, D, init_state=None, y=None, final_state=None,
+                           want_final: bool = True, seq_lens=None, dt_bias=None,
+                           dt_softplus: bool = False, z=None, y_io_dtype: bool = False,
+                           workspace=None):
+    """Selective scan of a prompt.  Returns (y, final_state or None).
+
+    x, dt [Bt,T,Dm] (float32 or bfloat16), A [Dm,N] f32 with N 8, 16, 32 or 64,
+    B, C [Bt,T,N] (x's dtype), D [Dm] f32, init_state [Bt,Dm,N] f32 or None;
+    ``final_state`` may be the same tensor.  y is [Bt,T,Dm] float32, x's dtype
+    with ``y_io_dtype``.  ``dt_bias`` [Dm] f32, ``dt_softplus`` and the gate
+    ``z`` (x's shape and dtype) are the layer options.  ``seq_lens`` [Bt]
+    int32: y past a sequence's length is zero and its final state is that at
+    its length.
+    """
+    if x.dim() != 3:
+        raise ValueError("x must be [Bt,T,Dm]")
+    dev, x, dt, A, B, C, D = _scan_tokens(x, dt, A, B, C, D, ("x", "dt", "B", "C"))
+    Bt, T, Dm = x.shape
+    N = A.shape[1]
+    dims = ScanDims(Bt, T, Dm, N, _io_code(x.dtype))
+    opts, dt_bias, z = _scan_layer(x, dt_bias, dt_softplus, z, "z", y_io_dtype, Dm, dev)
+    init_state = _opt(init_state, "init_state", torch.float32, (Bt, Dm, N), dev)
+    seq_lens = _opt(seq_lens, "seq_lens", torch.int32, (Bt,), dev)
+    ydt = x.dtype if y_io_dtype else torch.float32
+    y = (torch.empty((Bt, T, Dm), dtype=ydt, device=dev) if y is None
+         else _need_out(y, "y", ydt, (Bt, T, Dm), dev))
+    if final_state is not None:
+        final_state = _need_out(final_state, "final_state", torch.float32, (Bt, Dm, N), dev)
+    elif want_final:
+        final_state = torch.empty((Bt, Dm, N), dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = ssd_selective_scan_workspace_size(dims)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _call("ssd_selective_scan_fwd", dev, _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
+          _addr(D), _addr(init_state), _addr(seq_lens), _addr(y), _addr(final_state),
+          None if opts is None else ctypes.byref(opts), ctypes.byref(dims), _addr(workspace),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
+    return y, final_state
+
+
+def ssd_selective_scan_step(state, x_t, dt_t, A, B_t, C_t, D, slots=None, y_t=None, dt_bias=None,
+                            dt_softplus: bool = False, z_t=None, y_io_dtype: bool = False):
+    """One token of the selective scan per sequence; returns y_t [Bt,Dm].
+
+    state [num_slots,Dm,N] f32 is updated in place; slots [Bt] int32 (None =
+    sequence b has state b): a slot outside the pool marks a padded row (y
+    zero, no state touched); a slot may be named once.  x_t, dt_t [Bt,Dm],
+    B_t, C_t [Bt,N]; the other arguments as for ssd_selective_scan_fwd.
+    """
+    if x_t.dim() != 2:
+        raise ValueError("x_t must be [Bt,Dm]")
+    dev, x_t, dt_t, A, B_t, C_t, D = _scan_tokens(x_t, dt_t, A, B_t, C_t, D,
+                                                  ("x_t", "dt_t", "B_t", "C_t"))
+    Bt, Dm = x_t.shape
+    N = A.shape[1]
+    if state.dim() != 3:
+        raise ValueError("state must be [num_slots,Dm,N]")
+    state = _need_out(state, "state", torch.float32, (state.shape[0], Dm, N), dev)
+    slots = _opt(slots, "slots", torch.int32, (Bt,), dev)
+    opts, dt_bias, z_t = _scan_layer(x_t, dt_bias, dt_softplus, z_t, "z_t", y_io_dtype, Dm, dev)
+    ydt = x_t.dtype if y_io_dtype else torch.float32
+    y_t = (torch.empty((Bt, Dm), dtype=ydt, device=dev) if y_t is None
+           else _need_out(y_t, "y_t", ydt, (Bt, Dm), dev))
+    dims = ScanDims(Bt, 1, Dm, N, _io_code(x_t.dtype))
+    _call("ssd_selective_scan_step", dev, _addr(state), state.shape[0], _addr(slots), _addr(x_t),
+          _addr(dt_t), _addr(A), _addr(B_t), _addr(C_t), _addr(D), _addr(y_t),
+          None if opts is None else ctypes.byref(opts), ctypes.byref(dims))
+    return y_t
+
+
+def ssd_selective_scan_bwd_workspace_size(dims: ScanDims) -> int:
+    return int(load_library().ssd_selective_scan_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def ssd_selective_scan_bwd(x, dt, A, B, C, D, dy, init_state=None, dfinal=None, dt_bias=None,
+                           dt_softplus: bool = False, z=None, want_dinit: bool = True,
+                           workspace=None):
+    """Gradients of ssd_selective_scan_fwd (without seq_lens), float32: a dict of dx, ddt
+    [Bt,T,Dm], dA [Dm,N], dB, dC [Bt,T,N], dD [Dm], ddt_bias [Dm] (None without dt_bias),
+    dz [Bt,T,Dm] (None without z) and dinit [Bt,Dm,N] (None unless ``want_dinit``).
+    dy [Bt,T,Dm] f32; dfinal [Bt,Dm,N] f32 or None."""
+    if x.dim() != 3:
+        raise ValueError("x must be [Bt,T,Dm]")
+    dev, x, dt, A, B, C, D = _scan_tokens(x, dt, A, B, C, D, ("x", "dt", "B", "C"))
+    Bt, T, Dm = x.shape
+    N = A.shape[1]
+    dims = ScanDims(Bt, T, Dm, N, _io_code(x.dtype))
+    opts, dt_bias, z = _scan_layer(x, dt_bias, dt_softplus, z, "z", False, Dm, dev)
+    dy = _in(dy, "dy", torch.float32, (Bt, T, Dm), dev)
+    init_state = _opt(init_state, "init_state", torch.float32, (Bt, Dm, N), dev)
+    dfinal = _opt(dfinal, "dfinal", torch.float32, (Bt, Dm, N), dev)
+    if workspace is None:
+        workspace = torch.empty(max(ssd_selective_scan_bwd_workspace_size(dims), 16),
+                                dtype=torch.uint8, device=dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    out = dict(dx=torch.empty((Bt, T, Dm), **f32), ddt=torch.empty((Bt, T, Dm), **f32),
+               dA=torch.empty((Dm, N), **f32), dB=torch.empty((Bt, T, N), **f32),
+               dC=torch.empty((Bt, T, N), **f32), dD=torch.empty((Dm,), **f32),
+               ddt_bias=None if dt_bias is None else torch.empty((Dm,), **f32),
+               dz=None if z is None else torch.empty((Bt, T, Dm), **f32),
+               dinit=torch.empty((Bt, Dm, N), **f32) if want_dinit else None)
+    _call("ssd_selective_scan_bwd", dev, _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
+          _addr(D), _addr(init_state), _addr(dy), _addr(dfinal), _addr(out["dx"]),
+          _addr(out["ddt"]), _addr(out["dA"]), _addr(out["dB"]), _addr(out["dC"]),
+          _addr(out["dD"]), _addr(out["ddt_bias"]), _addr(out["dz"]), _addr(out["dinit"]),
+          None if opts is None else ctypes.byref(opts), ctypes.byref(dims), _addr(workspace),
+          workspace.numel() * workspace.element_size())
     return out
 
 
@@ -755,7 +914,7 @@ def ssd_cache_write(state, codes, scales, slots=None):
     pool skips that state; a slot may be named once."""
     codes, scales, dev = _cache_pool(codes, scales)
     n, size = state.shape[0], codes.shape[1]
-    state = _need(state, "state", torch.float32, tuple(state.shape), dev)
+    state = _in(state, "state", torch.float32, tuple(state.shape), dev)
     if state.numel() != n * size:
         raise ValueError("a state holds %d elements, the pool's rows %d"
                          % (state.numel() // max(n, 1), size))

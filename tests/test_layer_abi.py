@@ -107,6 +107,87 @@ def test_conv_workspace():
     assert ssd.ssd_conv1d_bwd_workspace_size(conv_dims(W=9)) == 0
 
 
+def scan_dims(Bt=2, T=30, Dm=64, N=16, io=ssd.SSD_BF16):
+    return ssd.ScanDims(Bt, T, Dm, N, io)
+
+
+def opts(bias=P16, softplus=1, yio=0, z=P16):
+    return ssd.LayerOpts(bias, softplus, yio, z)
+
+
+def scan_fwd(d, x=P16, dt=P16, A=P16, B=P16, C=P16, D=P16, init=P16, lens=P16, y=P16, fin=P16,
+             o=None, ws=P16, wsb=BIG):
+    return lib().ssd_selective_scan_fwd(x, dt, A, B, C, D, init, lens, y, fin, o,
+                                        None if d is None else ctypes.byref(d), ws, wsb, None)
+
+
+def scan_step(d, state=P16, num=8, slots=P16, x=P16, dt=P16, A=P16, B=P16, C=P16, D=P16, y=P16,
+              o=None):
+    return lib().ssd_selective_scan_step(state, num, slots, x, dt, A, B, C, D, y, o,
+                                         None if d is None else ctypes.byref(d), None)
+
+
+def scan_bwd(d, x=P16, dt=P16, A=P16, B=P16, C=P16, D=P16, init=P16, dy=P16, dfinal=P16, dx=P16,
+             ddt=P16, dA=P16, dB=P16, dC=P16, dD=P16, dbias=P16, dz=P16, dinit=P16, o=None,
+             ws=P16, wsb=BIG):
+    return lib().ssd_selective_scan_bwd(x, dt, A, B, C, D, init, dy, dfinal, dx, ddt, dA, dB, dC,
+                                        dD, dbias, dz, dinit, o,
+                                        None if d is None else ctypes.byref(d), ws, wsb, None)
+
+
+@pytest.mark.parametrize("call", [scan_fwd, scan_step, scan_bwd])
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(Bt=-1), -2, "batch"), (dict(Dm=0), -2, "dim"), (dict(Dm=(1 << 24) + 1), -2, "dim"),
+    (dict(N=12), -3, "dstate"), (dict(N=128), -3, "dstate"), (dict(io=5), -3, "io_dtype"),
+    (dict(Bt=1 << 28, Dm=1 << 20), -2, "too large"),
+])
+def test_scan_dims(call, kw, code, word):
+    assert call(scan_dims(**kw)) == code
+    assert word in detail()
+
+
+def test_scan_seqlen():
+    for call in (scan_fwd, scan_bwd):
+        assert call(scan_dims(T=-1)) == -2 and "seqlen" in detail()
+    for call in (scan_fwd, scan_bwd, scan_step):
+        assert call(None) == -1 and "dims" in detail()
+
+
+@pytest.mark.parametrize("call,required,optional", [
+    (scan_fwd, ["x", "dt", "A", "B", "C", "D", "y"], ["init", "lens", "fin", "ws"]),
+    (scan_step, ["state", "x", "dt", "A", "B", "C", "D", "y"], ["slots"]),
+    (scan_bwd, ["x", "dt", "A", "B", "C", "D", "dy", "dx", "ddt", "dA", "dB", "dC", "dD", "ws"],
+     ["init", "dfinal", "dbias", "dinit"]),
+])
+def test_scan_pointers(call, required, optional):
+    for f in required:
+        assert call(scan_dims(), **{f: None}) == -1, f
+    for f in required + optional:
+        assert call(scan_dims(), **{f: P_MIS}) == -4, f
+    for kw, code, word in [(dict(bias=P_MIS), -4, "dt_bias"), (dict(z=P_MIS), -4, "z"),
+                           (dict(yio=2), -3, "y_io_dtype")]:
+        assert call(scan_dims(), o=ctypes.byref(opts(**kw))) == code
+        assert word in detail()
+    if call is scan_bwd:   # a gate needs its gradient
+        assert call(scan_dims(), o=ctypes.byref(opts()), dz=None) == -1 and "dz" in detail()
+
+
+def test_scan_step_slots():
+    assert scan_step(scan_dims(), num=1, slots=None) == -2 and "num_slots" in detail()
+
+
+def test_scan_workspaces():
+    few = scan_dims(Bt=1, T=4096, Dm=64)
+    need = ssd.ssd_selective_scan_workspace_size(few)
+    assert need > 0 and scan_fwd(few, wsb=need - 1) == -5 and str(need) in detail()
+    assert scan_fwd(few, ws=None) == -1 and "workspace" in detail()
+    assert ssd.ssd_selective_scan_workspace_size(scan_dims(Bt=64, T=4096, Dm=5120)) == 0
+    assert ssd.ssd_selective_scan_workspace_size(scan_dims(N=5)) == 0
+    need = ssd.ssd_selective_scan_bwd_workspace_size(few)
+    assert need > 0 and scan_bwd(few, wsb=need - 1) == -5
+    assert ssd.ssd_selective_scan_bwd_workspace_size(scan_dims(Bt=0)) == 0
+
+
 def cache_write(state=P16, n=2, size=64, slots=P16, num=4, codes=P16, scales=P16, fmt=0):
     return lib().ssd_cache_write(state, n, size, slots, num, codes, scales, fmt, None)
 
@@ -137,6 +218,7 @@ def test_binding_refuses_host_tensors():
     for f in (lambda: ssd.ssd_conv1d_fwd(x, w),
               lambda: ssd.ssd_conv1d_step(torch.zeros(1, 3, 8), x[:, 0], w),
               lambda: ssd.ssd_conv1d_bwd(x, w, x),
+              lambda: ssd.ssd_selective_scan_fwd(x, x, w, w[None, :2], w[None, :2], w[:, 0]),
               lambda: ssd.ssd_cache_read(torch.zeros(1, 64, dtype=torch.int8),
                                          torch.zeros(1, 1))):
         with pytest.raises(ValueError):
