@@ -96,8 +96,8 @@ ssd_status check_scan(const ssd_scan_dims *d, bool need_seq, const ssd_layer_opt
         return fail(SSD_ERR_SHAPE, "batch = %lld out of range [0, 2^30]", (long long)d->batch);
     if (need_seq && (d->seqlen < 0 || d->seqlen > kMaxDim))
         return fail(SSD_ERR_SHAPE, "seqlen = %lld out of range [0, 2^30]", (long long)d->seqlen);
-    if (d->dim < 1 || d->dim > (int64_t(1) << 24))
-        return fail(SSD_ERR_SHAPE, "dim = %lld out of range [1, 2^24]", (long long)d->dim);
+    if (d->dim < 1 || d->dim > (int64_t(1) << 22))
+        return fail(SSD_ERR_SHAPE, "dim = %lld out of range [1, 2^22]", (long long)d->dim);
     if (d->dstate != 8 && d->dstate != 16 && d->dstate != 32 && d->dstate != 64)
         return fail(SSD_ERR_UNSUPPORTED, "dstate = %lld; only 8, 16, 32 and 64 are instantiated",
                     (long long)d->dstate);

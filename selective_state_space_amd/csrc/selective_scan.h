@@ -1,12 +1,12 @@
 // Shared by the forward, step and backward kernels of the per-channel
 // selective scan (gfx950 only).
 //
-// Work split: a channel's N states lie on S = N/4 neighbouring lanes, 4 per
-// lane, so a wavefront holds 64/S channels and a workgroup of 4 wavefronts CB
-// = 256/S.  Token tiles pass through LDS: 16-byte row segments are loaded,
+// Work split: a channel's N states lie on S = N/KS neighbouring lanes, KS (4 or
+// 2) per lane, so a wavefront holds 64/S channels and a workgroup of 4
+// wavefronts CB = 256/S.  Token tiles pass through LDS: 16-byte row segments are loaded,
 // d = softplus(dt + bias) and u = d x formed once per (token, channel), and
-// the scanning lanes then read (d, u) of their channel and their 4 elements
-// of B and C.
+// the scanning lanes then read (d, u) of their channel and their
+// KS elements of B and C.
 #pragma once
 
 #include <type_traits>
@@ -16,11 +16,15 @@
 
 namespace ssd {
 
-template <int N>
+template <int N, int KS = 4>
 struct SelSplit {
-    static constexpr int S = N / 4;        // lanes of a channel
+    static constexpr int S = N / KS;       // lanes of a channel
     static constexpr int CPW = 64 / S;     // channels of a wavefront
     static constexpr int CB = 4 * CPW;     // channels of a workgroup
+    static constexpr int TL = 1024 / CB;   // tokens of a tile: 4 elements per thread
+    static constexpr int VPR = CB / 4;     // 4-channel vectors of a tile's row
+    static constexpr int BC = TL * N / 4;  // 4-element vectors of a tile's B (or C)
+    static constexpr int NBC = (BC + 255) / 256;   // of them per thread
 };
 
 constexpr float kLn2 = 0.69314718055994531f;
@@ -97,19 +101,20 @@ __device__ __forceinline__ void store4(uint16_t *p, float4 v, int n) {
     }
 }
 
-// log(1 + e^r), r above 20 unchanged.  e^r as a power of two with the
-// argument's rounding put back; log(1 + e) with the rounding of 1 + e put
-// back, so small results keep their relative accuracy.
+// log(1 + e^r) = max(r, 0) + log(1 + e^-|r|); above 20 that is r in float32.
+// e^-|r| as a power of two with the argument's rounding put back; log(1 + e)
+// with the rounding of 1 + e put back (1 - e/2 stands for 1 / (1 + e): the
+// term matters where e is small), so small results keep their relative
+// accuracy.
 __device__ __forceinline__ float softplus_f(float r) {
-    if (r > 20.f) return r;
-    r = r < -150.f ? -150.f : r;   // (e^r is 0 in float32; -inf stays out of the products)
     constexpr float kLog2eLo = 1.9259629911266175e-8f;   // log2(e) - (float)log2(e)
-    const float hi = r * kLog2e;
-    const float lo = fmaf(r, kLog2eLo, fmaf(r, kLog2e, -hi));
+    const float q = -fabsf(r), hi = q * kLog2e;
+    const float lo = fmaf(q, kLog2eLo, fmaf(q, kLog2e, -hi));
     float e = fast_exp2(hi);
-    e = fmaf(e, lo * kLn2, e);
+    e = fmaf(e, e > 0.f ? lo * kLn2 : 0.f, e);
     const float w = 1.f + e;
-    return fmaf(__builtin_amdgcn_logf(w), kLn2, (e - (w - 1.f)) * __builtin_amdgcn_rcpf(w));
+    const float l = __builtin_amdgcn_logf(w) * kLn2;
+    return fmaxf(r, 0.f) + fmaf(e - (w - 1.f), fmaf(e, -0.5f, 1.f), l);
 }
 __device__ __forceinline__ float sigmoid_f(float v) {
     return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * v));
@@ -125,13 +130,95 @@ __device__ __forceinline__ float chan_sum(float v) {
     return v;
 }
 
-// Tokens of a tile: N * CB = 1024 elements, 4 per thread.
-template <int N>
-struct Tile {
-    static constexpr int TL = N;
-    static constexpr int VPR = SelSplit<N>::CB / 4;              // 4-channel vectors of a row
-    static constexpr int NBC = (2 * TL * N / 4 + 255) / 256;     // B, C vectors per thread
-};
+// Sums over the S lanes of a channel of S values per lane (one per token):
+// lane s receives the sum of p[s].  Each step pairs lanes by a mirror or a
+// swap, keeps half of the values and hands the partner the other half: S - 1
+// additions for S sums, where S separate butterflies take S log2 S.
+template <int S>
+__device__ __forceinline__ float lane_sums(float (&p)[S], int s) {
+    if constexpr (S == 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float keep = s & 8 ? p[i + 8] : p[i], send = s & 8 ? p[i] : p[i + 8];
+            p[i] = keep + dpp_mov<0x140>(send);   // row_mirror: lane 15 - s
+        }
+    }
+    if constexpr (S >= 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float keep = s & 4 ? p[i + 4] : p[i], send = s & 4 ? p[i] : p[i + 4];
+            p[i] = keep + dpp_mov<0x141>(send);   // row_half_mirror: lane 7 - s
+        }
+    }
+    if constexpr (S >= 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float keep = s & 2 ? p[i + 2] : p[i], send = s & 2 ? p[i] : p[i + 2];
+            p[i] = keep + dpp_mov<0x4E>(send);    // lane s ^ 2
+        }
+    }
+    const float keep = s & 1 ? p[1] : p[0], send = s & 1 ? p[0] : p[1];
+    return keep + dpp_mov<0xB1>(send);            // lane s ^ 1
+}
+
+// KS consecutive floats of LDS or global memory (aligned)
+template <int KS>
+__device__ __forceinline__ void load_ks(const float *p, float (&v)[KS]) {
+    if constexpr (KS == 4) {
+        const float4 w = *reinterpret_cast<const float4 *>(p);
+        v[0] = w.x;
+        v[1] = w.y;
+        v[2] = w.z;
+        v[3] = w.w;
+    } else {
+        const float2 w = *reinterpret_cast<const float2 *>(p);
+        v[0] = w.x;
+        v[1] = w.y;
+    }
+}
+template <int KS>
+__device__ __forceinline__ void store_ks(float *p, const float (&v)[KS]) {
+    if constexpr (KS == 4)
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+        *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+}
+
+// Rows of a token tile through a buffer resource: row r, byte v within it at
+// offset r * width + v from the tile's first row, rows past the last token
+// read as zero and are not written (the buffer range check).
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(T *base, int64_t row, int64_t rows,
+                                                            int32_t width) {
+    const int64_t left = rows < 64 ? (rows > 0 ? rows : 0) : 64;
+    return make_rsrc(base + row * width, (uint32_t)(left * width * (int64_t)sizeof(T)));
+}
+constexpr uint32_t kNoOffset = 0x80000000u;   // past every tile
+__device__ __forceinline__ Raw4<float> load_buf(__amdgpu_buffer_rsrc_t r, uint32_t off, float) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+    Raw4<float> o;
+    o.v = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]),
+                      __uint_as_float(v[3]));
+    return o;
+}
+__device__ __forceinline__ Raw4<uint16_t> load_buf(__amdgpu_buffer_rsrc_t r, uint32_t off,
+                                                   uint16_t) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+    Raw4<uint16_t> o;
+    o.v = make_uint2(v[0], v[1]);
+    return o;
+}
+__device__ __forceinline__ void store_buf(__amdgpu_buffer_rsrc_t r, uint32_t off, float4 v,
+                                          float) {
+    const u32x4 w = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
+                     __float_as_uint(v.w)};
+    __builtin_amdgcn_raw_buffer_store_b128(w, r, off, 0, 0);
+}
+__device__ __forceinline__ void store_buf(__amdgpu_buffer_rsrc_t r, uint32_t off, float4 v,
+                                          uint16_t) {
+    const u32x2 w = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+    __builtin_amdgcn_raw_buffer_store_b64(w, r, off, 0, 0);
+}
 
 struct SelGeom {
     int64_t T, Bt;
@@ -149,7 +236,7 @@ struct SelGeom {
 //              segments (each then started from zero), the sum of d up to it,
 //              the end states and sums of d.
 enum ScanMode { SCAN_OUT, SCAN_END, SCAN_CKPT };
-template <int N, typename Tio, typename Ty, bool GATE, bool RAG, ScanMode MODE>
+template <int N, int KS, typename Tio, typename Ty, bool GATE, bool RAG, ScanMode MODE>
 __global__ __launch_bounds__(256) void sel_scan_kernel(
     const Tio *__restrict__ x, const Tio *__restrict__ dt, const float *__restrict__ A,
     const Tio *__restrict__ B, const Tio *__restrict__ C, const float *__restrict__ D,
@@ -157,8 +244,9 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(
     const int32_t *__restrict__ lens, Ty *__restrict__ y, float *fin, float *__restrict__ dsum,
     float *__restrict__ ckpt, float *__restrict__ cumd, SelGeom g) {
     constexpr bool OUT = MODE == SCAN_OUT;
-    constexpr int S = SelSplit<N>::S, CPW = SelSplit<N>::CPW, CB = SelSplit<N>::CB;
-    constexpr int TL = Tile<N>::TL, VPR = Tile<N>::VPR, NBC = Tile<N>::NBC;
+    typedef SelSplit<N, KS> Sp;
+    constexpr int S = Sp::S, CPW = Sp::CPW, CB = Sp::CB, TL = Sp::TL, VPR = Sp::VPR;
+    constexpr int BC = Sp::BC, NBC = Sp::NBC;
     __shared__ __align__(16) float2 sdu[TL][CB];
     __shared__ __align__(16) float sbc[2][TL][N];
     __shared__ __align__(16) float sy[OUT ? TL : 1][OUT ? CB : 4];
@@ -185,52 +273,57 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(
         Dv[i] = OUT && i < scn ? D[sc + i] : 0.f;
     }
     const int64_t row0 = b * g.T;
-    auto load_tok = [&](const Tio *p, int64_t t) {
-        Raw4<Tio> r;
-        zero_raw(r);
-        if (t < te && scn > 0) r = load_raw<RAG>(p + (row0 + t) * g.Dm + sc, scn);
-        return r;
-    };
-    auto load_bc = [&](int64_t tb, int k) {           // vector k of this thread's B, C share
-        const int e = tid + 256 * k;
-        Raw4<Tio> r;
-        zero_raw(r);
-        if (e < 2 * TL * N / 4) {
-            const int q = e / (TL * N / 4), o = e % (TL * N / 4);
-            const int64_t t = tb + o / (N / 4);
-            if (t < te && (OUT || q == 0))
-                r = load_raw<false>((q ? C : B) + (row0 + t) * N + 4 * (o % (N / 4)), 4);
+    // (rows of an odd width are not aligned to a lane's vector: RAG takes them
+    // through plain loads and bounds its last channels by hand)
+    const uint32_t off = scn > 0 ? ((uint32_t)sr * g.Dm + sc) : kNoOffset / sizeof(Tio);
+    auto load_tok = [&](const Tio *p, int64_t tb) {
+        if constexpr (RAG) {
+            Raw4<Tio> r;
+            zero_raw(r);
+            if (tb + sr < te && scn > 0)
+                r = load_raw<true>(p + (row0 + tb + sr) * g.Dm + sc, scn);
+            return r;
+        } else {
+            return load_buf(tile_rsrc(p, row0 + tb, te - tb, g.Dm), off * sizeof(Tio), Tio());
         }
-        return r;
+    };
+    auto store_tok = [&](int64_t tb, float4 v) {
+        if constexpr (RAG) {
+            if (tb + sr < te && scn > 0)
+                store4<true>(y + (row0 + tb + sr) * g.Dm + sc, v, scn);
+        } else {
+            store_buf(tile_rsrc(y, row0 + tb, te - tb, g.Dm),
+                      scn > 0 ? off * (uint32_t)sizeof(Ty) : kNoOffset, v, Ty());
+        }
+    };
+    // vectors e of the tile's B (from the first thread up) and C (from the last down)
+    auto load_bc = [&](const Tio *p, int64_t tb, int e) {
+        return load_buf(tile_rsrc(p, row0 + tb, min(te - tb, (int64_t)TL), N),
+                        e < BC ? (uint32_t)e * 4 * sizeof(Tio) : kNoOffset, Tio());
     };
 
-    // scanning role: 4 states of one channel
+    // scanning role: KS states of one channel
     const int lane = tid & 63, wave = tid >> 6;
     const int s = lane % S, cl = wave * CPW + lane / S;
     const int32_t c = cb * CB + cl;
-    float a2[4], h[4], ds = 0.f;
+    float a2[KS], h[KS], ds = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a2[i] = h[i] = 0.f;
+    for (int i = 0; i < KS; ++i) a2[i] = h[i] = 0.f;
     if (c < g.Dm) {
-        const float4 av = *reinterpret_cast<const float4 *>(A + (int64_t)c * N + 4 * s);
-        a2[0] = av.x * kLog2e;
-        a2[1] = av.y * kLog2e;
-        a2[2] = av.z * kLog2e;
-        a2[3] = av.w * kLog2e;
-        if (start) {   // [Bt][nseg][Dm][N]: with one segment the initial state
-            const float4 hv = *reinterpret_cast<const float4 *>(
-                start + (((b * g.nseg) + seg) * g.Dm + c) * N + 4 * s);
-            h[0] = hv.x;
-            h[1] = hv.y;
-            h[2] = hv.z;
-            h[3] = hv.w;
-        }
+        load_ks(A + (int64_t)c * N + KS * s, a2);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) a2[i] *= kLog2e;
+        if (start)   // [Bt][nseg][Dm][N]: with one segment the initial state
+            load_ks(start + (((b * g.nseg) + seg) * g.Dm + c) * N + KS * s, h);
     }
 
-    Raw4<Tio> rx = load_tok(x, t0 + sr), rd = load_tok(dt, t0 + sr), rz, rbc[NBC];
-    if constexpr (GATE && OUT) rz = load_tok(z, t0 + sr);
+    Raw4<Tio> rx = load_tok(x, t0), rd = load_tok(dt, t0), rz, rb[NBC], rc[NBC];
+    if constexpr (GATE && OUT) rz = load_tok(z, t0);
 #pragma unroll
-    for (int k = 0; k < NBC; ++k) rbc[k] = load_bc(t0, k);
+    for (int k = 0; k < NBC; ++k) {
+        rb[k] = load_bc(B, t0, tid + 256 * k);
+        if constexpr (OUT) rc[k] = load_bc(C, t0, 255 - tid + 256 * k);
+    }
 
     for (int64_t tb = t0; tb < te; tb += TL) {
         // stage the tile
@@ -241,88 +334,89 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(
         for (int i = 0; i < 4; ++i) {
             const float r = dp[i] + bias[i];
             d[i] = g.softplus ? softplus_f(r) : r;
-            if (tb + sr >= te) d[i] = 0.f;
+        }
+        if (tb + TL > te) {   // (tokens past the end leave the state as it is)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (tb + sr >= te) d[i] = 0.f;
         }
         float4 *du = reinterpret_cast<float4 *>(&sdu[sr][4 * sv]);
         du[0] = make_float4(d[0], d[0] * xp[0], d[1], d[1] * xp[1]);
         du[1] = make_float4(d[2], d[2] * xp[2], d[3], d[3] * xp[3]);
 #pragma unroll
         for (int k = 0; k < NBC; ++k) {
-            const int e = tid + 256 * k;
-            if (e < 2 * TL * N / 4)
-                reinterpret_cast<float4 *>(&sbc[0][0][0])[e] = widen4(rbc[k]);
+            const int eb = tid + 256 * k, ec = 255 - tid + 256 * k;
+            if (eb < BC) reinterpret_cast<float4 *>(&sbc[0][0][0])[eb] = widen4(rb[k]);
+            if (OUT && ec < BC) reinterpret_cast<float4 *>(&sbc[1][0][0])[ec] = widen4(rc[k]);
         }
         // the next tile's loads, in flight during the scan
         const int64_t tn = tb + TL;
-        const Raw4<Tio> nx = load_tok(x, tn + sr), nd = load_tok(dt, tn + sr);
-        Raw4<Tio> nz, nbc[NBC];
-        if constexpr (GATE && OUT) nz = load_tok(z, tn + sr);
+        const Raw4<Tio> nx = load_tok(x, tn), nd = load_tok(dt, tn);
+        Raw4<Tio> nz;
+        if constexpr (GATE && OUT) nz = load_tok(z, tn);
 #pragma unroll
-        for (int k = 0; k < NBC; ++k) nbc[k] = load_bc(tn, k);
+        for (int k = 0; k < NBC; ++k) {
+            rb[k] = load_bc(B, tn, tid + 256 * k);
+            if constexpr (OUT) rc[k] = load_bc(C, tn, 255 - tid + 256 * k);
+        }
         lds_barrier();
 
         // scan the tile
+        constexpr int U = TL < 32 ? TL : 32;   // tokens unrolled
 #pragma unroll 1
-        for (int tq = 0; tq < TL; tq += 8) {
-            if constexpr (MODE == SCAN_CKPT) {
-                const int64_t t = tb + tq;
-                if ((t & 15) == 0 && t < te && c < g.Dm) {
-                    const int64_t u = (b * ((g.T + 15) >> 4) + (t >> 4)) * g.Dm + c;
-                    *reinterpret_cast<float4 *>(ckpt + u * N + 4 * s) =
-                        make_float4(h[0], h[1], h[2], h[3]);
-                    if (g.nseg > 1 && s == 0) cumd[u] = ds;
-                }
-            }
-            float keep = 0.f;
+        for (int tq = 0; tq < TL; tq += U) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int t = tq + k;
-                const float2 w = sdu[t][cl];
-                const float4 bv = *reinterpret_cast<const float4 *>(&sbc[0][t][4 * s]);
-                h[0] = fmaf(fast_exp2(w.x * a2[0]), h[0], w.y * bv.x);
-                h[1] = fmaf(fast_exp2(w.x * a2[1]), h[1], w.y * bv.y);
-                h[2] = fmaf(fast_exp2(w.x * a2[2]), h[2], w.y * bv.z);
-                h[3] = fmaf(fast_exp2(w.x * a2[3]), h[3], w.y * bv.w);
-                if constexpr (OUT) {
-                    const float4 cv = *reinterpret_cast<const float4 *>(&sbc[1][t][4 * s]);
-                    float p = h[0] * cv.x + h[1] * cv.y + h[2] * cv.z + h[3] * cv.w;
-                    p = chan_sum<S>(p);
-                    // lane s of a channel keeps token s of every S
-                    if (S >= 8 ? s == t % S : s == k % S) keep = p;
-                    if constexpr (S <= 8) {
-                        if ((k + 1) % S == 0) sy[t - (S - 1) + s][cl] = keep;
-                    } else if (k == 7 && (s >> 3) == ((tq >> 3) & 1)) {
-                        sy[(tq & ~(S - 1)) + s][cl] = keep;
+            for (int k0 = 0; k0 < U; k0 += S) {
+                float p[S];
+#pragma unroll
+                for (int k = 0; k < S; ++k) {
+                    const int t = tq + k0 + k;
+                    if constexpr (MODE == SCAN_CKPT) {
+                        if ((k0 + k) % 8 == 0 && ((tb + t) & 15) == 0 && tb + t < te && c < g.Dm) {
+                            const int64_t u =
+                                (b * ((g.T + 15) >> 4) + ((tb + t) >> 4)) * g.Dm + c;
+                            store_ks(ckpt + u * N + KS * s, h);
+                            if (g.nseg > 1 && s == 0) cumd[u] = ds;
+                        }
                     }
-                } else {
-                    ds += w.x;
+                    const float2 w = sdu[t][cl];
+                    float bv[KS];
+                    load_ks(&sbc[0][t][KS * s], bv);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+                        h[i] = fmaf(fast_exp2(w.x * a2[i]), h[i], w.y * bv[i]);
+                    if constexpr (OUT) {
+                        float cv[KS];
+                        load_ks(&sbc[1][t][KS * s], cv);
+                        p[k] = h[0] * cv[0];
+#pragma unroll
+                        for (int i = 1; i < KS; ++i) p[k] = fmaf(h[i], cv[i], p[k]);
+                    } else {
+                        ds += w.x;
+                    }
                 }
+                if constexpr (OUT) sy[tq + k0 + s][cl] = lane_sums<S>(p, s);
             }
         }
         lds_barrier();
 
         if constexpr (OUT) {
-            const int64_t t = tb + sr;
-            if (t < te && scn > 0) {
-                const float4 yv = *reinterpret_cast<const float4 *>(&sy[sr][4 * sv]);
-                const float *yp = &yv.x;
-                float o[4];
+            const float4 yv = *reinterpret_cast<const float4 *>(&sy[sr][4 * sv]);
+            const float *yp = &yv.x;
+            float o[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = yp[i] + Dv[i] * xp[i];
-                if constexpr (GATE) {
-                    const float4 zv = widen4(rz);
-                    const float *zp = &zv.x;
+            for (int i = 0; i < 4; ++i) o[i] = yp[i] + Dv[i] * xp[i];
+            if constexpr (GATE) {
+                const float4 zv = widen4(rz);
+                const float *zp = &zv.x;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] *= fast_silu(zp[i]);
-                }
-                store4<RAG>(y + (row0 + t) * g.Dm + sc, make_float4(o[0], o[1], o[2], o[3]), scn);
+                for (int i = 0; i < 4; ++i) o[i] *= fast_silu(zp[i]);
             }
+            store_tok(tb, make_float4(o[0], o[1], o[2], o[3]));
             if constexpr (GATE) rz = nz;
         }
         rx = nx;
         rd = nd;
-#pragma unroll
-        for (int k = 0; k < NBC; ++k) rbc[k] = nbc[k];
     }
 
     if constexpr (OUT) {
@@ -331,11 +425,10 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(
             for (int64_t t = te + sr; t < t1; t += TL)
                 store4<RAG>(y + (row0 + t) * g.Dm + sc, make_float4(0.f, 0.f, 0.f, 0.f), scn);
         if (fin && seg == g.nseg - 1 && c < g.Dm)
-            *reinterpret_cast<float4 *>(fin + (b * g.Dm + c) * N + 4 * s) =
-                make_float4(h[0], h[1], h[2], h[3]);
+            store_ks(fin + (b * g.Dm + c) * N + KS * s, h);
     } else if (c < g.Dm && g.nseg > 1) {
         const int64_t u = (b * g.nseg + seg) * g.Dm + c;
-        *reinterpret_cast<float4 *>(fin + u * N + 4 * s) = make_float4(h[0], h[1], h[2], h[3]);
+        store_ks(fin + u * N + KS * s, h);
         if (s == 0) dsum[u] = ds;
     }
 }
@@ -363,6 +456,8 @@ void by_flag(bool v, F f) {
 }
 
 inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline int64_t chan_blocks(const SelArgs &a) { return cdiv64(a.Dm, 1024 / a.N); }
+inline int64_t chan_blocks(const SelArgs &a, int ks = 4) {
+    return cdiv64(a.Dm, 256 * ks / a.N);
+}
 
 }  // namespace ssd

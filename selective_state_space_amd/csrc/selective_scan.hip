@@ -40,12 +40,20 @@ __global__ __launch_bounds__(256) void sel_chain_kernel(float *__restrict__ seg,
     float h = init ? init[i] : 0.f;
     float *p = seg + b * nseg * per + cn;
     const float *q = dsum + b * nseg * Dm + c;
-    for (int32_t k = 0; k < nseg; ++k) {
-        const bool more = k + 1 < nseg;
-        const float e = more ? p[k * per] : 0.f;
-        const float d = more ? q[(int64_t)k * Dm] : 0.f;
-        p[k * per] = h;
-        h = fmaf(fast_exp2(d * a2), h, e);
+    // 8 segments' values in flight at a time (the last end state is not there)
+    for (int32_t k0 = 0; k0 < nseg; k0 += 8) {
+        float e[8], d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int32_t k = k0 + j;
+            e[j] = k + 1 < nseg ? p[k * per] : 0.f;
+            d[j] = k + 1 < nseg ? q[(int64_t)k * Dm] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (k0 + j < nseg) p[(k0 + j) * per] = h;
+            h = fmaf(fast_exp2(d[j] * a2), h, e[j]);
+        }
     }
 }
 
@@ -113,26 +121,49 @@ __global__ __launch_bounds__(256) void sel_step_kernel(
     }
 }
 
-struct Segs {
-    int64_t n, len;
+// How a launch is cut: states per lane, and segments of a sequence.
+//   * Sequences and channels alone fill the chip (400 workgroups or more with 2
+//     states per lane): one segment, as a second pass over the tokens costs
+//     more than idle lanes.  2 states per lane give twice the wavefronts of 4
+//     (8 x 4096 tokens, 5120 channels, N 16: 741 us against 882, 5 wavefronts
+//     per SIMD against 2.5), but 4 do less work per state once they fill it too
+//     (16 x 2048 tokens: 705 us against 713).
+//   * Else segments of at least 64 tokens, enough for 2048 workgroups of the
+//     4-state form (1 x 4096 tokens, 5120 channels: 153 us in 32 segments, 285
+//     us in one).
+struct Cut {
+    int ks;
+    int64_t ncb, n, len;
 };
-// Segments of a sequence: one where sequences and channel blocks alone give 2
-// workgroups per CU (a second pass over the tokens costs more than the idle
-// lanes), else enough for 4, of at least 64 tokens each.
-Segs segments(const SelArgs &a) {
-    const int64_t blocks = a.Bt * chan_blocks(a);
-    const int64_t tile = a.N;
-    Segs s{1, cdiv64(a.T > 0 ? a.T : 1, tile) * tile};
-    if (blocks >= 512 || blocks == 0) return s;
-    int64_t n = cdiv64(1024, blocks);
-    n = n < a.T / 64 ? n : a.T / 64;
-    if (n < 2) return s;
-    s.len = cdiv64(cdiv64(a.T, n), tile) * tile;
-    s.n = cdiv64(a.T, s.len);
+Cut cut_of(const SelArgs &a) {
+    const int64_t few = a.N == 64 ? 4 : 2;   // (16 lanes of a channel at most)
+    const int64_t b4 = a.Bt * chan_blocks(a, 4), bf = a.Bt * chan_blocks(a, few);
+    Cut s;
+    s.ks = (int)(b4 >= 1024 ? 4 : few);
+    s.n = 1;
+    if (bf > 0 && bf < 400) {
+        int64_t n = cdiv64(2048, b4);
+        n = n < a.T / 64 ? n : a.T / 64;
+        if (n > 1) {
+            s.n = n;
+            s.ks = (int)(b4 * n >= 1024 ? 4 : few);
+        }
+    }
+    s.ncb = chan_blocks(a, s.ks);
+    const int64_t tile = 4 * a.N / s.ks;
+    s.len = cdiv64(cdiv64(a.T > 0 ? a.T : 1, s.n), tile) * tile;
+    if (s.n > 1) s.n = cdiv64(a.T, s.len);
     return s;
 }
-size_t seg_bytes(const SelArgs &a, const Segs &s) {
+size_t seg_bytes(const SelArgs &a, const Cut &s) {
     return s.n > 1 ? (size_t)(a.Bt * s.n * a.Dm * a.N) * sizeof(float) : 0;
+}
+// f(integral_constant<KS>): the sums over a channel's lanes are built for up to 16
+template <int N, typename F>
+void by_ks(const Cut &s, F f) {
+    if constexpr (N < 64)
+        if (s.ks == 2) return f(std::integral_constant<int, 2>());
+    f(std::integral_constant<int, 4>());
 }
 
 // f(y type): bf16 where the caller asked for the io dtype and that is bf16
@@ -154,18 +185,18 @@ bool selective_scan_fits(const SelArgs &a) {
 }
 
 size_t selective_scan_workspace(const SelArgs &a) {
-    const Segs s = segments(a);
+    const Cut s = cut_of(a);
     const size_t b = seg_bytes(a, s);
     return b ? b + (size_t)(a.Bt * s.n * a.Dm) * sizeof(float) : 0;
 }
 
 hipError_t launch_selective_scan(const SelArgs &a, hipStream_t st) {
-    const Segs sg = segments(a);
+    const Cut sg = cut_of(a);
     SelGeom g;
     g.T = a.T;
     g.Bt = a.Bt;
     g.Dm = (int32_t)a.Dm;
-    g.ncb = (int32_t)chan_blocks(a);
+    g.ncb = (int32_t)sg.ncb;
     g.nseg = (int32_t)sg.n;
     g.seg_len = sg.len;
     g.softplus = a.softplus ? 1 : 0;
@@ -177,12 +208,15 @@ hipError_t launch_selective_scan(const SelArgs &a, hipStream_t st) {
         float *dsum = seg + (size_t)(a.Bt * sg.n * a.Dm * a.N);
         by_state(a, [&](auto n, auto io) {
             typedef decltype(io) Tio;
-            by_flag(rag, [&](auto r) {
-                sel_scan_kernel<decltype(n)::value, Tio, float, false, decltype(r)::value, SCAN_END>
-                    <<<dim3((uint32_t)(a.Bt * (sg.n - 1) * g.ncb)), 256, 0, st>>>(
-                        (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B, nullptr,
-                        nullptr, nullptr, a.dt_bias, nullptr, a.lens, nullptr, seg, dsum,
-                        nullptr, nullptr, g);
+            by_ks<decltype(n)::value>(sg, [&](auto ks) {
+                by_flag(rag, [&](auto r) {
+                    sel_scan_kernel<decltype(n)::value, decltype(ks)::value, Tio, float, false,
+                                    decltype(r)::value, SCAN_END>
+                        <<<dim3((uint32_t)(a.Bt * (sg.n - 1) * g.ncb)), 256, 0, st>>>(
+                            (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B, nullptr,
+                            nullptr, nullptr, a.dt_bias, nullptr, a.lens, nullptr, seg, dsum,
+                            nullptr, nullptr, g);
+                });
             });
         });
         e = hipGetLastError();
@@ -196,17 +230,19 @@ hipError_t launch_selective_scan(const SelArgs &a, hipStream_t st) {
     }
     by_state(a, [&](auto n, auto io) {
         typedef decltype(io) Tio;
-        by_flag(rag, [&](auto r) {
-            by_flag(a.z != nullptr, [&](auto gate) {
-                by_y(a, [&](auto yt) {
-                    typedef decltype(yt) Ty;
-                    if constexpr (sizeof(Ty) == 4 || sizeof(Tio) == 2)   // bf16 y only for bf16 io
-                        sel_scan_kernel<decltype(n)::value, Tio, Ty, decltype(gate)::value,
-                                        decltype(r)::value, SCAN_OUT>
-                            <<<dim3((uint32_t)(a.Bt * sg.n * g.ncb)), 256, 0, st>>>(
-                                (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B,
-                                (const Tio *)a.C, a.D, (const Tio *)a.z, a.dt_bias, start, a.lens,
-                                (Ty *)a.y, a.fin, nullptr, nullptr, nullptr, g);
+        by_ks<decltype(n)::value>(sg, [&](auto ks) {
+            by_flag(rag, [&](auto r) {
+                by_flag(a.z != nullptr, [&](auto gate) {
+                    by_y(a, [&](auto yt) {
+                        typedef decltype(yt) Ty;
+                        if constexpr (sizeof(Ty) == 4 || sizeof(Tio) == 2)   // bf16 y: bf16 io
+                            sel_scan_kernel<decltype(n)::value, decltype(ks)::value, Tio, Ty,
+                                            decltype(gate)::value, decltype(r)::value, SCAN_OUT>
+                                <<<dim3((uint32_t)(a.Bt * sg.n * g.ncb)), 256, 0, st>>>(
+                                    (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B,
+                                    (const Tio *)a.C, a.D, (const Tio *)a.z, a.dt_bias, start,
+                                    a.lens, (Ty *)a.y, a.fin, nullptr, nullptr, nullptr, g);
+                    });
                 });
             });
         });

@@ -179,17 +179,36 @@ __global__ __launch_bounds__(256) void sel_chain_bwd_kernel(
     const float *q = dsum + b * nseg * Dm + cn / N;
     float *p = hseg + b * nseg * per + cn;
     float h = init ? init[i] : 0.f;
-    for (int32_t k = 0; k < nseg; ++k) {
-        const float e = p[k * per];
-        p[k * per] = h;
-        h = fmaf(fast_exp2(q[(int64_t)k * Dm] * a2), h, e);
+    // 8 segments' values in flight at a time
+    for (int32_t k0 = 0; k0 < nseg; k0 += 8) {
+        float e[8], d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int32_t k = k0 + j;
+            e[j] = k < nseg ? p[k * per] : 0.f;
+            d[j] = k < nseg ? q[(int64_t)k * Dm] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (k0 + j < nseg) p[(k0 + j) * per] = h;
+            h = fmaf(fast_exp2(d[j] * a2), h, e[j]);
+        }
     }
     p = adj + b * nseg * per + cn;
     float r = dfinal ? dfinal[i] : 0.f;
-    for (int32_t k = nseg - 1; k >= 0; --k) {
-        const float e = k > 0 ? p[k * per] : 0.f;
-        p[k * per] = r;
-        r = fmaf(fast_exp2(q[(int64_t)k * Dm] * a2), r, e);
+    for (int32_t k0 = nseg - 1; k0 >= 0; k0 -= 8) {
+        float e[8], d[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int32_t k = k0 - j;
+            e[j] = k > 0 ? p[k * per] : 0.f;
+            d[j] = k >= 0 ? q[(int64_t)k * Dm] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (k0 - j >= 0) p[(k0 - j) * per] = r;
+            r = fmaf(fast_exp2(d[j] * a2), r, e[j]);
+        }
     }
 }
 
@@ -606,7 +625,7 @@ hipError_t launch_selective_scan_bwd(const SelArgs &a, hipStream_t st) {
         by_state(a, [&](auto n, auto io) {
             typedef decltype(io) Tio;
             by_flag(rag, [&](auto r) {
-                sel_scan_kernel<decltype(n)::value, Tio, float, false, decltype(r)::value,
+                sel_scan_kernel<decltype(n)::value, 4, Tio, float, false, decltype(r)::value,
                                 SCAN_CKPT><<<dim3((uint32_t)(rows * g.ncb)), 256, 0, st>>>(
                     (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B, nullptr, nullptr,
                     nullptr, a.dt_bias, split ? nullptr : a.init, nullptr, nullptr, ws + p.hseg,
