@@ -609,26 +609,34 @@ def _on_gpu(t: torch.Tensor, name: str) -> torch.device:
     return t.device
 
 
+def _current_stream(dev: torch.device) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# torch's raw handle of the current stream (what current_stream wraps, at a tenth of its
+# cost per call), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _call(fn: str, dev: torch.device, *args):
     """One library call on dev's current stream, with dev the current device."""
     f = getattr(load_library(), fn)
+    stream = _current_stream(dev) if _raw_stream is None else _raw_stream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = f(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = f(*args, stream)
     if st != 0:
         _check(fn, st)
-
-
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
 
 
 def _in(t, name, dtype, shape, device):
     """An input the library can read: contiguous, and a copy where a view starts off a
     16-byte boundary."""
-    t = _need(t, name, dtype, shape, device)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        t = _need(t, name, dtype, shape, device)
     return t.clone() if t.data_ptr() & 15 else t
 
 
@@ -636,8 +644,15 @@ def _opt(t, name, dtype, shape, device):
     return None if t is None else _in(t, name, dtype, shape, device)
 
 
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+_Ptr3 = ctypes.c_void_p * 3
+
+
 def _parts3(ts):
-    return (ctypes.c_void_p * 3)(*[_addr(t) if t is not None and t.numel() else None for t in ts])
+    return _Ptr3(*[None if t is None or not t.numel() else t.data_ptr() for t in ts])
 
 
 def _conv_args(x, weight, bias, splits, silu, tokens: int):
@@ -656,7 +671,7 @@ def _conv_args(x, weight, bias, splits, silu, tokens: int):
     if not 1 <= len(splits) <= 3 or sum(splits) != C or min(splits) < 0:
         raise ValueError("splits %s must be one to three channel counts that sum to %d"
                          % (splits, C))
-    if C > 1 and x.stride(-1) != 1 or min(x.stride()) < 0:
+    if C > 1 and x.stride(-1) != 1:
         x = x.contiguous()
     dims = ConvDims(x.shape[0], x.shape[1] if tokens else 1, weight.shape[1],
                     (ctypes.c_int64 * 3)(*(splits + (0, 0))[:3]), x.stride(0),
