@@ -184,6 +184,14 @@ __device__ __forceinline__ void store_ks(float *p, const float (&v)[KS]) {
         *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
 }
 
+// A value that every lane holds alike, in scalar registers: a resource built
+// from vector registers would be read lane by lane in a loop.
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // Rows of a token tile through a buffer resource: row r, byte v within it at
 // offset r * width + v from the tile's first row, rows past the last token
 // read as zero and are not written (the buffer range check).
@@ -191,7 +199,9 @@ template <typename T>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_rsrc(T *base, int64_t row, int64_t rows,
                                                             int32_t width) {
     const int64_t left = rows < 64 ? (rows > 0 ? rows : 0) : 64;
-    return make_rsrc(base + row * width, (uint32_t)(left * width * (int64_t)sizeof(T)));
+    return make_rsrc(base + uniform64(row * width),
+                     __builtin_amdgcn_readfirstlane(
+                         (uint32_t)(left * width * (int64_t)sizeof(T))));
 }
 constexpr uint32_t kNoOffset = 0x80000000u;   // past every tile
 __device__ __forceinline__ Raw4<float> load_buf(__amdgpu_buffer_rsrc_t r, uint32_t off, float) {
@@ -218,6 +228,21 @@ __device__ __forceinline__ void store_buf(__amdgpu_buffer_rsrc_t r, uint32_t off
                                           uint16_t) {
     const u32x2 w = {pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
     __builtin_amdgcn_raw_buffer_store_b64(w, r, off, 0, 0);
+}
+
+// KS floats at byte offset off (zero past the resource)
+template <int KS>
+__device__ __forceinline__ void load_buf_ks(__amdgpu_buffer_rsrc_t r, uint32_t off,
+                                            float (&v)[KS]) {
+    if constexpr (KS == 4) {
+        const auto w = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+        const auto w = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+        v[0] = __uint_as_float(w[0]);
+        v[1] = __uint_as_float(w[1]);
+    }
 }
 
 struct SelGeom {

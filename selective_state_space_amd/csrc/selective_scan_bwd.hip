@@ -25,6 +25,8 @@
 // decayed entry state to its checkpoints; the adjoints entering the segments
 // come from a reverse pass without outputs and a chain over segments.
 
+#include <type_traits>
+
 #include "selective_scan.h"
 
 namespace ssd {
@@ -33,44 +35,15 @@ namespace {
 
 constexpr int TB = 16;   // tokens of a backward tile, and between checkpoints
 
-template <int N>
+template <int N, int KS>
 struct BTile {
-    static constexpr int VPR = SelSplit<N>::CB / 4;              // 4-channel vectors of a row
+    typedef SelSplit<N, KS> Sp;
+    static constexpr int VPR = Sp::CB / 4;                       // 4-channel vectors of a row
     static constexpr int ITEMS = TB * VPR;                       // (token, vector) pairs
     static constexpr int NI = (ITEMS + 255) / 256;               // of them per thread
     static constexpr int ROWS = ITEMS < 256 ? ITEMS / VPR : 256 / VPR;
     static constexpr int BC = TB * N / 4;                        // 4-element vectors of B (or C)
-    static constexpr int NBC = (2 * BC + 255) / 256;
 };
-
-// 8 values per lane summed over the channels of the wavefront: afterwards the
-// lanes of each half (0 = v[0..3], 1 = v[4..7]) and row parity hold the sums of
-// values 2 parity and 2 parity + 1 of their half for their lane s.
-__device__ __forceinline__ float add_swapped32(float a, float b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
-                                                    false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-__device__ __forceinline__ float add_swapped16(float a, float b) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false,
-                                                    false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-template <int S>
-__device__ __forceinline__ float row_sum(float v) {
-    if constexpr (S <= 8) v += dpp_mov<0x128>(v);   // row_ror:8
-    if constexpr (S <= 4) v += dpp_mov<0x124>(v);   // row_ror:4
-    if constexpr (S <= 2) v += dpp_mov<0x122>(v);   // row_ror:2
-    return v;
-}
-template <int S>
-__device__ __forceinline__ float2 channels_sum(const float (&v)[8]) {
-    float r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = add_swapped32(v[i], v[i + 4]);
-    return make_float2(row_sum<S>(add_swapped16(r[0], r[2])),
-                       row_sum<S>(add_swapped16(r[1], r[3])));
-}
 
 // silu(z) and its derivative
 __device__ __forceinline__ void silu_grad(float z, float &f, float &df) {
@@ -86,9 +59,9 @@ __global__ __launch_bounds__(256) void sel_adj_kernel(
     const Tio *__restrict__ dt, const float *__restrict__ A, const Tio *__restrict__ C,
     const Tio *__restrict__ z, const float *__restrict__ dt_bias, const float *__restrict__ dy,
     float *__restrict__ adj, SelGeom g) {
-    constexpr int S = SelSplit<N>::S, CPW = SelSplit<N>::CPW, CB = SelSplit<N>::CB;
-    constexpr int VPR = BTile<N>::VPR, NI = BTile<N>::NI, ITEMS = BTile<N>::ITEMS;
-    constexpr int BC = BTile<N>::BC;
+    constexpr int S = SelSplit<N, 4>::S, CPW = SelSplit<N, 4>::CPW, CB = SelSplit<N, 4>::CB;
+    constexpr int VPR = BTile<N, 4>::VPR, NI = BTile<N, 4>::NI, ITEMS = BTile<N, 4>::ITEMS;
+    constexpr int BC = BTile<N, 4>::BC;
     __shared__ __align__(16) float2 sdy[TB][CB];   // (d, dyp)
     __shared__ __align__(16) float sc[TB][N];
     const int tid = threadIdx.x;
@@ -212,7 +185,7 @@ __global__ __launch_bounds__(256) void sel_chain_bwd_kernel(
     }
 }
 
-template <int N, typename Tio, bool GATE, bool RAG>
+template <int N, int KS, typename Tio, bool GATE, bool RAG>
 __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
     const Tio *__restrict__ x, const Tio *__restrict__ dt, const float *__restrict__ A,
     const Tio *__restrict__ B, const Tio *__restrict__ C, const float *__restrict__ D,
@@ -222,15 +195,23 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
     float *__restrict__ ddt, float *__restrict__ dz, float *__restrict__ dinit,
     float *__restrict__ pbc, float *__restrict__ pA, float *__restrict__ pD,
     float *__restrict__ pbias, SelGeom g) {
-    constexpr int S = SelSplit<N>::S, CPW = SelSplit<N>::CPW, CB = SelSplit<N>::CB;
-    constexpr int VPR = BTile<N>::VPR, NI = BTile<N>::NI, ITEMS = BTile<N>::ITEMS;
-    constexpr int BC = BTile<N>::BC, NBC = BTile<N>::NBC, ROWS = BTile<N>::ROWS;
+    typedef SelSplit<N, KS> Sp;
+    typedef BTile<N, KS> Bt;
+    constexpr int S = Sp::S, CPW = Sp::CPW, CB = Sp::CB;
+    constexpr int VPR = Bt::VPR, NI = Bt::NI, ITEMS = Bt::ITEMS;
+    constexpr int BC = Bt::BC, NBC = (BC + 255) / 256, ROWS = Bt::ROWS;
     __shared__ __align__(16) float2 sdu[TB][CB];          // (d, d x)
     __shared__ __align__(16) float sdy[TB][CB];           // dyp
     __shared__ __align__(16) float sbc[2][TB][N];
     __shared__ __align__(16) float2 sgd[TB][CB];          // (gB, sum q a2)
     __shared__ __align__(16) float sy[GATE ? TB : 1][GATE ? CB : 4];
     __shared__ __align__(16) float sdbc[4][TB][2 * N];
+    // the products summed over a wavefront's channels: RT tokens of [channel][dB, dC]
+    constexpr int RT = N <= 16 ? 2 : 1;
+    constexpr int RV = N <= 32 ? 1 : 2;                       // values per summing lane
+    constexpr int RC = N == 8 ? CPW / 2 : CPW;                // channels it sums
+    constexpr int RP = CPW * 2 * N + 32;                      // (+ 32: tokens on other banks)
+    __shared__ __align__(16) float sred[4][RT][RP];
     const int tid = threadIdx.x;
     const uint32_t cb = blockIdx.x % (uint32_t)g.ncb;
     const uint32_t rest = blockIdx.x / (uint32_t)g.ncb;   // (b, segment)
@@ -239,7 +220,10 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
     const int64_t t0 = seg * g.seg_len, t1 = min(g.T, t0 + g.seg_len);
     const int64_t ntile = (t1 - t0 + TB - 1) / TB;
 
-    const int sv = tid % VPR;
+    // (staging may need half of the threads: odd and even workgroups take
+    // different halves, so that every SIMD has its share)
+    const int st = ITEMS < 256 ? tid ^ (int)((blockIdx.x & 1) << 7) : tid;
+    const int sv = st % VPR;
     const int32_t ch0 = cb * CB + 4 * sv;
     const int chn = min(4, g.Dm - ch0);
     float bias[4], Dv[4], accD[4] = {}, accb[4] = {};
@@ -251,89 +235,94 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
     const int lane = tid & 63, wave = tid >> 6;
     const int s = lane % S, cl = wave * CPW + lane / S;
     const int32_t c = cb * CB + cl;
-    float a2[4] = {}, car[4] = {}, dA[4] = {};
-    float4 hs = make_float4(0.f, 0.f, 0.f, 0.f);
+    float a2[KS] = {}, car[KS] = {}, dA[KS] = {}, hs[KS] = {};
     if (c < g.Dm) {
-        const float4 av = *reinterpret_cast<const float4 *>(A + (int64_t)c * N + 4 * s);
-        a2[0] = av.x * kLog2e;
-        a2[1] = av.y * kLog2e;
-        a2[2] = av.z * kLog2e;
-        a2[3] = av.w * kLog2e;
-        const int64_t u = ((int64_t)rest * g.Dm + c) * N + 4 * s;
-        if (right) {   // [Bt][nseg][Dm][N]: with one segment dfinal
-            const float4 rv = *reinterpret_cast<const float4 *>(right + u);
-            car[0] = rv.x;
-            car[1] = rv.y;
-            car[2] = rv.z;
-            car[3] = rv.w;
-        }
-        if (g.nseg > 1) hs = *reinterpret_cast<const float4 *>(hseg + u);
+        load_ks(A + (int64_t)c * N + KS * s, a2);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) a2[i] *= kLog2e;
+        const int64_t u = ((int64_t)rest * g.Dm + c) * N + KS * s;
+        if (right) load_ks(right + u, car);   // [Bt][nseg][Dm][N]: with one segment dfinal
+        if (g.nseg > 1) load_ks(hseg + u, hs);
     }
-
     struct Tok {
         Raw4<Tio> x, dt, z;
         Raw4<float> dy;
     };
+    // (rows of an odd width are not aligned to a lane's vector: RAG takes them
+    // through plain loads and bounds its last channels by hand)
+    const int64_t row0 = b * g.T;
+    const uint32_t off = chn > 0 ? (uint32_t)(st / VPR) * g.Dm + ch0 : kNoOffset / 4;
+    const uint32_t item = (256 / VPR) * (uint32_t)g.Dm;   // elements between a thread's items
+    auto left = [&](int64_t tb) { return tb >= t0 ? min(t1 - tb, (int64_t)TB) : (int64_t)0; };
+    auto load_one = [&](auto *p, int64_t tb, int i) {
+        typedef typename std::remove_cv<typename std::remove_pointer<decltype(p)>::type>::type T;
+        if constexpr (RAG) {
+            Raw4<T> r;
+            zero_raw(r);
+            const int64_t row = (st + 256 * i) / VPR;
+            if (st + 256 * i < ITEMS && row < left(tb) && chn > 0)
+                r = load_raw<true>(p + (row0 + tb + row) * g.Dm + ch0, chn);
+            return r;
+        } else {
+            return load_buf(tile_rsrc(p, row0 + tb, left(tb), g.Dm),
+                            (off + i * item) * (uint32_t)sizeof(T), T());
+        }
+    };
+    auto store_one = [&](float *p, int64_t tb, int i, float4 v) {
+        if constexpr (RAG) {
+            const int64_t row = (st + 256 * i) / VPR;
+            if (row < left(tb) && chn > 0)
+                store4<true>(p + (row0 + tb + row) * g.Dm + ch0, v, chn);
+        } else {
+            store_buf(tile_rsrc(p, row0 + tb, left(tb), g.Dm), (off + i * item) * 4u, v, 0.f);
+        }
+    };
     auto load_tok = [&](int64_t tb, int i) {
-        const int e = tid + 256 * i;
-        const int64_t t = tb + e / VPR;
         Tok r;
-        zero_raw(r.x);
-        zero_raw(r.dt);
-        zero_raw(r.z);
-        zero_raw(r.dy);
-        if (e < ITEMS && tb >= t0 && t < t1 && chn > 0) {
-            const int64_t o = (b * g.T + t) * g.Dm + ch0;
-            r.x = load_raw<RAG>(x + o, chn);
-            r.dt = load_raw<RAG>(dt + o, chn);
-            r.dy = load_raw<RAG>(dy + o, chn);
-            if constexpr (GATE) r.z = load_raw<RAG>(z + o, chn);
-        }
+        r.x = load_one(x, tb, i);
+        r.dt = load_one(dt, tb, i);
+        r.dy = load_one(dy, tb, i);
+        if constexpr (GATE) r.z = load_one(z, tb, i);
         return r;
     };
-    auto load_bc = [&](int64_t tb, int k) {
-        const int e = tid + 256 * k;
-        Raw4<Tio> r;
-        zero_raw(r);
-        if (e < 2 * BC) {
-            const int o = e % BC;
-            const int64_t t = tb + o / (N / 4);
-            if (tb >= t0 && t < t1)
-                r = load_raw<false>((e / BC ? C : B) + (b * g.T + t) * N + 4 * (o % (N / 4)), 4);
-        }
-        return r;
+    // vectors e of the tile's B (from the first thread up) and C (from the last down)
+    auto load_bc = [&](const Tio *p, int64_t tb, int e) {
+        return load_buf(tile_rsrc(p, row0 + tb, left(tb), N),
+                        e < BC ? (uint32_t)e * 4 * sizeof(Tio) : kNoOffset, Tio());
     };
-    auto load_h0 = [&](int64_t tb) {
-        float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < g.Dm && tb >= t0) {
-            const int64_t u = (b * ((g.T + 15) >> 4) + (tb >> 4)) * g.Dm + c;
-            h = *reinterpret_cast<const float4 *>(ckpt + u * N + 4 * s);
-            if (g.nseg > 1) {
-                const float cd = cumd[u];
-                h.x = fmaf(fast_exp2(cd * a2[0]), hs.x, h.x);
-                h.y = fmaf(fast_exp2(cd * a2[1]), hs.y, h.y);
-                h.z = fmaf(fast_exp2(cd * a2[2]), hs.z, h.z);
-                h.w = fmaf(fast_exp2(cd * a2[3]), hs.w, h.w);
-            }
+    const uint32_t coff = c < g.Dm ? (uint32_t)c * N + KS * s : kNoOffset / 4;
+    auto load_h0 = [&](int64_t tb, float (&h)[KS]) {
+        const int64_t u = uniform64((b * ((g.T + 15) >> 4) + (tb >> 4)) * g.Dm);
+        const uint32_t bytes =
+            __builtin_amdgcn_readfirstlane(tb >= t0 ? (uint32_t)g.Dm * 4u : 0u);
+        load_buf_ks(make_rsrc(ckpt + u * N, bytes * N), coff * 4u, h);
+        if (g.nseg > 1) {
+            const float cd = __uint_as_float(
+                __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(cumd + u, bytes), c * 4u, 0, 0));
+#pragma unroll
+            for (int i = 0; i < KS; ++i) h[i] = fmaf(fast_exp2(cd * a2[i]), hs[i], h[i]);
         }
-        return h;
     };
 
     int64_t tb = t0 + (ntile - 1) * TB;
     Tok tok[NI];
-    Raw4<Tio> rbc[NBC];
+    Raw4<Tio> rb[NBC], rc[NBC];
 #pragma unroll
     for (int i = 0; i < NI; ++i) tok[i] = load_tok(tb, i);
 #pragma unroll
-    for (int k = 0; k < NBC; ++k) rbc[k] = load_bc(tb, k);
-    float4 h0 = load_h0(tb);
+    for (int k = 0; k < NBC; ++k) {
+        rb[k] = load_bc(B, tb, tid + 256 * k);
+        rc[k] = load_bc(C, tb, 255 - tid + 256 * k);
+    }
+    float h0[KS];
+    load_h0(tb, h0);
 
     for (; tb >= t0; tb -= TB) {
         // stage
         float dkeep[NI][4];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int e = tid + 256 * i, r = e / VPR;
+            const int e = st + 256 * i, r = e / VPR;
             if (e < ITEMS) {
                 const float4 xv = widen4(tok[i].x), dv = widen4(tok[i].dt), yv = tok[i].dy.v;
                 const float4 zv = widen4(tok[i].z);
@@ -342,7 +331,7 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
                 for (int j = 0; j < 4; ++j) {
                     const float rw = (&dv.x)[j] + bias[j];
                     float d = g.softplus ? softplus_f(rw) : rw;
-                    if (tb + r >= t1) d = 0.f;
+                    if (tb + TB > t1 && tb + r >= t1) d = 0.f;
                     dkeep[i][j] = d;
                     u[j] = d * (&xv.x)[j];
                     p[j] = (&yv.x)[j];
@@ -356,81 +345,180 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
         }
 #pragma unroll
         for (int k = 0; k < NBC; ++k) {
-            const int e = tid + 256 * k;
-            if (e < 2 * BC) reinterpret_cast<float4 *>(&sbc[0][0][0])[e] = widen4(rbc[k]);
+            const int eb = tid + 256 * k, ec = 255 - tid + 256 * k;
+            if (eb < BC) reinterpret_cast<float4 *>(&sbc[0][0][0])[eb] = widen4(rb[k]);
+            if (ec < BC) reinterpret_cast<float4 *>(&sbc[1][0][0])[ec] = widen4(rc[k]);
         }
         // the previous tile's loads, in flight during this one's arithmetic
         const int64_t tp = tb - TB;
         Tok ntok[NI];
-        Raw4<Tio> nbc[NBC];
 #pragma unroll
         for (int i = 0; i < NI; ++i) ntok[i] = load_tok(tp, i);
 #pragma unroll
-        for (int k = 0; k < NBC; ++k) nbc[k] = load_bc(tp, k);
+        for (int k = 0; k < NBC; ++k) {
+            rb[k] = load_bc(B, tp, tid + 256 * k);
+            rc[k] = load_bc(C, tp, 255 - tid + 256 * k);
+        }
         lds_barrier();
 
-        // the tile's states
-        float H[TB][4];
-        float keep = 0.f;
+        // the tile's states; a token's operands are loaded two tokens ahead and
+        // its exponentials taken one ahead, and no earlier (registers)
+        struct Op {
+            float2 w;
+            float p, bv[KS], cv[KS];
+        };
+        float H[TB][KS];
+        {
+            auto load_op = [&](int t, Op &o) {
+                o.w = sdu[t][cl];
+                load_ks(&sbc[0][t][KS * s], o.bv);
+                if constexpr (GATE) load_ks(&sbc[1][t][KS * s], o.cv);
+            };
+            Op op[2];
+            float a[KS], an[KS];
+            load_op(0, op[0]);
+            load_op(1, op[1]);
 #pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            const float2 w = sdu[t][cl];
-            const float4 bv = *reinterpret_cast<const float4 *>(&sbc[0][t][4 * s]);
+            for (int i = 0; i < KS; ++i) a[i] = fast_exp2(op[0].w.x * a2[i]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float prev = t ? H[t ? t - 1 : 0][i] : (&h0.x)[i];
-                H[t][i] = fmaf(fast_exp2(w.x * a2[i]), prev, w.y * (&bv.x)[i]);
+            for (int tq = 0; tq < TB; tq += S) {
+                float y[S];
+#pragma unroll
+                for (int k = 0; k < S; ++k) {
+                    const int t = tq + k;
+                    const Op cur = op[t & 1];
+                    if (t + 2 < TB) load_op(t + 2, op[t & 1]);
+                    if (t + 1 < TB) {
+#pragma unroll
+                        for (int i = 0; i < KS; ++i)
+                            an[i] = fast_exp2(op[(t + 1) & 1].w.x * a2[i]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+                        H[t][i] = fmaf(a[i], t ? H[t ? t - 1 : 0][i] : h0[i], cur.w.y * cur.bv[i]);
+                    if constexpr (GATE) {
+                        y[k] = H[t][0] * cur.cv[0];
+#pragma unroll
+                        for (int i = 1; i < KS; ++i) y[k] = fmaf(H[t][i], cur.cv[i], y[k]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) a[i] = an[i];
+                }
+                if constexpr (GATE) sy[tq + s][cl] = lane_sums<S>(y, s);
             }
-            if constexpr (GATE) {
-                const float4 cv = *reinterpret_cast<const float4 *>(&sbc[1][t][4 * s]);
-                const float p = chan_sum<S>(H[t][0] * cv.x + H[t][1] * cv.y + H[t][2] * cv.z +
-                                            H[t][3] * cv.w);
-                if (s == t % S) keep = p;
-                if ((t + 1) % S == 0) sy[t - (S - 1) + s][cl] = keep;
-            }
-            // (keeps the scheduler from loading every token's operands at once)
-            if ((t & 3) == 3) __builtin_amdgcn_sched_barrier(0);
         }
-        // and backwards
-        float dAt[4] = {};
-        float2 kgd = make_float2(0.f, 0.f);
+        // and backwards (the operands are read from LDS again: kept in
+        // registers from the first walk they would halve the wavefronts)
+        float dAt[KS] = {};
+        int cr = cl, sr = KS * s;
+        asm volatile("" : "+v"(cr), "+v"(sr));
+        // Sums over the wavefront's channels (dB, dC) through LDS: every lane
+        // writes its 2 KS products, then adds up one value (RV of them) of one
+        // token over the channels.  The values are read after a batch of RT
+        // tokens and added during the next.
+        const int wl = lane / S;   // channel in the wavefront
+        // (every other channel, or pair for N 8, has dB and dC exchanged in its
+        // row: the lanes that write together then meet different banks)
+        const int wx = N == 16 ? (wl & 1) * N : (N == 8 ? (wl >> 1 & 1) * N : 0);
+        const int rj = RV * lane % (2 * N), rt = RV * lane / (2 * N) % RT;   // value, token
+        const int rc = N == 8 ? lane >> 5 : 0;                          // half of the channels
+        float rr[RC][RV];
+        auto red_read = [&] {
 #pragma unroll
-        for (int t = TB - 1; t >= 0; --t) {
-            const float2 w = sdu[t][cl];
-            const float p = sdy[t][cl];
-            const float4 bv = *reinterpret_cast<const float4 *>(&sbc[0][t][4 * s]);
-            const float4 cv = *reinterpret_cast<const float4 *>(&sbc[1][t][4 * s]);
-            float v[8], gb = 0.f, qa = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float gi = fmaf(p, (&cv.x)[i], car[i]);
-                v[i] = gi * w.y;
-                v[4 + i] = p * H[t][i];
-                gb = fmaf(gi, (&bv.x)[i], gb);
-                car[i] = gi * fast_exp2(w.x * a2[i]);
-                const float q = car[i] * (t ? H[t ? t - 1 : 0][i] : (&h0.x)[i]);
-                qa = fmaf(q, a2[i], qa);
-                dAt[i] = fmaf(q, w.x, dAt[i]);
+            for (int i = 0; i < RC; ++i) {
+                const int x = N == 16 ? (i & 1) * N : (N == 8 ? (i >> 1 & 1) * N : 0);
+                const float *p = &sred[wave][rt][(rc * RC + i) * 2 * N + (rj ^ x)];
+                if constexpr (RV == 1)
+                    rr[i][0] = *p;
+                else
+                    load_ks(p, rr[i]);
             }
-            gb = chan_sum<S>(gb);
-            qa = chan_sum<S>(qa);
-            if (s == t % S) kgd = make_float2(gb, qa);
-            if (t % S == 0) sgd[t + s][cl] = kgd;
-            const float2 r = channels_sum<S>(v);
-            if ((lane & 15) < S)
-                *reinterpret_cast<float2 *>(
-                    &sdbc[wave][t][(lane >> 5) * N + 4 * s + 2 * ((lane >> 4) & 1)]) = r;
-            if ((t & 1) == 0) __builtin_amdgcn_sched_barrier(0);
-        }
+        };
+        auto red_add = [&](int t) {   // of the batch whose first token is t
+            float o[RV];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dA[i] += dAt[i];
-        h0 = load_h0(tp);
+            for (int q = 0; q < RV; ++q) {
+#pragma unroll
+                for (int w = 1; w < RC; w *= 2)
+#pragma unroll
+                    for (int i = 0; i + w < RC; i += 2 * w) rr[i][q] += rr[i + w][q];
+                o[q] = rr[0][q];
+                if constexpr (N == 8) o[q] += __shfl_xor(o[q], 32, 64);
+            }
+            if constexpr (RV == 1)
+                sdbc[wave][t + rt][rj] = o[0];
+            else
+                store_ks(&sdbc[wave][t + rt][rj], o);
+        };
+        {
+            auto load_op = [&](int t, Op &o) {
+                o.w = sdu[t][cr];
+                o.p = sdy[t][cr];
+                load_ks(&sbc[0][t][sr], o.bv);
+                load_ks(&sbc[1][t][sr], o.cv);
+            };
+            Op op[2];
+            float a[KS], an[KS];
+            load_op(TB - 1, op[1]);
+            load_op(TB - 2, op[0]);
+#pragma unroll
+            for (int i = 0; i < KS; ++i) a[i] = fast_exp2(op[1].w.x * a2[i]);
+#pragma unroll
+            for (int tq = TB - S; tq >= 0; tq -= S) {
+                float pg[S], pq[S];
+#pragma unroll
+                for (int k = S - 1; k >= 0; --k) {
+                    const int t = tq + k;
+                    const Op cur = op[t & 1];
+                    if (t > 1) load_op(t - 2, op[t & 1]);
+                    if (t > 0) {
+#pragma unroll
+                        for (int i = 0; i < KS; ++i)
+                            an[i] = fast_exp2(op[(t - 1) & 1].w.x * a2[i]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    float vb[KS], vc[KS], g1, q1;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        const float gi = fmaf(cur.p, cur.cv[i], car[i]);
+                        vb[i] = gi * cur.w.y;
+                        vc[i] = cur.p * H[t][i];
+                        g1 = i ? fmaf(gi, cur.bv[i], g1) : gi * cur.bv[i];
+                        car[i] = gi * a[i];
+                        const float q = car[i] * (t ? H[t ? t - 1 : 0][i] : h0[i]);
+                        q1 = i ? fmaf(q, a2[i], q1) : q * a2[i];
+                        dAt[i] = fmaf(q, cur.w.x, dAt[i]);
+                    }
+                    pg[k] = g1;
+                    pq[k] = q1;
+                    // (pinned here: else the sums are put off and hold their terms in registers)
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(dAt[i]), "+v"(car[i]));
+                    asm volatile("" : "+v"(pg[k]), "+v"(pq[k]));
+                    if (RT == 1 ? t < TB - 1 : t % 2 == 1 && t < TB - 2) red_add(t + 1);
+                    float *to = &sred[wave][RT == 1 ? 0 : t % 2][wl * 2 * N + KS * s];
+                    store_ks(to + wx, vb);
+                    store_ks(to + (wx ^ N), vc);
+                    if (t % RT == 0) red_read();
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) a[i] = an[i];
+                }
+                sgd[tq + s][cl] = make_float2(lane_sums<S>(pg, s), lane_sums<S>(pq, s));
+            }
+        }
+        red_add(0);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) dA[i] += dAt[i];
+        load_h0(tp, h0);
         lds_barrier();
 
         // per-channel outputs
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int e = tid + 256 * i, r = e / VPR;
+            const int e = st + 256 * i, r = e / VPR;
             const int64_t t = tb + r;
             if (e < ITEMS && t < t1 && chn > 0) {
                 const float4 xv = widen4(tok[i].x), dv = widen4(tok[i].dt), yv = tok[i].dy.v;
@@ -459,48 +547,38 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
                     accD[j] = fmaf(p, xj, accD[j]);
                     accb[j] += dd;
                 }
-                const int64_t o = (b * g.T + t) * g.Dm + ch0;
-                store4<RAG>(dx + o, make_float4(ox[0], ox[1], ox[2], ox[3]), chn);
-                store4<RAG>(ddt + o, make_float4(od[0], od[1], od[2], od[3]), chn);
-                if constexpr (GATE)
-                    store4<RAG>(dz + o, make_float4(oz[0], oz[1], oz[2], oz[3]), chn);
+                store_one(dx, tb, i, make_float4(ox[0], ox[1], ox[2], ox[3]));
+                store_one(ddt, tb, i, make_float4(od[0], od[1], od[2], od[3]));
+                if constexpr (GATE) store_one(dz, tb, i, make_float4(oz[0], oz[1], oz[2], oz[3]));
             }
         }
         // dB and dC of this channel block
+        const auto rp = tile_rsrc(pbc, ((int64_t)cb * g.Bt + b) * g.T + tb, left(tb), 2 * N);
         for (int e = tid; e < TB * N / 2; e += 256) {
             const int r = e / (N / 2), o = 4 * (e % (N / 2));
-            if (tb + r < t1) {
-                float4 v[4];
+            float4 v[4];
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    v[w] = *reinterpret_cast<const float4 *>(&sdbc[w][r][o]);
-                float4 q;
-                q.x = (v[0].x + v[1].x) + (v[2].x + v[3].x);
-                q.y = (v[0].y + v[1].y) + (v[2].y + v[3].y);
-                q.z = (v[0].z + v[1].z) + (v[2].z + v[3].z);
-                q.w = (v[0].w + v[1].w) + (v[2].w + v[3].w);
-                *reinterpret_cast<float4 *>(pbc + ((cb * g.Bt + b) * g.T + tb + r) * (2 * N) + o) =
-                    q;
-            }
+            for (int w = 0; w < 4; ++w) v[w] = *reinterpret_cast<const float4 *>(&sdbc[w][r][o]);
+            float4 q;
+            q.x = (v[0].x + v[1].x) + (v[2].x + v[3].x);
+            q.y = (v[0].y + v[1].y) + (v[2].y + v[3].y);
+            q.z = (v[0].z + v[1].z) + (v[2].z + v[3].z);
+            q.w = (v[0].w + v[1].w) + (v[2].w + v[3].w);
+            store_buf(rp, (uint32_t)e * 16u, q, 0.f);
         }
 #pragma unroll
         for (int i = 0; i < NI; ++i) tok[i] = ntok[i];
-#pragma unroll
-        for (int k = 0; k < NBC; ++k) rbc[k] = nbc[k];
     }
 
     if (c < g.Dm) {
-        *reinterpret_cast<float4 *>(pA + ((int64_t)rest * g.Dm + c) * N + 4 * s) =
-            make_float4(dA[0], dA[1], dA[2], dA[3]);
-        if (dinit && seg == 0)
-            *reinterpret_cast<float4 *>(dinit + (b * g.Dm + c) * N + 4 * s) =
-                make_float4(car[0], car[1], car[2], car[3]);
+        store_ks(pA + ((int64_t)rest * g.Dm + c) * N + KS * s, dA);
+        if (dinit && seg == 0) store_ks(dinit + (b * g.Dm + c) * N + KS * s, car);
     }
     // sums over this block's token rows
     __syncthreads();
     float(*red)[CB] = reinterpret_cast<float(*)[CB]>(&sdu[0][0]);   // [2 ROWS][CB]
-    if (tid < ROWS * VPR) {
-        const int r = tid / VPR;
+    if (st < ROWS * VPR) {
+        const int r = st / VPR;
         *reinterpret_cast<float4 *>(&red[r][4 * sv]) =
             make_float4(accD[0], accD[1], accD[2], accD[3]);
         *reinterpret_cast<float4 *>(&red[ROWS + r][4 * sv]) =
@@ -561,15 +639,20 @@ __global__ __launch_bounds__(256) void sel_sum_kernel(SumJobs jobs) {
     }
 }
 
+// States per lane of the reverse pass: its 16 tokens' states and their sums
+// over channels take 20 registers per state.
+constexpr int main_ks(int) { return 4; }
+
 struct BwdPlan {
-    int64_t nseg, seg_len;
+    int64_t nseg, seg_len, ncb;   // ncb: channel blocks of the reverse pass
     // float offsets into the workspace
     size_t ckpt, cumd, hseg, adj, dsum, pbc, pA, pD, pbias, total;
 };
 BwdPlan plan(const SelArgs &a) {
     BwdPlan p;
     const int64_t tile = a.N > TB ? a.N : TB;
-    const int64_t ncb = chan_blocks(a), blocks = a.Bt * ncb;
+    const int64_t ncb = chan_blocks(a, main_ks(a.N)), blocks = a.Bt * ncb;
+    p.ncb = ncb;
     p.nseg = 1;
     p.seg_len = cdiv64(a.T > 0 ? a.T : 1, tile) * tile;
     if (blocks > 0 && blocks < 512) {
@@ -618,6 +701,8 @@ hipError_t launch_selective_scan_bwd(const SelArgs &a, hipStream_t st) {
     g.nseg = (int32_t)p.nseg;
     g.seg_len = p.seg_len;
     g.softplus = a.softplus ? 1 : 0;
+    SelGeom gm = g;   // of the reverse pass
+    gm.ncb = (int32_t)p.ncb;
     const bool rag = a.Dm % 4 != 0, split = p.nseg > 1;
     const int64_t rows = a.Bt * p.nseg;
     hipError_t e;
@@ -657,14 +742,15 @@ hipError_t launch_selective_scan_bwd(const SelArgs &a, hipStream_t st) {
             typedef decltype(io) Tio;
             by_flag(rag, [&](auto r) {
                 by_flag(a.z != nullptr, [&](auto gate) {
-                    sel_bwd_kernel<decltype(n)::value, Tio, decltype(gate)::value,
+                    constexpr int N = decltype(n)::value;
+                    sel_bwd_kernel<N, main_ks(N), Tio, decltype(gate)::value,
                                    decltype(r)::value>
-                        <<<dim3((uint32_t)(rows * g.ncb)), 256, 0, st>>>(
+                        <<<dim3((uint32_t)(rows * p.ncb)), 256, 0, st>>>(
                             (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B,
                             (const Tio *)a.C, a.D, (const Tio *)a.z, a.dt_bias, a.dy,
                             split ? ws + p.adj : a.dfinal, ws + p.ckpt, ws + p.cumd, ws + p.hseg,
                             a.dx, a.ddt, a.dz, a.dinit, ws + p.pbc, ws + p.pA, ws + p.pD,
-                            ws + p.pbias, g);
+                            ws + p.pbias, gm);
                 });
             });
         });
@@ -674,7 +760,7 @@ hipError_t launch_selective_scan_bwd(const SelArgs &a, hipStream_t st) {
     auto job = [&](const float *part, int64_t count, int64_t np, float *o0, float *o1, int half) {
         return SumJob{part, count, np, o0, o1, half, (uint32_t)cdiv64(count, 64)};
     };
-    jobs.j[0] = job(ws + p.pbc, a.Bt * a.T * 2 * a.N, g.ncb, a.dB, a.dC, a.N);
+    jobs.j[0] = job(ws + p.pbc, a.Bt * a.T * 2 * a.N, p.ncb, a.dB, a.dC, a.N);
     jobs.j[1] = job(ws + p.pA, a.Dm * a.N, rows, a.dA, nullptr, 0);
     jobs.j[2] = job(ws + p.pD, a.Dm, rows, a.dD, nullptr, 0);
     jobs.j[3] = job(ws + p.pbias, a.Dm, rows, a.dbias, nullptr, 0);
