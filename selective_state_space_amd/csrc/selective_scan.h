@@ -101,20 +101,30 @@ __device__ __forceinline__ void store4(uint16_t *p, float4 v, int n) {
     }
 }
 
-// log(1 + e^r) = max(r, 0) + log(1 + e^-|r|); above 20 that is r in float32.
-// e^-|r| as a power of two with the argument's rounding put back; log(1 + e)
-// with the rounding of 1 + e put back (1 - e/2 stands for 1 / (1 + e): the
-// term matters where e is small), so small results keep their relative
-// accuracy.
-__device__ __forceinline__ float softplus_f(float r) {
-    constexpr float kLog2eLo = 1.9259629911266175e-8f;   // log2(e) - (float)log2(e)
+// d = log(1 + e^r) = max(r, 0) + log(1 + e^-|r|); above 20 that is r in
+// float32.  e^-|r| as a power of two (of hi, with the rest of the argument put
+// back to first order), and log(1 + e) with the rounding of 1 + e put back, so
+// small results keep their relative accuracy.  The maxima let NaN through, and
+// keep -inf out of the products.  w = 1 + e, for the derivative below.
+__device__ __forceinline__ float softplus_f(float r, float &e, float &w) {
+    r = __builtin_elementwise_maximum(r, -126.f);
     const float q = -fabsf(r), hi = q * kLog2e;
-    const float lo = fmaf(q, kLog2eLo, fmaf(q, kLog2e, -hi));
-    float e = fast_exp2(hi);
-    e = fmaf(e, e > 0.f ? lo * kLn2 : 0.f, e);
-    const float w = 1.f + e;
-    const float l = __builtin_amdgcn_logf(w) * kLn2;
-    return fmaxf(r, 0.f) + fmaf(e - (w - 1.f), fmaf(e, -0.5f, 1.f), l);
+    e = fast_exp2(hi);
+    e = fmaf(e, fmaf(hi, -kLn2, q), e);
+    w = 1.f + e;
+    return __builtin_elementwise_maximum(r, 0.f) +
+           fmaf(__builtin_amdgcn_logf(w), kLn2, e - (w - 1.f));
+}
+__device__ __forceinline__ float softplus_f(float r) {
+    float e, w;
+    return softplus_f(r, e, w);
+}
+// d and its derivative sigmoid(r)
+__device__ __forceinline__ float softplus_f(float r, float &slope) {
+    float e, w;
+    const float d = softplus_f(r, e, w);
+    slope = (r < 0.f ? e : 1.f) * __builtin_amdgcn_rcpf(w);
+    return d;
 }
 __device__ __forceinline__ float sigmoid_f(float v) {
     return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * v));
@@ -389,7 +399,7 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(
         // scan the tile
         constexpr int U = TL < 32 ? TL : 32;   // tokens unrolled
 #pragma unroll 1
-        for (int tq = 0; tq < TL; tq += U) {
+        for (int tq = 0; tq < TL && tb + tq < te; tq += U) {
 #pragma unroll
             for (int k0 = 0; k0 < U; k0 += S) {
                 float p[S];

@@ -45,23 +45,17 @@ struct BTile {
     static constexpr int BC = TB * N / 4;                        // 4-element vectors of B (or C)
 };
 
-// silu(z) and its derivative
-__device__ __forceinline__ void silu_grad(float z, float &f, float &df) {
-    const float s = sigmoid_f(z);
-    f = z * s;
-    df = s * (1.f + z * (1.f - s));
-}
-
 // The adjoint leaving a segment at its first token, started from zero after
 // its last one (segments 1 .. nseg-1).
-template <int N, typename Tio, bool GATE, bool RAG>
+template <int N, int KS, typename Tio, bool GATE, bool RAG>
 __global__ __launch_bounds__(256) void sel_adj_kernel(
     const Tio *__restrict__ dt, const float *__restrict__ A, const Tio *__restrict__ C,
     const Tio *__restrict__ z, const float *__restrict__ dt_bias, const float *__restrict__ dy,
     float *__restrict__ adj, SelGeom g) {
-    constexpr int S = SelSplit<N, 4>::S, CPW = SelSplit<N, 4>::CPW, CB = SelSplit<N, 4>::CB;
-    constexpr int VPR = BTile<N, 4>::VPR, NI = BTile<N, 4>::NI, ITEMS = BTile<N, 4>::ITEMS;
-    constexpr int BC = BTile<N, 4>::BC;
+    typedef SelSplit<N, KS> Sp;
+    typedef BTile<N, KS> Bt;
+    constexpr int S = Sp::S, CPW = Sp::CPW, CB = Sp::CB;
+    constexpr int VPR = Bt::VPR, NI = Bt::NI, ITEMS = Bt::ITEMS, BC = Bt::BC;
     __shared__ __align__(16) float2 sdy[TB][CB];   // (d, dyp)
     __shared__ __align__(16) float sc[TB][N];
     const int tid = threadIdx.x;
@@ -79,13 +73,11 @@ __global__ __launch_bounds__(256) void sel_adj_kernel(
     const int lane = tid & 63, wave = tid >> 6;
     const int s = lane % S, cl = wave * CPW + lane / S;
     const int32_t c = cb * CB + cl;
-    float a2[4] = {}, car[4] = {};
+    float a2[KS] = {}, car[KS] = {};
     if (c < g.Dm) {
-        const float4 av = *reinterpret_cast<const float4 *>(A + (int64_t)c * N + 4 * s);
-        a2[0] = av.x * kLog2e;
-        a2[1] = av.y * kLog2e;
-        a2[2] = av.z * kLog2e;
-        a2[3] = av.w * kLog2e;
+        load_ks(A + (int64_t)c * N + KS * s, a2);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) a2[i] *= kLog2e;
     }
     const int64_t ntile = (t1 - t0 + TB - 1) / TB;
     for (int64_t k = ntile - 1; k >= 0; --k) {
@@ -125,17 +117,16 @@ __global__ __launch_bounds__(256) void sel_adj_kernel(
 #pragma unroll
         for (int t = TB - 1; t >= 0; --t) {
             const float2 w = sdy[t][cl];
-            const float4 cv = *reinterpret_cast<const float4 *>(&sc[t][4 * s]);
-            car[0] = fast_exp2(w.x * a2[0]) * fmaf(w.y, cv.x, car[0]);
-            car[1] = fast_exp2(w.x * a2[1]) * fmaf(w.y, cv.y, car[1]);
-            car[2] = fast_exp2(w.x * a2[2]) * fmaf(w.y, cv.z, car[2]);
-            car[3] = fast_exp2(w.x * a2[3]) * fmaf(w.y, cv.w, car[3]);
+            float cv[KS];
+            load_ks(&sc[t][KS * s], cv);
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+                car[i] = fast_exp2(w.x * a2[i]) * fmaf(w.y, cv[i], car[i]);
         }
         lds_barrier();
     }
     if (c < g.Dm)
-        *reinterpret_cast<float4 *>(adj + (((b * g.nseg) + seg) * g.Dm + c) * N + 4 * s) =
-            make_float4(car[0], car[1], car[2], car[3]);
+        store_ks(adj + (((b * g.nseg) + seg) * g.Dm + c) * N + KS * s, car);
 }
 
 // Both chains over the segments: the states entering each (hseg, in place of
@@ -206,6 +197,8 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
     __shared__ __align__(16) float2 sgd[TB][CB];          // (gB, sum q a2)
     __shared__ __align__(16) float sy[GATE ? TB : 1][GATE ? CB : 4];
     __shared__ __align__(16) float sdbc[4][TB][2 * N];
+    __shared__ __align__(16) float ssp[TB][CB];                        // softplus'
+    __shared__ __align__(16) float ssz[GATE ? TB : 1][GATE ? CB : 4];   // sigmoid(z)
     // the products summed over a wavefront's channels: RT tokens of [channel][dB, dC]
     constexpr int RT = N <= 16 ? 2 : 1;
     constexpr int RV = N <= 32 ? 1 : 2;                       // values per summing lane
@@ -326,17 +319,25 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
             if (e < ITEMS) {
                 const float4 xv = widen4(tok[i].x), dv = widen4(tok[i].dt), yv = tok[i].dy.v;
                 const float4 zv = widen4(tok[i].z);
-                float u[4], p[4];
+                float u[4], p[4], sp[4], sz[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float rw = (&dv.x)[j] + bias[j];
-                    float d = g.softplus ? softplus_f(rw) : rw;
+                    sp[j] = 1.f;
+                    float d = g.softplus ? softplus_f(rw, sp[j]) : rw;
                     if (tb + TB > t1 && tb + r >= t1) d = 0.f;
                     dkeep[i][j] = d;
                     u[j] = d * (&xv.x)[j];
                     p[j] = (&yv.x)[j];
-                    if constexpr (GATE) p[j] *= fast_silu((&zv.x)[j]);
+                    if constexpr (GATE) {
+                        sz[j] = sigmoid_f((&zv.x)[j]);
+                        p[j] *= (&zv.x)[j] * sz[j];
+                    }
                 }
+                *reinterpret_cast<float4 *>(&ssp[r][4 * sv]) = make_float4(sp[0], sp[1], sp[2], sp[3]);
+                if constexpr (GATE)
+                    *reinterpret_cast<float4 *>(&ssz[r][4 * sv]) =
+                        make_float4(sz[0], sz[1], sz[2], sz[3]);
                 float4 *w = reinterpret_cast<float4 *>(&sdu[r][4 * sv]);
                 w[0] = make_float4(dkeep[i][0], u[0], dkeep[i][1], u[1]);
                 w[1] = make_float4(dkeep[i][2], u[2], dkeep[i][3], u[3]);
@@ -521,31 +522,32 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
             const int e = st + 256 * i, r = e / VPR;
             const int64_t t = tb + r;
             if (e < ITEMS && t < t1 && chn > 0) {
-                const float4 xv = widen4(tok[i].x), dv = widen4(tok[i].dt), yv = tok[i].dy.v;
+                const float4 xv = widen4(tok[i].x), yv = tok[i].dy.v;
                 const float4 zv = widen4(tok[i].z);
                 const float4 *w = reinterpret_cast<const float4 *>(&sgd[r][4 * sv]);
                 const float4 w0 = w[0], w1 = w[1];
                 const float gb[4] = {w0.x, w0.z, w1.x, w1.z}, qa[4] = {w0.y, w0.w, w1.y, w1.w};
-                float4 ys = make_float4(0.f, 0.f, 0.f, 0.f);
-                if constexpr (GATE) ys = *reinterpret_cast<const float4 *>(&sy[r][4 * sv]);
+                const float4 sp = *reinterpret_cast<const float4 *>(&ssp[r][4 * sv]);
+                const float4 pv = *reinterpret_cast<const float4 *>(&sdy[r][4 * sv]);
+                float4 ys = make_float4(0.f, 0.f, 0.f, 0.f), sz = ys;
+                if constexpr (GATE) {
+                    ys = *reinterpret_cast<const float4 *>(&sy[r][4 * sv]);
+                    sz = *reinterpret_cast<const float4 *>(&ssz[r][4 * sv]);
+                }
                 float ox[4], od[4], oz[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float xj = (&xv.x)[j], dyj = (&yv.x)[j];
-                    float p = dyj;
+                    const float xj = (&xv.x)[j], p = (&pv.x)[j];
                     if constexpr (GATE) {
-                        float f, df;
-                        silu_grad((&zv.x)[j], f, df);
-                        p *= f;
-                        oz[j] = dyj * ((&ys.x)[j] + Dv[j] * xj) * df;
+                        // silu' = s (1 + z (1 - s))
+                        const float s = (&sz.x)[j], zj = (&zv.x)[j];
+                        oz[j] = (&yv.x)[j] * ((&ys.x)[j] + Dv[j] * xj) *
+                                (s * fmaf(zj, 1.f - s, 1.f));
                     }
                     ox[j] = fmaf(dkeep[i][j], gb[j], Dv[j] * p);
-                    float dd = fmaf(xj, gb[j], qa[j] * kLn2);
-                    const float rw = (&dv.x)[j] + bias[j];
-                    if (g.softplus && rw <= 20.f) dd *= sigmoid_f(rw);
-                    od[j] = dd;
+                    od[j] = fmaf(xj, gb[j], qa[j] * kLn2) * (&sp.x)[j];
                     accD[j] = fmaf(p, xj, accD[j]);
-                    accb[j] += dd;
+                    accb[j] += od[j];
                 }
                 store_one(dx, tb, i, make_float4(ox[0], ox[1], ox[2], ox[3]));
                 store_one(ddt, tb, i, make_float4(od[0], od[1], od[2], od[3]));
@@ -639,30 +641,38 @@ __global__ __launch_bounds__(256) void sel_sum_kernel(SumJobs jobs) {
     }
 }
 
-// States per lane of the reverse pass: its 16 tokens' states and their sums
-// over channels take 20 registers per state.
-constexpr int main_ks(int) { return 4; }
-
+// How a launch is cut.  The reverse pass keeps 16 tokens' states in registers,
+// so 2 workgroups of 4 states per lane fill a CU, 512 the chip.  Whole
+// sequences take ceil(workgroups / 512) rounds; in segments the rounds even out
+// at the price of a second pass over the tokens, about a third of the work:
+// segments of at least 32 tokens, enough for 2048 workgroups, where the rounds
+// waste more than that (8 x 1024 tokens, 5120 channels, 640 workgroups: 872 us
+// in segments, 958 us whole; 16 x 512 x 2048, 512 workgroups: 372 and 326 us; 4
+// x 2048 x 2048, 128 workgroups: 382 and 925 us).  Where segments still leave
+// CUs without 2 workgroups, 2 states per lane shorten each wavefront's walk.
+// (N 8 with 4 states per lane would spill registers)
+constexpr int bwd_most_ks(int N) { return N == 8 ? 2 : 4; }
 struct BwdPlan {
-    int64_t nseg, seg_len, ncb;   // ncb: channel blocks of the reverse pass
+    int ks;
+    int64_t nseg, seg_len, ncb;
     // float offsets into the workspace
     size_t ckpt, cumd, hseg, adj, dsum, pbc, pA, pD, pbias, total;
 };
 BwdPlan plan(const SelArgs &a) {
     BwdPlan p;
-    const int64_t tile = a.N > TB ? a.N : TB;
-    const int64_t ncb = chan_blocks(a, main_ks(a.N)), blocks = a.Bt * ncb;
-    p.ncb = ncb;
-    p.nseg = 1;
-    p.seg_len = cdiv64(a.T > 0 ? a.T : 1, tile) * tile;
-    if (blocks > 0 && blocks < 512) {
-        int64_t n = cdiv64(1024, blocks);
-        n = n < a.T / 64 ? n : a.T / 64;
-        if (n >= 2) {
-            p.seg_len = cdiv64(cdiv64(a.T, n), tile) * tile;
-            p.nseg = cdiv64(a.T, p.seg_len);
-        }
+    const int most = bwd_most_ks(a.N);
+    const int64_t blocks = a.Bt * chan_blocks(a, most);
+    int64_t n = 1;
+    if (10 * cdiv64(blocks, 512) * 512 > 13 * blocks && blocks > 0) {
+        n = cdiv64(2048, blocks);
+        n = n < a.T / 32 ? n : a.T / 32;
+        if (n < 1) n = 1;
     }
+    p.ks = a.N < 64 && blocks * n < 512 ? 2 : most;
+    p.ncb = chan_blocks(a, p.ks);
+    p.seg_len = cdiv64(cdiv64(a.T > 0 ? a.T : 1, n), TB) * TB;
+    p.nseg = n > 1 ? cdiv64(a.T, p.seg_len) : 1;
+    const int64_t ncb = p.ncb;
     const size_t st = (size_t)a.Bt * a.Dm * a.N, ch = (size_t)a.Bt * a.Dm;
     const size_t nt = (size_t)cdiv64(a.T, TB), ns = p.nseg;
     size_t o = 0;
@@ -697,38 +707,44 @@ hipError_t launch_selective_scan_bwd(const SelArgs &a, hipStream_t st) {
     g.T = a.T;
     g.Bt = a.Bt;
     g.Dm = (int32_t)a.Dm;
-    g.ncb = (int32_t)chan_blocks(a);
+    g.ncb = (int32_t)p.ncb;
     g.nseg = (int32_t)p.nseg;
     g.seg_len = p.seg_len;
     g.softplus = a.softplus ? 1 : 0;
-    SelGeom gm = g;   // of the reverse pass
-    gm.ncb = (int32_t)p.ncb;
     const bool rag = a.Dm % 4 != 0, split = p.nseg > 1;
     const int64_t rows = a.Bt * p.nseg;
     hipError_t e;
     if (a.Bt > 0) {
-        by_state(a, [&](auto n, auto io) {
+        // f(N, KS, io type, RAG)
+        auto each = [&](auto f) {
+            by_state(a, [&](auto n, auto io) {
+                by_flag(rag, [&](auto r) {
+                    constexpr int N = decltype(n)::value;
+                    if constexpr (N < 64 && bwd_most_ks(N) > 2)
+                        if (p.ks == 2) return f(n, std::integral_constant<int, 2>(), io, r);
+                    f(n, std::integral_constant<int, bwd_most_ks(N)>(), io, r);
+                });
+            });
+        };
+        each([&](auto n, auto ks, auto io, auto r) {
             typedef decltype(io) Tio;
-            by_flag(rag, [&](auto r) {
-                sel_scan_kernel<decltype(n)::value, 4, Tio, float, false, decltype(r)::value,
-                                SCAN_CKPT><<<dim3((uint32_t)(rows * g.ncb)), 256, 0, st>>>(
+            sel_scan_kernel<decltype(n)::value, decltype(ks)::value, Tio, float, false,
+                            decltype(r)::value, SCAN_CKPT>
+                <<<dim3((uint32_t)(rows * g.ncb)), 256, 0, st>>>(
                     (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B, nullptr, nullptr,
                     nullptr, a.dt_bias, split ? nullptr : a.init, nullptr, nullptr, ws + p.hseg,
                     ws + p.dsum, ws + p.ckpt, ws + p.cumd, g);
-            });
         });
         if ((e = hipGetLastError()) != hipSuccess) return e;
         if (split) {
-            by_state(a, [&](auto n, auto io) {
+            each([&](auto n, auto ks, auto io, auto r) {
                 typedef decltype(io) Tio;
-                by_flag(rag, [&](auto r) {
-                    by_flag(a.z != nullptr, [&](auto gate) {
-                        sel_adj_kernel<decltype(n)::value, Tio, decltype(gate)::value,
-                                       decltype(r)::value>
-                            <<<dim3((uint32_t)(a.Bt * (p.nseg - 1) * g.ncb)), 256, 0, st>>>(
-                                (const Tio *)a.dt, a.A, (const Tio *)a.C, (const Tio *)a.z,
-                                a.dt_bias, a.dy, ws + p.adj, g);
-                    });
+                by_flag(a.z != nullptr, [&](auto gate) {
+                    sel_adj_kernel<decltype(n)::value, decltype(ks)::value, Tio,
+                                   decltype(gate)::value, decltype(r)::value>
+                        <<<dim3((uint32_t)(a.Bt * (p.nseg - 1) * g.ncb)), 256, 0, st>>>(
+                            (const Tio *)a.dt, a.A, (const Tio *)a.C, (const Tio *)a.z, a.dt_bias,
+                            a.dy, ws + p.adj, g);
                 });
             });
             if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -738,20 +754,17 @@ hipError_t launch_selective_scan_bwd(const SelArgs &a, hipStream_t st) {
                 (int32_t)a.Dm, (int32_t)a.N, (int32_t)p.nseg);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
-        by_state(a, [&](auto n, auto io) {
+        each([&](auto n, auto ks, auto io, auto r) {
             typedef decltype(io) Tio;
-            by_flag(rag, [&](auto r) {
-                by_flag(a.z != nullptr, [&](auto gate) {
-                    constexpr int N = decltype(n)::value;
-                    sel_bwd_kernel<N, main_ks(N), Tio, decltype(gate)::value,
-                                   decltype(r)::value>
-                        <<<dim3((uint32_t)(rows * p.ncb)), 256, 0, st>>>(
-                            (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B,
-                            (const Tio *)a.C, a.D, (const Tio *)a.z, a.dt_bias, a.dy,
-                            split ? ws + p.adj : a.dfinal, ws + p.ckpt, ws + p.cumd, ws + p.hseg,
-                            a.dx, a.ddt, a.dz, a.dinit, ws + p.pbc, ws + p.pA, ws + p.pD,
-                            ws + p.pbias, gm);
-                });
+            by_flag(a.z != nullptr, [&](auto gate) {
+                sel_bwd_kernel<decltype(n)::value, decltype(ks)::value, Tio,
+                               decltype(gate)::value, decltype(r)::value>
+                    <<<dim3((uint32_t)(rows * g.ncb)), 256, 0, st>>>(
+                        (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B,
+                        (const Tio *)a.C, a.D, (const Tio *)a.z, a.dt_bias, a.dy,
+                        split ? ws + p.adj : a.dfinal, ws + p.ckpt, ws + p.cumd, ws + p.hseg,
+                        a.dx, a.ddt, a.dz, a.dinit, ws + p.pbc, ws + p.pA, ws + p.pD,
+                        ws + p.pbias, g);
             });
         });
         if ((e = hipGetLastError()) != hipSuccess) return e;
