@@ -20,9 +20,11 @@ namespace ssd {
 
 namespace {
 
+constexpr int kVec = 4;   // channels of a lane
+
 // V consecutive elements as stored.  Rows of an odd width or a slice start at
 // any element, so the copies below assume element alignment only (the global
-// memory path takes unaligned 16-byte accesses).  RAG: n may be less than V.
+// memory path takes unaligned 8- and 16-byte accesses).  RAG: n may be less than V.
 template <typename T, int V>
 struct Vec {
     T v[V];
@@ -140,11 +142,12 @@ __device__ __forceinline__ void load_weights(const float *__restrict__ weight,
 // the sequence's length are written as zeros.  The first run also writes the
 // final state: it alone reads the initial state, so the two may be the same
 // memory.
-template <typename Tio, int V, int W, bool RAG>
+template <typename Tio, int W, bool RAG>
 __global__ __launch_bounds__(256) void conv1d_fwd_kernel(
     const Tio *__restrict__ x, const float *__restrict__ weight, const float *__restrict__ bias,
     const Tio *init, const int32_t *__restrict__ lens, Tio *__restrict__ y0,
     Tio *__restrict__ y1, Tio *__restrict__ y2, Tio *fin, ConvGeom g) {
+    constexpr int V = kVec;
     const int32_t b = blockIdx.x / (uint32_t)g.blk;
     const uint32_t idx = (blockIdx.x - (uint32_t)b * g.blk) * 256u + threadIdx.x;
     if (idx >= (uint32_t)g.nvec * (uint32_t)g.ntile) return;
@@ -234,11 +237,12 @@ __global__ __launch_bounds__(256) void conv1d_fwd_kernel(
 // the state moves up by one row in place.  A lane serves R sequences so that
 // its weights (as many bytes as a sequence's whole traffic) are read once for
 // all of them.
-template <typename Tio, int V, int W, int R, bool RAG>
+template <typename Tio, int W, int R, bool RAG>
 __global__ __launch_bounds__(256) void conv1d_step_kernel(
     Tio *__restrict__ state, const int32_t *__restrict__ slots, int64_t nslots,
     const Tio *__restrict__ x, const float *__restrict__ weight, const float *__restrict__ bias,
     Tio *__restrict__ y0, Tio *__restrict__ y1, Tio *__restrict__ y2, ConvGeom g) {
+    constexpr int V = kVec;
     const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
     const uint32_t grp = idx / (uint32_t)g.nvec;
     const int64_t b0 = (int64_t)grp * R;
@@ -304,7 +308,7 @@ __global__ __launch_bounds__(256) void conv1d_bwd_kernel(
     const Tio *__restrict__ init, const float *__restrict__ dy0, const float *__restrict__ dy1,
     const float *__restrict__ dy2, const float *__restrict__ dfinal, float *__restrict__ dx,
     float *__restrict__ dinit, float *__restrict__ part, ConvGeom g) {
-    constexpr int V = 4;
+    constexpr int V = kVec;
     __shared__ float red[4][(W + 1) * V][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t vb = blockIdx.x % (uint32_t)g.blk;
@@ -333,30 +337,37 @@ __global__ __launch_bounds__(256) void conv1d_bwd_kernel(
             widen(r, win[k]);
         }
         const int64_t send = t1 + W - 1;   // dp of tokens t0 .. send-1 (0 past T)
-        constexpr int U = 4;
-        for (int64_t s0 = t0; s0 < send; s0 += U) {
-            Vec<Tio, V> xr[U];
-            Vec<float, V> dr[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t s = s0 + u;
-                xr[u] = Vec<Tio, V>{};
-                dr[u] = Vec<float, V>{};
-                if (s < send && s < g.T) {
-                    xr[u] = load_vec<RAG, Tio, V>(xb + s * g.sxt, ci.n);
-                    dr[u] = load_vec<RAG, float, V>(dyb + s * ci.width, ci.n);
-                }
+        constexpr int U = 2;   // rows in flight ahead of the arithmetic
+        struct Row {
+            Vec<Tio, V> x;
+            Vec<float, V> dy;
+        };
+        const int64_t slast = min(send, g.T);   // (rows past T are zero)
+        auto load_row = [&](int64_t s) {
+            Row r = Row{};
+            if (s < slast) {
+                r.x = load_vec<RAG, Tio, V>(xb + s * g.sxt, ci.n);
+                r.dy = load_vec<RAG, float, V>(dyb + s * ci.width, ci.n);
             }
+            return r;
+        };
+        Row cur[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) cur[u] = load_row(t0 + u);
+        for (int64_t s0 = t0; s0 < send; s0 += U) {
+            Row nxt[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) nxt[u] = load_row(s0 + U + u);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t s = s0 + u;
                 if (s >= send) break;
                 float xv[V], out[V];
-                widen(xr[u], xv);
+                widen(cur[u].x, xv);
                 const bool own = s < t1;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    float dp = dr[u].v[i];
+                    float dp = cur[u].dy.v[i];
                     if (g.silu) {
                         float p = bs[i];
 #pragma unroll
@@ -400,6 +411,8 @@ __global__ __launch_bounds__(256) void conv1d_bwd_kernel(
                 else if (t < 0 && dinit)    // the first run: rows of the initial state
                     store_vec<RAG, float, V>(dinit + ((int64_t)b * (W - 1) + s) * g.C + ci.c, o, ci.n);
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) cur[u] = nxt[u];
         }
     }
 #pragma unroll
@@ -453,22 +466,22 @@ __global__ __launch_bounds__(256) void conv1d_bwd_reduce_kernel(const float *__r
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-int64_t vectors(const ConvArgs &a, int V) {
-    return cdiv(a.ch[0], V) + cdiv(a.ch[1], V) + cdiv(a.ch[2], V);
+int64_t vectors(const ConvArgs &a) {
+    return cdiv(a.ch[0], kVec) + cdiv(a.ch[1], kVec) + cdiv(a.ch[2], kVec);
 }
-int fwd_vec(const ConvArgs &a) { return a.bf16 ? 8 : 4; }
-
 // Tokens per lane: long runs reread few rows and weights, short ones fill the
-// chip (256 CUs x 2048 lanes) when there are few sequences or channels.
-int64_t run_length(int64_t lanes_per_token, int64_t T, int64_t most) {
-    int64_t tt = most;
-    while (tt > 4 && lanes_per_token * cdiv(T, tt) < (int64_t(1) << 18)) tt >>= 1;
+// chip when there are few sequences or channels: 2^18 lanes or more (half of
+// the chip's) forward, 2^17 backward, where a lane holds twice the registers
+// (4 x 2048 tokens, 2304 channels: 51 us in runs of 32, 55 in runs of 16).
+int64_t run_length(const ConvArgs &a, int64_t lanes) {
+    int64_t tt = 32;
+    while (tt > 4 && a.Bt * vectors(a) * cdiv(a.T, tt) < lanes) tt >>= 1;
     return tt;
 }
-int64_t fwd_run(const ConvArgs &a) { return run_length(a.Bt * vectors(a, fwd_vec(a)), a.T, 32); }
-int64_t bwd_run(const ConvArgs &a) { return run_length(a.Bt * vectors(a, 4), a.T, 32); }
+int64_t fwd_run(const ConvArgs &a) { return run_length(a, int64_t(1) << 18); }
+int64_t bwd_run(const ConvArgs &a) { return run_length(a, int64_t(1) << 17); }
 
-ConvGeom geom(const ConvArgs &a, int V, int64_t tt) {
+ConvGeom geom(const ConvArgs &a, int64_t tt) {
     ConvGeom g;
     g.T = a.T;
     g.sxb = a.sxb;
@@ -476,7 +489,7 @@ ConvGeom geom(const ConvArgs &a, int V, int64_t tt) {
     g.Bt = (int32_t)a.Bt;
     g.C = (int32_t)a.C;
     for (int i = 0; i < 3; ++i) g.ch[i] = (int32_t)a.ch[i];
-    g.nvec = (int32_t)vectors(a, V);
+    g.nvec = (int32_t)vectors(a);
     g.tt = (int32_t)tt;
     g.ntile = (int32_t)(a.T > 0 ? cdiv(a.T, tt) : 1);
     g.blk = 0;
@@ -487,8 +500,8 @@ ConvGeom geom(const ConvArgs &a, int V, int64_t tt) {
 // f(integral_constant<W>, bool_constant<RAG>) for the launch's taps, and
 // whether some tensor's channels end inside a lane's vector.
 template <typename F>
-void by_width(const ConvArgs &a, int V, F f) {
-    const bool rag = a.ch[0] % V || a.ch[1] % V || a.ch[2] % V;
+void by_width(const ConvArgs &a, F f) {
+    const bool rag = a.ch[0] % kVec || a.ch[1] % kVec || a.ch[2] % kVec;
     auto g = [&](auto w) {
         if (rag)
             f(w, std::true_type());
@@ -500,37 +513,37 @@ void by_width(const ConvArgs &a, int V, F f) {
     if (a.W == 4) g(std::integral_constant<int, 4>());
 }
 
-template <typename Tio, int V>
+template <typename Tio>
 void fwd_t(const ConvArgs &a, const ConvGeom &g, hipStream_t st) {
-    by_width(a, V, [&](auto w, auto rag) {
-        conv1d_fwd_kernel<Tio, V, decltype(w)::value, decltype(rag)::value>
+    by_width(a, [&](auto w, auto rag) {
+        conv1d_fwd_kernel<Tio, decltype(w)::value, decltype(rag)::value>
             <<<dim3((uint32_t)(a.Bt * g.blk)), 256, 0, st>>>(
                 (const Tio *)a.x, a.weight, a.bias, (const Tio *)a.init, a.lens, (Tio *)a.y[0],
                 (Tio *)a.y[1], (Tio *)a.y[2], (Tio *)a.fin, g);
     });
 }
 
-template <typename Tio, int V, int R>
+template <typename Tio, int R>
 void step_r(const ConvArgs &a, const ConvGeom &g, hipStream_t st) {
     const dim3 grid((uint32_t)cdiv(cdiv(a.Bt, R) * g.nvec, 256));
-    by_width(a, V, [&](auto w, auto rag) {
-        conv1d_step_kernel<Tio, V, decltype(w)::value, R, decltype(rag)::value>
+    by_width(a, [&](auto w, auto rag) {
+        conv1d_step_kernel<Tio, decltype(w)::value, R, decltype(rag)::value>
             <<<grid, 256, 0, st>>>((Tio *)a.state, a.slots, a.nslots, (const Tio *)a.x, a.weight,
                                    a.bias, (Tio *)a.y[0], (Tio *)a.y[1], (Tio *)a.y[2], g);
     });
 }
-template <typename Tio, int V>
+template <typename Tio>
 void step_t(const ConvArgs &a, const ConvGeom &g, hipStream_t st) {
     // 4 sequences per lane where that still leaves a wavefront per SIMD
     if (a.Bt * (int64_t)g.nvec >= 4 * 65536)
-        step_r<Tio, V, 4>(a, g, st);
+        step_r<Tio, 4>(a, g, st);
     else
-        step_r<Tio, V, 1>(a, g, st);
+        step_r<Tio, 1>(a, g, st);
 }
 
 template <typename Tio>
 void bwd_t(const ConvArgs &a, const ConvGeom &g, int64_t parts, hipStream_t st) {
-    by_width(a, 4, [&](auto w, auto rag) {
+    by_width(a, [&](auto w, auto rag) {
         conv1d_bwd_kernel<Tio, decltype(w)::value, decltype(rag)::value>
             <<<dim3((uint32_t)(parts * g.blk)), 256, 0, st>>>(
                 (const Tio *)a.x, a.weight, a.bias, (const Tio *)a.init, a.dy[0], a.dy[1], a.dy[2],
@@ -547,27 +560,27 @@ int64_t bwd_parts(const ConvArgs &a) {
 bool conv1d_fits(const ConvArgs &a) {
     // lane positions of one sequence, and workgroups, in 31 bits, at the
     // shortest run of either direction
-    const int64_t nvec = vectors(a, 4), runs = cdiv(a.T > 0 ? a.T : 1, 4);
+    const int64_t nvec = vectors(a), runs = cdiv(a.T > 0 ? a.T : 1, 4);
     const int64_t most = int64_t(1) << 31;
     return runs < most / nvec && a.Bt < most / cdiv(nvec * runs, 256) && a.Bt < most / nvec;
 }
 
 hipError_t launch_conv1d_fwd(const ConvArgs &a, hipStream_t st) {
-    ConvGeom g = geom(a, fwd_vec(a), fwd_run(a));
+    ConvGeom g = geom(a, fwd_run(a));
     g.blk = (int32_t)cdiv((int64_t)g.nvec * g.ntile, 256);
     if (a.bf16)
-        fwd_t<uint16_t, 8>(a, g, st);
+        fwd_t<uint16_t>(a, g, st);
     else
-        fwd_t<float, 4>(a, g, st);
+        fwd_t<float>(a, g, st);
     return hipGetLastError();
 }
 
 hipError_t launch_conv1d_step(const ConvArgs &a, hipStream_t st) {
-    const ConvGeom g = geom(a, fwd_vec(a), 1);
+    const ConvGeom g = geom(a, 1);
     if (a.bf16)
-        step_t<uint16_t, 8>(a, g, st);
+        step_t<uint16_t>(a, g, st);
     else
-        step_t<float, 4>(a, g, st);
+        step_t<float>(a, g, st);
     return hipGetLastError();
 }
 
@@ -576,7 +589,7 @@ size_t conv1d_bwd_workspace(const ConvArgs &a) {
 }
 
 hipError_t launch_conv1d_bwd(const ConvArgs &a, hipStream_t st) {
-    ConvGeom g = geom(a, 4, bwd_run(a));
+    ConvGeom g = geom(a, bwd_run(a));
     g.blk = (int32_t)cdiv(g.nvec, 64);
     const int64_t parts = bwd_parts(a);
     if (parts > 0) {   // (no sequences: the sums below are zero)
