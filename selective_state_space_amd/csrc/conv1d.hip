@@ -51,11 +51,16 @@ __device__ __forceinline__ Vec<T, V> load_vec(const T *p, int n) {
     for (int i = 0; i < V; ++i) r.v[i] = i < n ? p[i] : T(0);
     return r;
 }
-template <bool RAG, typename T, int V>
+// (NT: a nontemporal store)
+template <bool RAG, bool NT = false, typename T, int V>
 __device__ __forceinline__ void store_vec(T *p, const Vec<T, V> &r, int n) {
     typedef typename Words<sizeof(T) * V>::type words;
     if (!RAG || n == V) {
-        *reinterpret_cast<words *>(p) = __builtin_bit_cast(words, r);
+        if constexpr (NT)
+            __builtin_nontemporal_store(__builtin_bit_cast(words, r),
+                                        reinterpret_cast<words *>(p));
+        else
+            *reinterpret_cast<words *>(p) = __builtin_bit_cast(words, r);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -142,7 +147,7 @@ __device__ __forceinline__ void load_weights(const float *__restrict__ weight,
 // the sequence's length are written as zeros.  The first run also writes the
 // final state: it alone reads the initial state, so the two may be the same
 // memory.
-template <typename Tio, int W, bool RAG>
+template <typename Tio, int W, bool RAG, bool NT>
 __global__ __launch_bounds__(256) void conv1d_fwd_kernel(
     const Tio *__restrict__ x, const float *__restrict__ weight, const float *__restrict__ bias,
     const Tio *init, const int32_t *__restrict__ lens, Tio *__restrict__ y0,
@@ -203,7 +208,7 @@ __global__ __launch_bounds__(256) void conv1d_fwd_kernel(
                         for (int k = 0; k + 1 < W - 1; ++k) win[k][i] = win[k + 1][i];
                         win[W - 2][i] = xv[i];
                     }
-                    store_vec<RAG, Tio, V>(yb + (t + u) * ci.width, narrow(out, Tio(0)), ci.n);
+                    store_vec<RAG, NT>(yb + (t + u) * ci.width, narrow(out, Tio(0)), ci.n);
                 }
             }
 #pragma unroll
@@ -211,7 +216,7 @@ __global__ __launch_bounds__(256) void conv1d_fwd_kernel(
         }
     }
     for (int64_t t = max(te, t0); t < t1; ++t)
-        store_vec<RAG, Tio, V>(yb + t * ci.width, Vec<Tio, V>{}, ci.n);
+        store_vec<RAG>(yb + t * ci.width, Vec<Tio, V>{}, ci.n);
 
     if (tile == 0 && fin) {
         Vec<Tio, V> last[W - 1];
@@ -229,7 +234,7 @@ __global__ __launch_bounds__(256) void conv1d_fwd_kernel(
         }
 #pragma unroll
         for (int r = 0; r < W - 1; ++r)
-            store_vec<RAG, Tio, V>(fin + ((int64_t)b * (W - 1) + r) * g.C + ci.c, last[r], ci.n);
+            store_vec<RAG>(fin + ((int64_t)b * (W - 1) + r) * g.C + ci.c, last[r], ci.n);
     }
 }
 
@@ -286,12 +291,12 @@ __global__ __launch_bounds__(256) void conv1d_step_kernel(
             for (int i = 0; i < V; ++i) out[i] = g.silu ? fast_silu(out[i]) : out[i];
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
-                store_vec<RAG, Tio, V>(state + base[r] + (int64_t)k * g.C, row[r][k + 1], ci.n);
+                store_vec<RAG>(state + base[r] + (int64_t)k * g.C, row[r][k + 1], ci.n);
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) out[i] = 0.f;
         }
-        store_vec<RAG, Tio, V>(yp + b * ci.width, narrow(out, Tio(0)), ci.n);
+        store_vec<RAG>(yp + b * ci.width, narrow(out, Tio(0)), ci.n);
     }
 }
 
@@ -407,9 +412,9 @@ __global__ __launch_bounds__(256) void conv1d_bwd_kernel(
 #pragma unroll
                 for (int i = 0; i < V; ++i) o.v[i] = out[i];
                 if (t >= t0)
-                    store_vec<RAG, float, V>(dx + ((int64_t)b * g.T + t) * g.C + ci.c, o, ci.n);
+                    store_vec<RAG>(dx + ((int64_t)b * g.T + t) * g.C + ci.c, o, ci.n);
                 else if (t < 0 && dinit)    // the first run: rows of the initial state
-                    store_vec<RAG, float, V>(dinit + ((int64_t)b * (W - 1) + s) * g.C + ci.c, o, ci.n);
+                    store_vec<RAG>(dinit + ((int64_t)b * (W - 1) + s) * g.C + ci.c, o, ci.n);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) cur[u] = nxt[u];
@@ -513,13 +518,26 @@ void by_width(const ConvArgs &a, F f) {
     if (a.W == 4) g(std::integral_constant<int, 4>());
 }
 
+// Outputs that outgrow the 256 MB memory-side cache are not found there by the
+// scan that reads them next: nontemporal stores (8 x 4096 tokens, 5376 channels,
+// 352 MB: 142 us, plain 148).  Smaller ones stay cached.
+bool streams(const ConvArgs &a) {
+    return a.Bt * a.T * a.C * (a.bf16 ? 2 : 4) > (int64_t(256) << 20);
+}
+
 template <typename Tio>
 void fwd_t(const ConvArgs &a, const ConvGeom &g, hipStream_t st) {
     by_width(a, [&](auto w, auto rag) {
-        conv1d_fwd_kernel<Tio, decltype(w)::value, decltype(rag)::value>
-            <<<dim3((uint32_t)(a.Bt * g.blk)), 256, 0, st>>>(
-                (const Tio *)a.x, a.weight, a.bias, (const Tio *)a.init, a.lens, (Tio *)a.y[0],
-                (Tio *)a.y[1], (Tio *)a.y[2], (Tio *)a.fin, g);
+        auto launch = [&](auto nt) {
+            conv1d_fwd_kernel<Tio, decltype(w)::value, decltype(rag)::value, decltype(nt)::value>
+                <<<dim3((uint32_t)(a.Bt * g.blk)), 256, 0, st>>>(
+                    (const Tio *)a.x, a.weight, a.bias, (const Tio *)a.init, a.lens,
+                    (Tio *)a.y[0], (Tio *)a.y[1], (Tio *)a.y[2], (Tio *)a.fin, g);
+        };
+        if (streams(a))
+            launch(std::true_type());
+        else
+            launch(std::false_type());
     });
 }
 
@@ -558,11 +576,12 @@ int64_t bwd_parts(const ConvArgs &a) {
 }  // namespace
 
 bool conv1d_fits(const ConvArgs &a) {
-    // lane positions of one sequence, and workgroups, in 31 bits, at the
-    // shortest run of either direction
-    const int64_t nvec = vectors(a), runs = cdiv(a.T > 0 ? a.T : 1, 4);
-    const int64_t most = int64_t(1) << 31;
-    return runs < most / nvec && a.Bt < most / cdiv(nvec * runs, 256) && a.Bt < most / nvec;
+    const double nvec = (double)vectors(a), T = a.T > 0 ? (double)a.T : 1.0, Bt = (double)a.Bt;
+    const double fwd = Bt * (nvec * (T / (double)fwd_run(a) + 1.0) / 256.0 + 1.0);
+    const double bwd = Bt * (T / (4.0 * (double)bwd_run(a)) + 1.0) * (nvec / 64.0 + 1.0);
+    const double step = Bt * nvec / 256.0 + 1.0;
+    const double most = (double)kMaxBlocks;
+    return fwd <= most && bwd <= most && step <= most;
 }
 
 hipError_t launch_conv1d_fwd(const ConvArgs &a, hipStream_t st) {

@@ -14,7 +14,6 @@ namespace {
 using ssd::fail;
 using ssd::hip_result;
 using ssd::kMaxDim;
-using ssd::kMaxGrid;
 using ssd::misaligned;
 using ssd::ok;
 
@@ -90,7 +89,7 @@ ssd_status check_slots(const int32_t *slots, int64_t num_slots, int64_t n) {
 }
 
 ssd_status check_scan(const ssd_scan_dims *d, bool need_seq, const ssd_layer_opts *o,
-                      ssd::SelArgs *a) {
+                      bool (*fits)(const ssd::SelArgs &), ssd::SelArgs *a) {
     if (!d) return fail(SSD_ERR_NULL, "dims is NULL");
     if (d->batch < 0 || d->batch > kMaxDim)
         return fail(SSD_ERR_SHAPE, "batch = %lld out of range [0, 2^30]", (long long)d->batch);
@@ -120,7 +119,7 @@ ssd_status check_scan(const ssd_scan_dims *d, bool need_seq, const ssd_layer_opt
         a->ybf = a->bf16 && o->y_io_dtype != 0;
         a->z = o->z;
     }
-    if (!ssd::selective_scan_fits(*a))
+    if (!fits(*a))
         return fail(SSD_ERR_SHAPE, "problem too large for one launch (batch %lld, seqlen %lld, "
                     "dim %lld)", (long long)a->Bt, (long long)a->T, (long long)a->Dm);
     return SSD_OK;
@@ -153,11 +152,11 @@ ssd_status check_cache(int64_t n, int64_t size, const int32_t *slots, int64_t nu
                     "format = %d; only SSD_CACHE_INT8 (0) and SSD_CACHE_FP8 (1)", (int)format);
     const ssd_status r = check_slots(slots, num_slots, n);
     if (r != SSD_OK) return r;
-    if ((double)n * (double)((size + 4095) / 4096) > (double)kMaxGrid)
-        return fail(SSD_ERR_SHAPE, "n * size = %lld * %lld too large for one launch", (long long)n,
-                    (long long)size);
     a->n = n;
     a->size = size;
+    if (!ssd::cache_fits(*a))
+        return fail(SSD_ERR_SHAPE, "n * size = %lld * %lld too large for one launch", (long long)n,
+                    (long long)size);
     a->slots = slots;
     a->nslots = num_slots;
     a->fp8 = format == SSD_CACHE_FP8;
@@ -277,7 +276,7 @@ ssd_status ssd_conv1d_bwd(const void *x, const float *weight, const float *bias,
 
 size_t ssd_selective_scan_workspace_size(const ssd_scan_dims *dims) {
     ssd::SelArgs a;
-    if (check_scan(dims, true, nullptr, &a) != SSD_OK) return 0;
+    if (check_scan(dims, true, nullptr, ssd::selective_scan_fits, &a) != SSD_OK) return 0;
     return ssd::selective_scan_workspace(a);
 }
 
@@ -287,7 +286,7 @@ ssd_status ssd_selective_scan_fwd(const void *x, const void *dt, const float *A,
                                   const ssd_layer_opts *opts, const ssd_scan_dims *dims,
                                   void *workspace, size_t workspace_bytes, void *stream) {
     ssd::SelArgs a;
-    ssd_status r = check_scan(dims, true, opts, &a);
+    ssd_status r = check_scan(dims, true, opts, ssd::selective_scan_fits, &a);
     if (r != SSD_OK) return r;
     const bool tokens = a.Bt > 0 && a.T > 0;
     PTR_IF(tokens, x);
@@ -327,7 +326,7 @@ ssd_status ssd_selective_scan_step(float *state, int64_t num_slots, const int32_
                                    const ssd_layer_opts *opts, const ssd_scan_dims *dims,
                                    void *stream) {
     ssd::SelArgs a;
-    ssd_status r = check_scan(dims, false, opts, &a);
+    ssd_status r = check_scan(dims, false, opts, ssd::selective_step_fits, &a);
     if (r != SSD_OK) return r;
     if ((r = check_slots(slots, num_slots, a.Bt)) != SSD_OK) return r;
     PTR_IF(a.Bt > 0, state);
@@ -357,7 +356,7 @@ ssd_status ssd_selective_scan_step(float *state, int64_t num_slots, const int32_
 
 size_t ssd_selective_scan_bwd_workspace_size(const ssd_scan_dims *dims) {
     ssd::SelArgs a;
-    if (check_scan(dims, true, nullptr, &a) != SSD_OK) return 0;
+    if (check_scan(dims, true, nullptr, ssd::selective_scan_bwd_fits, &a) != SSD_OK) return 0;
     return ssd::selective_scan_bwd_workspace(a);
 }
 
@@ -369,7 +368,7 @@ ssd_status ssd_selective_scan_bwd(const void *x, const void *dt, const float *A,
                                   const ssd_scan_dims *dims, void *workspace,
                                   size_t workspace_bytes, void *stream) {
     ssd::SelArgs a;
-    ssd_status r = check_scan(dims, true, opts, &a);
+    ssd_status r = check_scan(dims, true, opts, ssd::selective_scan_bwd_fits, &a);
     if (r != SSD_OK) return r;
     const bool tokens = a.Bt > 0 && a.T > 0;
     PTR_IF(tokens, x);

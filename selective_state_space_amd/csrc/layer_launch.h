@@ -9,6 +9,9 @@
 
 namespace ssd {
 
+// Workgroups of 256 threads that one launch holds (fewer than 2^32 threads).
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;
+
 struct ConvArgs {
     const void *x;             // io dtype, rows at the strides below
     const float *weight;       // [C, W]
@@ -34,7 +37,7 @@ hipError_t launch_conv1d_fwd(const ConvArgs &a, hipStream_t st);
 hipError_t launch_conv1d_step(const ConvArgs &a, hipStream_t st);
 hipError_t launch_conv1d_bwd(const ConvArgs &a, hipStream_t st);
 size_t conv1d_bwd_workspace(const ConvArgs &a);
-// false: more workgroups or 32-bit positions than one launch holds
+// false: more workgroups than one launch holds
 bool conv1d_fits(const ConvArgs &a);
 
 struct CacheArgs {
@@ -46,6 +49,7 @@ struct CacheArgs {
     float *dst;             // read: [n, size]
     bool fp8;               // e4m3 codes (else int8)
 };
+bool cache_fits(const CacheArgs &a);   // false: more workgroups than one launch holds
 hipError_t launch_cache_write(const CacheArgs &a, hipStream_t st);
 hipError_t launch_cache_read(const CacheArgs &a, hipStream_t st);
 
@@ -67,7 +71,10 @@ struct SelArgs {
     int N;
     bool softplus, bf16, ybf;
 };
-bool selective_scan_fits(const SelArgs &a);   // workgroups in one launch
+// false: more workgroups than one launch holds
+bool selective_scan_fits(const SelArgs &a);
+bool selective_step_fits(const SelArgs &a);
+bool selective_scan_bwd_fits(const SelArgs &a);
 size_t selective_scan_workspace(const SelArgs &a);
 hipError_t launch_selective_scan(const SelArgs &a, hipStream_t st);
 hipError_t launch_selective_step(const SelArgs &a, hipStream_t st);

@@ -178,10 +178,15 @@ void by_y(const SelArgs &a, F f) {
 }  // namespace
 
 bool selective_scan_fits(const SelArgs &a) {
-    // workgroups of the widest launch (segments of 16 tokens in the backward)
-    const double blocks = (double)a.Bt * (double)chan_blocks(a);
-    return blocks * 1024.0 < 0x1p31 && (double)a.Bt * (double)a.Dm * (double)a.N < 0x1p38 &&
-           (double)a.Bt * (double)a.T * (double)a.N < 0x1p38;
+    if (a.Bt == 0) return true;
+    if ((double)a.Bt * (double)chan_blocks(a, 2) > (double)kMaxBlocks) return false;
+    const Cut s = cut_of(a);
+    return (double)a.Bt * (double)s.n * (double)s.ncb <= (double)kMaxBlocks &&
+           (double)a.Bt * (double)a.Dm * (double)a.N <= 256.0 * (double)kMaxBlocks;
+}
+
+bool selective_step_fits(const SelArgs &a) {
+    return (double)a.Bt * (double)chan_blocks(a) <= (double)kMaxBlocks;
 }
 
 size_t selective_scan_workspace(const SelArgs &a) {

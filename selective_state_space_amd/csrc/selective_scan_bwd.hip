@@ -696,6 +696,18 @@ BwdPlan plan(const SelArgs &a) {
 
 }  // namespace
 
+bool selective_scan_bwd_fits(const SelArgs &a) {
+    if (a.Bt == 0) return true;
+    if ((double)a.Bt * (double)chan_blocks(a, 2) > (double)kMaxBlocks) return false;
+    const BwdPlan p = plan(a);
+    // the widest of the passes, the chain over segments and the last sums
+    const double sums = ((double)a.Bt * (double)a.T * 2.0 + (double)a.Dm) * a.N / 64.0 +
+                        (double)a.Dm / 32.0 + 4.0;
+    return (double)a.Bt * (double)p.nseg * (double)p.ncb <= (double)kMaxBlocks &&
+           (double)a.Bt * (double)a.Dm * (double)a.N <= 256.0 * (double)kMaxBlocks &&
+           sums <= (double)kMaxBlocks;
+}
+
 size_t selective_scan_bwd_workspace(const SelArgs &a) {
     return a.Bt > 0 ? plan(a).total * sizeof(float) : 0;
 }

@@ -159,6 +159,10 @@ uint32_t blocks_per_state(const CacheArgs &a) { return (uint32_t)((a.size + kSpa
 
 }  // namespace
 
+bool cache_fits(const CacheArgs &a) {
+    return (double)a.n * (double)((a.size + kSpan - 1) / kSpan) <= (double)kMaxBlocks;
+}
+
 hipError_t launch_cache_write(const CacheArgs &a, hipStream_t st) {
     const uint32_t blk = blocks_per_state(a);
     const dim3 grid((uint32_t)(a.n * blk));

@@ -682,6 +682,8 @@ def _conv_args(x, weight, bias, splits, silu, tokens: int):
 def _outs(y, name, dtype, shapes, dev):
     if y is None:
         return tuple([torch.empty(s, dtype=dtype, device=dev) for s in shapes])
+    if isinstance(y, torch.Tensor):
+        y = (y,)
     if len(y) != len(shapes):
         raise ValueError("%s must hold %d tensors" % (name, len(shapes)))
     return tuple([_need_out(t, "%s[%d]" % (name, i), dtype, s, dev)

@@ -143,6 +143,36 @@ def test_two_halves_equal_one_call():
     assert torch.equal(torch.cat([ya, yb], 1), y) and torch.equal(s2, fin)
 
 
+@pytest.mark.parametrize("C", [4096, 4101])
+def test_large_outputs_equal_their_parts(C):
+    """Outputs past 256 MB are stored nontemporally: the same values as two shorter calls."""
+    T = 33000
+    assert T * C * 2 > 256 << 20 and T * C < 256 << 20
+    x = torch.randn(1, T, C, device="cuda").to(torch.bfloat16)
+    w, b = torch.randn(C, 4, device="cuda"), torch.randn(C, device="cuda")
+    (y,), fin = ssd.ssd_conv1d_fwd(x, w, b)
+    (ya,), s1 = ssd.ssd_conv1d_fwd(x[:, :17000], w, b)
+    (yb,), s2 = ssd.ssd_conv1d_fwd(x[:, 17000:], w, b, init_state=s1)
+    assert torch.equal(y[:, :17000], ya) and torch.equal(y[:, 17000:], yb)
+    assert torch.equal(fin, s2)
+
+
+def test_step_pool_past_32_bit_offsets():
+    C, W = 4096, 4
+    num = 2 ** 32 // (C * (W - 1)) + 3
+    pool = torch.zeros(num, W - 1, C, dtype=torch.bfloat16, device="cuda")
+    assert pool.numel() > 2 ** 32
+    small = torch.randn(2, W - 1, C, device="cuda").to(torch.bfloat16)
+    pool[num - 1], pool[1] = small[0], small[1]
+    x = torch.randn(2, C, device="cuda").to(torch.bfloat16)
+    w = torch.randn(C, W, device="cuda")
+    (y,) = ssd.ssd_conv1d_step(pool, x, w, slots=torch.tensor([num - 1, 1], dtype=torch.int32).cuda())
+    (ref,) = ssd.ssd_conv1d_step(small, x, w)
+    assert torch.equal(y, ref)
+    assert torch.equal(pool[num - 1], small[0]) and torch.equal(pool[1], small[1])
+    assert not pool[num - 2].any() and not pool[0].any()
+
+
 @pytest.mark.parametrize("T", [0, 1, 2])
 def test_shorter_than_the_taps(T):
     m = make(2, T, 24, 4, "f32", 5)

@@ -373,6 +373,49 @@ def test_gradient_differences():
         assert abs(float(terms.sum()) - num) <= tol, (name, float(terms.sum()), num, tol)
 
 
+def test_offsets_past_32_bits():
+    """A prompt of more than 2^32 elements, and a state pool of as many: the last tokens
+    continue the state of the tokens before them."""
+    Dm, N = 4160, 16
+    T = 2 ** 32 // Dm + 130
+    x = torch.randn(1, 4099, Dm, device="cuda").to(torch.bfloat16).repeat(1, -(-T // 4099), 1)[:, :T]
+    assert x.numel() > 2 ** 32
+    dt = (x.flip(2) - 3).contiguous()
+    B = torch.randn(1, T, N, device="cuda").to(torch.bfloat16)
+    C = torch.randn(1, T, N, device="cuda").to(torch.bfloat16)
+    A = -torch.arange(1, N + 1, device="cuda").float().repeat(Dm, 1)
+    D = torch.randn(Dm, device="cuda")
+    cut = T - 100
+    part = lambda t, a, b: t[:, a:b].contiguous()
+    run = lambda a, b, h: ssd.ssd_selective_scan_fwd(
+        part(x, a, b), part(dt, a, b), A, part(B, a, b), part(C, a, b), D, init_state=h,
+        dt_softplus=True, y_io_dtype=True)
+    y, fin = run(0, T, None)
+    last, fin = y[:, cut:].float().clone(), fin.clone()
+    del y
+    # (tokens 500 back reach the end through exp(-sum of d) below 1e-9, so two starts agree)
+    _, h = run(cut - 2000, cut, None)
+    yt, ft = run(cut, T, h)
+    # bf16 outputs, off by half a step each, and float32 sums of 16 states and their decay
+    tol = 2.0 ** -8 * torch.maximum(last.abs(), yt.float().abs()) * 2 + 1e-4 * last.abs().max()
+    assert ((last - yt.float()).abs() <= tol).all()
+    assert float((fin - ft).abs().max()) <= 1e-4 * float(ft.abs().max())
+    del x, dt
+    num = 2 ** 32 // (Dm * N) + 3
+    pool = torch.zeros(num, Dm, N, device="cuda")
+    assert pool.numel() > 2 ** 32
+    pool[num - 1], pool[1] = fin[0], ft[0]
+    small = torch.cat([fin, ft])
+    xt = torch.randn(2, Dm, device="cuda").to(torch.bfloat16)
+    args = (xt, xt.flip(1), A, B[0, :2], C[0, :2], D)
+    yp = ssd.ssd_selective_scan_step(pool, *args, dt_softplus=True,
+                                     slots=torch.tensor([num - 1, 1], dtype=torch.int32).cuda())
+    ys = ssd.ssd_selective_scan_step(small, *args, dt_softplus=True)
+    assert torch.equal(yp, ys)
+    assert torch.equal(pool[num - 1], small[0]) and torch.equal(pool[1], small[1])
+    assert not pool[num - 2].any() and not pool[0].any()
+
+
 def test_graph_replays_follow_the_inputs():
     """Forward (split over time), step and gradients in one graph: every replay equals the
     eager calls on that replay's inputs, with eager work between."""

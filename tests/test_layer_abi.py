@@ -61,6 +61,7 @@ def conv_bwd(d, x=P16, weight=P16, bias=P16, init=P16, dy=parts(P16, P16, P16), 
     (dict(ch=(8, 8, (1 << 24) + 1)), -2, "channels[2]"),
     (dict(sb=-1), -2, "stride"), (dict(stt=-1), -2, "stride"), (dict(io=2), -3, "io_dtype"),
     (dict(Bt=1 << 30, T=1 << 30, ch=(1 << 24, 0, 0)), -2, "too large"),
+    (dict(Bt=1 << 24, T=1, ch=(1024, 0, 0)), -2, "too large"),
 ])
 def test_conv_dims(call, kw, code, word):
     assert call(conv_dims(**kw)) == code
@@ -140,10 +141,15 @@ def scan_bwd(d, x=P16, dt=P16, A=P16, B=P16, C=P16, D=P16, init=P16, dy=P16, dfi
     (dict(Bt=-1), -2, "batch"), (dict(Dm=0), -2, "dim"), (dict(Dm=(1 << 24) + 1), -2, "dim"),
     (dict(N=12), -3, "dstate"), (dict(N=128), -3, "dstate"), (dict(io=5), -3, "io_dtype"),
     (dict(Bt=1 << 28, Dm=1 << 20), -2, "too large"),
+    (dict(Bt=1 << 24, Dm=64), -2, "too large"),
 ])
 def test_scan_dims(call, kw, code, word):
     assert call(scan_dims(**kw)) == code
     assert word in detail()
+
+
+def test_scan_too_many_sums():
+    assert scan_bwd(scan_dims(Bt=1 << 10, T=1 << 20, N=64)) == -2 and "too large" in detail()
 
 
 def test_scan_seqlen():
