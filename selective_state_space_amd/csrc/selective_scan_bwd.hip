@@ -641,15 +641,18 @@ __global__ __launch_bounds__(256) void sel_sum_kernel(SumJobs jobs) {
     }
 }
 
-// How a launch is cut.  The reverse pass keeps 16 tokens' states in registers,
-// so 2 workgroups of 4 states per lane fill a CU, 512 the chip.  Whole
-// sequences take ceil(workgroups / 512) rounds; in segments the rounds even out
-// at the price of a second pass over the tokens, about a third of the work:
-// segments of at least 32 tokens, enough for 2048 workgroups, where the rounds
-// waste more than that (8 x 1024 tokens, 5120 channels, 640 workgroups: 872 us
-// in segments, 958 us whole; 16 x 512 x 2048, 512 workgroups: 372 and 326 us; 4
-// x 2048 x 2048, 128 workgroups: 382 and 925 us).  Where segments still leave
-// CUs without 2 workgroups, 2 states per lane shorten each wavefront's walk.
+// How a launch is cut.  Times are counted in tiles of the reverse pass (8.6 us
+// for 512 workgroups of 4 states per lane, which fill the chip: it keeps 16
+// tokens' states in registers):
+//   * the reverse pass takes its rounds of 512 workgroups times a segment's
+//     tiles, and half a tile for first loads and last sums;
+//   * the first pass, and with segments the adjoints', take 0.24 of that per
+//     tile, less where more workgroups hide their waits (58 us with 2048, 75
+//     with 512);
+//   * 2 states per lane take 0.62 of 4.
+// The cheapest is taken (8 x 1024 tokens, 5120 channels: 958 us whole, 860 us
+// in 4 segments; 16 x 512 x 2048: 317 us whole, 372 in 4; 4 x 2048 x 2048: 925
+// whole, 405 in 4, 374 in 16).
 // (N 8 with 4 states per lane would spill registers)
 constexpr int bwd_most_ks(int N) { return N == 8 ? 2 : 4; }
 struct BwdPlan {
@@ -660,18 +663,31 @@ struct BwdPlan {
 };
 BwdPlan plan(const SelArgs &a) {
     BwdPlan p;
-    const int most = bwd_most_ks(a.N);
-    const int64_t blocks = a.Bt * chan_blocks(a, most);
-    int64_t n = 1;
-    if (10 * cdiv64(blocks, 512) * 512 > 13 * blocks && blocks > 0) {
-        n = cdiv64(2048, blocks);
-        n = n < a.T / 32 ? n : a.T / 32;
-        if (n < 1) n = 1;
+    const int64_t tiles = cdiv64(a.T > 0 ? a.T : 1, TB);
+    double best = 0.0;
+    p.ks = 0;
+    for (int ks = bwd_most_ks(a.N); ks >= (a.N < 64 ? 2 : 4); ks -= 2) {
+        const int64_t ncb = chan_blocks(a, ks);
+        for (int64_t n = 1; n <= 64 && n <= tiles; ++n) {
+            const int64_t seg = cdiv64(tiles, n), nseg = cdiv64(tiles, seg);
+            const double blocks = (double)(a.Bt * ncb * nseg), len = (double)seg;
+            const double rounds = (double)cdiv64(a.Bt * ncb * nseg, 512);
+            const double work = blocks * len / 512.0;
+            const double passes = 2.0 - 1.0 / (double)nseg;
+            const double cost =
+                (ks == 2 ? 0.62 : 1.0) *
+                    (rounds * (len + 0.5) + 0.24 * passes * (work > 0.75 * len ? work : 0.75 * len) *
+                                                (0.8 + 240.0 / (blocks > 256.0 ? blocks : 256.0))) +
+                (nseg > 1 ? 0.5 + 0.01 * (double)nseg : 0.0);
+            if (p.ks == 0 || cost < best) {
+                best = cost;
+                p.ks = ks;
+                p.ncb = ncb;
+                p.nseg = nseg;
+                p.seg_len = seg * TB;
+            }
+        }
     }
-    p.ks = a.N < 64 && blocks * n < 512 ? 2 : most;
-    p.ncb = chan_blocks(a, p.ks);
-    p.seg_len = cdiv64(cdiv64(a.T > 0 ? a.T : 1, n), TB) * TB;
-    p.nseg = n > 1 ? cdiv64(a.T, p.seg_len) : 1;
     const int64_t ncb = p.ncb;
     const size_t st = (size_t)a.Bt * a.Dm * a.N, ch = (size_t)a.Bt * a.Dm;
     const size_t nt = (size_t)cdiv64(a.T, TB), ns = p.nseg;
