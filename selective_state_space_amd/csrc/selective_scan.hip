@@ -58,58 +58,62 @@ __global__ __launch_bounds__(256) void sel_chain_kernel(float *__restrict__ seg,
 }
 
 // One token per sequence: the state is read and written once, which is all
-// the traffic that counts.  A lane keeps its 4 decay rates for R sequences
-// (A is as large as one sequence's state).
+// the traffic that counts (A, as large as one sequence's state, comes from L2).
+// A lane holds 4 states of R channels; a wavefront's are contiguous, R KB of one
+// state (256 sequences, 5120 channels, N 16: 35 us with R 2, 5.1 TB/s; 37 with 4
+// channels, or with one channel of 4 sequences).
 template <int N, typename Tio, typename Ty, bool GATE, int R>
 __global__ __launch_bounds__(256) void sel_step_kernel(
     float *__restrict__ state, const int32_t *__restrict__ slots, int64_t nslots,
     const Tio *__restrict__ x, const Tio *__restrict__ dt, const float *__restrict__ A,
     const Tio *__restrict__ B, const Tio *__restrict__ C, const float *__restrict__ D,
-    const Tio *__restrict__ z, const float *__restrict__ dt_bias, Ty *__restrict__ y, int32_t Bt,
-    int32_t Dm, int32_t ncb, int32_t softplus) {
+    const Tio *__restrict__ z, const float *__restrict__ dt_bias, Ty *__restrict__ y, int32_t Dm,
+    int32_t ncb, int32_t softplus) {
     constexpr int S = SelSplit<N>::S, CPW = SelSplit<N>::CPW, CB = SelSplit<N>::CB;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t cb = blockIdx.x % (uint32_t)ncb;
-    const int64_t b0 = (int64_t)(blockIdx.x / (uint32_t)ncb) * R;
+    const int64_t b = blockIdx.x / (uint32_t)ncb;
     const int s = lane % S;
-    const int32_t c = cb * CB + wave * CPW + lane / S;
-    if (c >= Dm) return;
-    float4 hv[R], bv[R], cv[R];
-    float xv[R], dv[R], zv[R];
-    float *hp[R];
+    const int32_t c0 = (cb * R) * CB + wave * (CPW * R) + lane / S;
+    const int64_t slot = slots ? (int64_t)slots[b] : b;
+    const bool live = slot >= 0 && slot < nslots;
+    float *hp = state + (slot * Dm + c0) * N + 4 * s;
+    float4 hv[R], av[R], bv, cv;
+    float xv[R], dv[R], zv[R], bias[R], Dc[R];
+    if (live) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t b = b0 + r;
-        const int64_t slot = b < Bt ? (slots ? (int64_t)slots[b] : b) : -1;
-        hp[r] = slot >= 0 && slot < nslots ? state + (slot * Dm + c) * N + 4 * s : nullptr;
-        if (hp[r]) {
-            hv[r] = load_nt(hp[r]);
-            bv[r] = widen4(load_raw<false>(B + b * N + 4 * s, 4));
-            cv[r] = widen4(load_raw<false>(C + b * N + 4 * s, 4));
-            xv[r] = load1(x + b * Dm + c);
-            dv[r] = load1(dt + b * Dm + c);
-            if constexpr (GATE) zv[r] = load1(z + b * Dm + c);
+        for (int r = 0; r < R; ++r) {
+            const int32_t c = c0 + r * CPW;
+            if (c < Dm) {
+                hv[r] = load_nt(hp + (int64_t)r * CPW * N);
+                av[r] = *reinterpret_cast<const float4 *>(A + (int64_t)c * N + 4 * s);
+                xv[r] = load1(x + b * Dm + c);
+                dv[r] = load1(dt + b * Dm + c);
+                if constexpr (GATE) zv[r] = load1(z + b * Dm + c);
+                bias[r] = dt_bias ? dt_bias[c] : 0.f;
+                Dc[r] = D[c];
+            }
         }
+        bv = widen4(load_raw<false>(B + b * N + 4 * s, 4));
+        cv = widen4(load_raw<false>(C + b * N + 4 * s, 4));
     }
-    const float4 av = *reinterpret_cast<const float4 *>(A + (int64_t)c * N + 4 * s);
-    const float bias = dt_bias ? dt_bias[c] : 0.f, Dc = D[c];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int64_t b = b0 + r;
-        if (b >= Bt) break;
+        const int32_t c = c0 + r * CPW;
+        if (c >= Dm) break;
         float out = 0.f;
-        if (hp[r]) {
-            float d = dv[r] + bias;
+        if (live) {
+            float d = dv[r] + bias[r];
             if (softplus) d = softplus_f(d);
             const float u = d * xv[r], d2 = d * kLog2e;
             float4 h = hv[r];
-            h.x = fmaf(fast_exp2(d2 * av.x), h.x, u * bv[r].x);
-            h.y = fmaf(fast_exp2(d2 * av.y), h.y, u * bv[r].y);
-            h.z = fmaf(fast_exp2(d2 * av.z), h.z, u * bv[r].z);
-            h.w = fmaf(fast_exp2(d2 * av.w), h.w, u * bv[r].w);
-            store_nt(hp[r], h);
-            out = chan_sum<S>(h.x * cv[r].x + h.y * cv[r].y + h.z * cv[r].z + h.w * cv[r].w);
-            out += Dc * xv[r];
+            h.x = fmaf(fast_exp2(d2 * av[r].x), h.x, u * bv.x);
+            h.y = fmaf(fast_exp2(d2 * av[r].y), h.y, u * bv.y);
+            h.z = fmaf(fast_exp2(d2 * av[r].z), h.z, u * bv.z);
+            h.w = fmaf(fast_exp2(d2 * av[r].w), h.w, u * bv.w);
+            store_nt(hp + (int64_t)r * CPW * N, h);
+            out = chan_sum<S>(h.x * cv.x + h.y * cv.y + h.z * cv.z + h.w * cv.w);
+            out += Dc[r] * xv[r];
             if constexpr (GATE) out *= fast_silu(zv[r]);
         }
         if (s == 0) {
@@ -256,23 +260,23 @@ hipError_t launch_selective_scan(const SelArgs &a, hipStream_t st) {
 }
 
 hipError_t launch_selective_step(const SelArgs &a, hipStream_t st) {
-    const int64_t ncb = chan_blocks(a);
-    // 4 sequences per lane where that leaves 2 workgroups per CU
-    const bool four = a.Bt * ncb >= 4 * 512;
-    const dim3 grid((uint32_t)(ncb * cdiv64(a.Bt, four ? 4 : 1)));
+    const int64_t one = chan_blocks(a);
+    // 2 channels per lane where that leaves 2 workgroups per CU
+    const bool two = a.Bt * one >= 2 * 512;
+    const int64_t ncb = two ? cdiv64(one, 2) : one;
+    const dim3 grid((uint32_t)(ncb * a.Bt));
     by_state(a, [&](auto n, auto io) {
         typedef decltype(io) Tio;
         by_flag(a.z != nullptr, [&](auto gate) {
-            by_flag(four, [&](auto f) {
+            by_flag(two, [&](auto f) {
                 by_y(a, [&](auto yt) {
                     typedef decltype(yt) Ty;
                     if constexpr (sizeof(Ty) == 4 || sizeof(Tio) == 2)
                         sel_step_kernel<decltype(n)::value, Tio, Ty, decltype(gate)::value,
-                                        decltype(f)::value ? 4 : 1><<<grid, 256, 0, st>>>(
+                                        decltype(f)::value ? 2 : 1><<<grid, 256, 0, st>>>(
                             a.state, a.slots, a.nslots, (const Tio *)a.x, (const Tio *)a.dt, a.A,
                             (const Tio *)a.B, (const Tio *)a.C, a.D, (const Tio *)a.z, a.dt_bias,
-                            (Ty *)a.y, (int32_t)a.Bt, (int32_t)a.Dm, (int32_t)ncb,
-                            a.softplus ? 1 : 0);
+                            (Ty *)a.y, (int32_t)a.Dm, (int32_t)ncb, a.softplus ? 1 : 0);
                 });
             });
         });
