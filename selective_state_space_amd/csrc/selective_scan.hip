@@ -6,9 +6,11 @@
 // optionally y <- y silu(z).  ("mamba-metal: running Mamba on Apple Silicon",
 // the selective scan with a diagonal A per state element.)  The decay differs
 // for every (channel, state), so unlike the scalar-decay scan no part of it is
-// a matrix product: each state element costs an exponential and five vector
-// operations per token, 16 times more arithmetic per byte than memory needs,
-// and the kernels are bound by vector issue.
+// a matrix product: each state element costs an exponential (two issue
+// slots) and four vector operations per token, and forming d, the gate and the
+// sums over n some 3 more.  The kernels are bound by vector issue: 8 x 4096
+// tokens of 5120 channels, N 16, take 705 us (1.9 TB/s), 640 of them vector
+// issue at 2.4 GHz; 1 x 65536 of 2048 take 838 us in two passes.
 //
 // A sequence is walked in order, tile by tile (see selective_scan.h for the
 // split over lanes).  Where sequences and channels alone do not fill the chip
@@ -129,11 +131,11 @@ __global__ __launch_bounds__(256) void sel_step_kernel(
 //   * Sequences and channels alone fill the chip (400 workgroups or more with 2
 //     states per lane): one segment, as a second pass over the tokens costs
 //     more than idle lanes.  2 states per lane give twice the wavefronts of 4
-//     (8 x 4096 tokens, 5120 channels, N 16: 741 us against 882, 5 wavefronts
+//     (8 x 4096 tokens, 5120 channels, N 16: 705 us against 890, 5 wavefronts
 //     per SIMD against 2.5), but 4 do less work per state once they fill it too
-//     (16 x 2048 tokens: 705 us against 713).
+//     (16 x 2048 tokens: 682 us against 759).
 //   * Else segments of at least 64 tokens, enough for 2048 workgroups of the
-//     4-state form (1 x 4096 tokens, 5120 channels: 153 us in 32 segments, 285
+//     4-state form (1 x 4096 tokens, 5120 channels: 144 us in 32 segments, 282
 //     us in one).
 struct Cut {
     int ks;

@@ -15,10 +15,12 @@
 // the state before every 16th token; the reverse pass then recomputes a
 // tile's 16 states into registers (4 per lane and token) and walks them
 // backwards, so every h_{t-1} is exact, never divided out.  Sums over n are
-// made on the S lanes of a channel.  Sums over channels (dB, dC: 8 values per
-// lane and token) halve the values with every lane distance (permlane32 and
-// permlane16 swaps), then rotate within a row; wavefronts are joined in LDS
-// and channel blocks by a last kernel.  Every sum has a fixed order.
+// made on the S lanes of a channel.  Sums over channels (dB, dC: 2 KS values
+// per lane and token) pass through LDS, where each lane adds up a share of the
+// wavefront's; the wavefronts are joined there too, and channel blocks by a
+// last kernel.  Every sum has a fixed order.  (4 x 2048 tokens of 2048 channels,
+// N 16: the reverse pass takes 277 us, with the values swapped between lanes
+// 284, with matrix instructions that add them up 459.)
 //
 // With several segments per sequence (few rows, see segments() of the forward)
 // the first pass starts each segment from zero and the reverse pass adds the
@@ -56,7 +58,7 @@ __global__ __launch_bounds__(256) void sel_adj_kernel(
     typedef BTile<N, KS> Bt;
     constexpr int S = Sp::S, CPW = Sp::CPW, CB = Sp::CB;
     constexpr int VPR = Bt::VPR, NI = Bt::NI, ITEMS = Bt::ITEMS, BC = Bt::BC;
-    __shared__ __align__(16) float2 sdy[TB][CB];   // (d, dyp)
+    __shared__ __align__(16) float sdy[2][TB][CB];   // d, dyp
     __shared__ __align__(16) float sc[TB][N];
     const int tid = threadIdx.x;
     const uint32_t cb = blockIdx.x % (uint32_t)g.ncb;
@@ -102,9 +104,10 @@ __global__ __launch_bounds__(256) void sel_adj_kernel(
                         if constexpr (GATE) p[j] *= fast_silu((&zv.x)[j]);
                     }
                 }
-                float4 *w = reinterpret_cast<float4 *>(&sdy[r][4 * sv]);
-                w[0] = make_float4(d[0], p[0], d[1], p[1]);
-                w[1] = make_float4(d[2], p[2], d[3], p[3]);
+                *reinterpret_cast<float4 *>(&sdy[0][r][4 * sv]) =
+                    make_float4(d[0], d[1], d[2], d[3]);
+                *reinterpret_cast<float4 *>(&sdy[1][r][4 * sv]) =
+                    make_float4(p[0], p[1], p[2], p[3]);
             }
         }
         for (int e = tid; e < BC; e += 256) {
@@ -116,7 +119,7 @@ __global__ __launch_bounds__(256) void sel_adj_kernel(
         lds_barrier();
 #pragma unroll
         for (int t = TB - 1; t >= 0; --t) {
-            const float2 w = sdy[t][cl];
+            const float2 w = make_float2(sdy[0][t][cl], sdy[1][t][cl]);
             float cv[KS];
             load_ks(&sc[t][KS * s], cv);
 #pragma unroll
@@ -191,11 +194,11 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
     constexpr int S = Sp::S, CPW = Sp::CPW, CB = Sp::CB;
     constexpr int VPR = Bt::VPR, NI = Bt::NI, ITEMS = Bt::ITEMS;
     constexpr int BC = Bt::BC, NBC = (BC + 255) / 256, ROWS = Bt::ROWS;
-    __shared__ __align__(16) float2 sdu[TB][CB];          // (d, d x)
+    __shared__ __align__(16) float sdu[2][TB][CB];        // d, d x
     __shared__ __align__(16) float sdy[TB][CB];           // dyp
     __shared__ __align__(16) float sbc[2][TB][N];
-    __shared__ __align__(16) float2 sgd[TB][CB];          // (gB, sum q a2)
-    __shared__ __align__(16) float sy[GATE ? TB : 1][GATE ? CB : 4];
+    __shared__ __align__(16) float sgd[2][TB][Sp::ROW];   // gB, sum q a2
+    __shared__ __align__(16) float sy[GATE ? TB : 1][GATE ? Sp::ROW : 4];
     __shared__ __align__(16) float sdbc[4][TB][2 * N];
     __shared__ __align__(16) float ssp[TB][CB];                        // softplus'
     __shared__ __align__(16) float ssz[GATE ? TB : 1][GATE ? CB : 4];   // sigmoid(z)
@@ -334,13 +337,15 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
                         p[j] *= (&zv.x)[j] * sz[j];
                     }
                 }
-                *reinterpret_cast<float4 *>(&ssp[r][4 * sv]) = make_float4(sp[0], sp[1], sp[2], sp[3]);
+                *reinterpret_cast<float4 *>(&ssp[r][4 * sv]) =
+                    make_float4(sp[0], sp[1], sp[2], sp[3]);
                 if constexpr (GATE)
                     *reinterpret_cast<float4 *>(&ssz[r][4 * sv]) =
                         make_float4(sz[0], sz[1], sz[2], sz[3]);
-                float4 *w = reinterpret_cast<float4 *>(&sdu[r][4 * sv]);
-                w[0] = make_float4(dkeep[i][0], u[0], dkeep[i][1], u[1]);
-                w[1] = make_float4(dkeep[i][2], u[2], dkeep[i][3], u[3]);
+                *reinterpret_cast<float4 *>(&sdu[0][r][4 * sv]) =
+                    make_float4(dkeep[i][0], dkeep[i][1], dkeep[i][2], dkeep[i][3]);
+                *reinterpret_cast<float4 *>(&sdu[1][r][4 * sv]) =
+                    make_float4(u[0], u[1], u[2], u[3]);
                 *reinterpret_cast<float4 *>(&sdy[r][4 * sv]) = make_float4(p[0], p[1], p[2], p[3]);
             }
         }
@@ -371,7 +376,7 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
         float H[TB][KS];
         {
             auto load_op = [&](int t, Op &o) {
-                o.w = sdu[t][cl];
+                o.w = make_float2(sdu[0][t][cl], sdu[1][t][cl]);
                 load_ks(&sbc[0][t][KS * s], o.bv);
                 if constexpr (GATE) load_ks(&sbc[1][t][KS * s], o.cv);
             };
@@ -455,7 +460,7 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
         };
         {
             auto load_op = [&](int t, Op &o) {
-                o.w = sdu[t][cr];
+                o.w = make_float2(sdu[0][t][cr], sdu[1][t][cr]);
                 o.p = sdy[t][cr];
                 load_ks(&sbc[0][t][sr], o.bv);
                 load_ks(&sbc[1][t][sr], o.cv);
@@ -507,7 +512,8 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
 #pragma unroll
                     for (int i = 0; i < KS; ++i) a[i] = an[i];
                 }
-                sgd[tq + s][cl] = make_float2(lane_sums<S>(pg, s), lane_sums<S>(pq, s));
+                sgd[0][tq + s][cl] = lane_sums<S>(pg, s);
+                sgd[1][tq + s][cl] = lane_sums<S>(pq, s);
             }
         }
         red_add(0);
@@ -524,9 +530,8 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
             if (e < ITEMS && t < t1 && chn > 0) {
                 const float4 xv = widen4(tok[i].x), yv = tok[i].dy.v;
                 const float4 zv = widen4(tok[i].z);
-                const float4 *w = reinterpret_cast<const float4 *>(&sgd[r][4 * sv]);
-                const float4 w0 = w[0], w1 = w[1];
-                const float gb[4] = {w0.x, w0.z, w1.x, w1.z}, qa[4] = {w0.y, w0.w, w1.y, w1.w};
+                const float4 gb = *reinterpret_cast<const float4 *>(&sgd[0][r][4 * sv]);
+                const float4 qa = *reinterpret_cast<const float4 *>(&sgd[1][r][4 * sv]);
                 const float4 sp = *reinterpret_cast<const float4 *>(&ssp[r][4 * sv]);
                 const float4 pv = *reinterpret_cast<const float4 *>(&sdy[r][4 * sv]);
                 float4 ys = make_float4(0.f, 0.f, 0.f, 0.f), sz = ys;
@@ -544,8 +549,8 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
                         oz[j] = (&yv.x)[j] * ((&ys.x)[j] + Dv[j] * xj) *
                                 (s * fmaf(zj, 1.f - s, 1.f));
                     }
-                    ox[j] = fmaf(dkeep[i][j], gb[j], Dv[j] * p);
-                    od[j] = fmaf(xj, gb[j], qa[j] * kLn2) * (&sp.x)[j];
+                    ox[j] = fmaf(dkeep[i][j], (&gb.x)[j], Dv[j] * p);
+                    od[j] = fmaf(xj, (&gb.x)[j], (&qa.x)[j] * kLn2) * (&sp.x)[j];
                     accD[j] = fmaf(p, xj, accD[j]);
                     accb[j] += od[j];
                 }
@@ -578,7 +583,7 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
     }
     // sums over this block's token rows
     __syncthreads();
-    float(*red)[CB] = reinterpret_cast<float(*)[CB]>(&sdu[0][0]);   // [2 ROWS][CB]
+    float(*red)[CB] = reinterpret_cast<float(*)[CB]>(&sdu[0][0][0]);   // [2 ROWS][CB]
     if (st < ROWS * VPR) {
         const int r = st / VPR;
         *reinterpret_cast<float4 *>(&red[r][4 * sv]) =
@@ -672,12 +677,13 @@ BwdPlan plan(const SelArgs &a) {
             const int64_t seg = cdiv64(tiles, n), nseg = cdiv64(tiles, seg);
             const double blocks = (double)(a.Bt * ncb * nseg), len = (double)seg;
             const double rounds = (double)cdiv64(a.Bt * ncb * nseg, 512);
-            const double work = blocks * len / 512.0;
+            const double work = blocks * len / 512.0, least = 0.75 * len;
             const double passes = 2.0 - 1.0 / (double)nseg;
             const double cost =
                 (ks == 2 ? 0.62 : 1.0) *
-                    (rounds * (len + 0.5) + 0.24 * passes * (work > 0.75 * len ? work : 0.75 * len) *
-                                                (0.8 + 240.0 / (blocks > 256.0 ? blocks : 256.0))) +
+                    (rounds * (len + 0.5) +
+                     0.24 * passes * (work > least ? work : least) *
+                         (0.8 + 240.0 / (blocks > 256.0 ? blocks : 256.0))) +
                 (nseg > 1 ? 0.5 + 0.01 * (double)nseg : 0.0);
             if (p.ks == 0 || cost < best) {
                 best = cost;

@@ -791,7 +791,8 @@ def _scan_tokens(x, dt, A, B, C, D, names):
     if A.dim() != 2:
         raise ValueError("A must be [Dm,N]")
     N = A.shape[1]
-    return (dev, _in(x, names[0], x.dtype, lead + (Dm,), dev), _in(dt, names[1], x.dtype, lead + (Dm,), dev),
+    return (dev, _in(x, names[0], x.dtype, lead + (Dm,), dev),
+            _in(dt, names[1], x.dtype, lead + (Dm,), dev),
             _in(A, "A", torch.float32, (Dm, N), dev),
             _in(B, names[2], x.dtype, lead + (N,), dev),
             _in(C, names[3], x.dtype, lead + (N,), dev),

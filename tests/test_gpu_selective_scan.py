@@ -393,7 +393,7 @@ def test_offsets_past_32_bits():
     y, fin = run(0, T, None)
     last, fin = y[:, cut:].float().clone(), fin.clone()
     del y
-    # (tokens 500 back reach the end through exp(-sum of d) below 1e-9, so two starts agree)
+    # (tokens 2000 back reach the end through exp(-sum of d) below 1e-9, so two starts agree)
     _, h = run(cut - 2000, cut, None)
     yt, ft = run(cut, T, h)
     # bf16 outputs, off by half a step each, and float32 sums of 16 states and their decay
