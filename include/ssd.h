@@ -415,6 +415,12 @@ ssd_status ssd_chunked_bwd(const void *x, const float *dt, const float *A, const
                            size_t workspace_bytes, void *stream);
 
 /*
+ * Of the arguments of the calls below, an output may overlap another argument
+ * only where that is said; any other overlap is undefined.  Calls that share a
+ * workspace must be ordered (one stream, or events).
+ */
+
+/*
  * The short causal convolution in front of the scan ("Optimizing Nemotron v3
  * Super in TensorRT-LLM", section on CausalConv1d; the layer's in_proj ->
  * causal conv1d -> SiLU -> scan order): per channel c of C = channels[0] +

@@ -241,7 +241,7 @@ __global__ __launch_bounds__(256) void conv1d_fwd_kernel(
 // One token per sequence: the window is the slot's state and the new token;
 // the state moves up by one row in place.  A lane serves R sequences so that
 // its weights (as many bytes as a sequence's whole traffic) are read once for
-// all of them (512 sequences, 5120 channels, bf16: 9.4 us, 4.5 TB/s).
+// all of them (256 sequences, 10240 channels, bf16: 9.4 us, 4.5 TB/s).
 template <typename Tio, int W, int R, bool RAG>
 __global__ __launch_bounds__(256) void conv1d_step_kernel(
     Tio *__restrict__ state, const int32_t *__restrict__ slots, int64_t nslots,
@@ -476,12 +476,18 @@ int64_t vectors(const ConvArgs &a) {
     return cdiv(a.ch[0], kVec) + cdiv(a.ch[1], kVec) + cdiv(a.ch[2], kVec);
 }
 // Tokens per lane: long runs reread few rows and weights, short ones fill the
-// chip when there are few sequences or channels: 2^18 lanes or more (half of
-// the chip's) forward, 2^17 backward, where a lane holds twice the registers
-// (4 x 2048 tokens, 2304 channels: 51 us in runs of 32, 55 in runs of 16).
+// chip when there are few sequences or channels.  Forward runs of 32 where that
+// leaves 2^18 lanes (half of the chip's; 8 x 4096 tokens, 5376 channels: 126 us,
+// runs of 16 135; 4 x 2048 tokens, 2304 channels, 2^17 lanes: 19.3, runs of 16
+// 18.1), runs under 16 only to reach 2^17 (1 x 1024 tokens, 5376 channels: 8.7
+// us in runs of 8, 2^17 lanes, 9.4 in 16, 10.4 in 4).  Backward, where a lane
+// holds twice the registers, 2^17 (4 x 2048 tokens, 2304 channels: 51 us in
+// runs of 32, 55 in runs of 16).
 int64_t run_length(const ConvArgs &a, int64_t lanes) {
     int64_t tt = 32;
-    while (tt > 4 && a.Bt * vectors(a) * cdiv(a.T, tt) < lanes) tt >>= 1;
+    while (tt > 4 &&
+           a.Bt * vectors(a) * cdiv(a.T, tt) < (tt > 16 ? lanes : int64_t(1) << 17))
+        tt >>= 1;
     return tt;
 }
 int64_t fwd_run(const ConvArgs &a) { return run_length(a, int64_t(1) << 18); }
@@ -553,8 +559,10 @@ void step_r(const ConvArgs &a, const ConvGeom &g, hipStream_t st) {
 }
 template <typename Tio>
 void step_t(const ConvArgs &a, const ConvGeom &g, hipStream_t st) {
-    // 4 sequences per lane where that still leaves a wavefront per SIMD
-    if (a.Bt * (int64_t)g.nvec >= 4 * 65536)
+    // 4 sequences per lane where that still leaves a wavefront on every other
+    // SIMD (10240 channels: 64 sequences 4.2 us, one per lane 4.6; 256: 8.4,
+    // 10.5; but 32, a wavefront on a third of them: 3.9, 3.7)
+    if (a.Bt * (int64_t)g.nvec >= int64_t(1) << 17)
         step_r<Tio, 4>(a, g, st);
     else
         step_r<Tio, 1>(a, g, st);

@@ -25,7 +25,7 @@ struct SelSplit {
     static constexpr int VPR = CB / 4;     // 4-channel vectors of a tile's row
     // Row of an LDS array that a channel's lanes write as S tokens at once: rows
     // are moved on by 32 / S banks, so that they do not meet in one (conflict
-    // cycles of 8 x 4096 tokens, 5120 channels: 3 million, 47 without; 705 us, 718)
+    // cycles of 8 x 4096 tokens, 5120 channels: 13 million, 47 without; 705 us, 718)
     static constexpr int ROW = CB + (S <= 2 ? 16 : (S == 4 ? 8 : 4));
     static constexpr int BC = TL * N / 4;  // 4-element vectors of a tile's B (or C)
     static constexpr int NBC = (BC + 255) / 256;   // of them per thread

@@ -5,8 +5,8 @@
 // Both directions move each element once and are bound by memory.  A lane
 // holds 4 consecutive elements (16 bytes of the state, 4 of codes), 16 lanes
 // hold a block, whose maximum is formed by DPP moves; a lane serves kIter
-// such groups, all loaded before any is used.  (256 slots of 163840 elements,
-// float32: write 35 us, 6.0 TB/s; read 31 us, 6.8 TB/s, part of it from the
+// such groups, all loaded before any is used.  (64 states of 655360 elements,
+// int8: write 35 us, 6.0 TB/s; read 31 us, 6.8 TB/s, part of it from the
 // memory-side cache.)
 
 #include "layer_launch.h"
