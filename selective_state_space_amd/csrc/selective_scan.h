@@ -3,9 +3,9 @@
 //
 // Work split: a channel's N states lie on S = N/KS neighbouring lanes, KS (4 or
 // 2) per lane, so a wavefront holds 64/S channels and a workgroup of 4
-// wavefronts CB = 256/S.  Token tiles pass through LDS: 16-byte row segments are loaded,
-// d = softplus(dt + bias) and u = d x formed once per (token, channel), and
-// the scanning lanes then read (d, u) of their channel and their
+// wavefronts CB = 256/S.  Token tiles pass through LDS: lanes load 4 channels
+// of a token, d = softplus(dt + bias) and u = d x are formed once per (token,
+// channel), and the scanning lanes then read (d, u) of their channel and their
 // KS elements of B and C.
 #pragma once
 
