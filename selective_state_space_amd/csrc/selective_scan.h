@@ -267,7 +267,7 @@ struct SelGeom {
     int32_t softplus;
 };
 
-// One segment of one sequence, CB channels.
+// One segment of one sequence, CB channels (block blk of the launch's).
 //   SCAN_OUT   write y, and the last segment the final state;
 //   SCAN_END   write the segment's end state, started from zero, and its sum of
 //              d (every segment but the last);
@@ -276,12 +276,12 @@ struct SelGeom {
 //              the end states and sums of d.
 enum ScanMode { SCAN_OUT, SCAN_END, SCAN_CKPT };
 template <int N, int KS, typename Tio, typename Ty, bool GATE, bool RAG, ScanMode MODE>
-__global__ __launch_bounds__(256) void sel_scan_kernel(
+__device__ __forceinline__ void sel_scan(
     const Tio *__restrict__ x, const Tio *__restrict__ dt, const float *__restrict__ A,
     const Tio *__restrict__ B, const Tio *__restrict__ C, const float *__restrict__ D,
     const Tio *__restrict__ z, const float *__restrict__ dt_bias, const float *start,
     const int32_t *__restrict__ lens, Ty *__restrict__ y, float *fin, float *__restrict__ dsum,
-    float *__restrict__ ckpt, float *__restrict__ cumd, SelGeom g) {
+    float *__restrict__ ckpt, float *__restrict__ cumd, SelGeom g, uint32_t blk) {
     constexpr bool OUT = MODE == SCAN_OUT;
     typedef SelSplit<N, KS> Sp;
     constexpr int S = Sp::S, CPW = Sp::CPW, CB = Sp::CB, TL = Sp::TL, VPR = Sp::VPR;
@@ -291,8 +291,8 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(
     __shared__ __align__(16) float sy[OUT ? TL : 1][OUT ? Sp::ROW : 4];
 
     const int tid = threadIdx.x;
-    const uint32_t cb = blockIdx.x % (uint32_t)g.ncb;
-    const uint32_t rest = blockIdx.x / (uint32_t)g.ncb;
+    const uint32_t cb = blk % (uint32_t)g.ncb;
+    const uint32_t rest = blk / (uint32_t)g.ncb;
     const uint32_t nsg = MODE == SCAN_END ? g.nseg - 1 : g.nseg;
     const int64_t b = rest / nsg;
     const int32_t seg = rest % nsg;
@@ -470,6 +470,16 @@ __global__ __launch_bounds__(256) void sel_scan_kernel(
         store_ks(fin + u * N + KS * s, h);
         if (s == 0) dsum[u] = ds;
     }
+}
+template <int N, int KS, typename Tio, typename Ty, bool GATE, bool RAG, ScanMode MODE>
+__global__ __launch_bounds__(256) void sel_scan_kernel(
+    const Tio *__restrict__ x, const Tio *__restrict__ dt, const float *__restrict__ A,
+    const Tio *__restrict__ B, const Tio *__restrict__ C, const float *__restrict__ D,
+    const Tio *__restrict__ z, const float *__restrict__ dt_bias, const float *start,
+    const int32_t *__restrict__ lens, Ty *__restrict__ y, float *fin, float *__restrict__ dsum,
+    float *__restrict__ ckpt, float *__restrict__ cumd, SelGeom g) {
+    sel_scan<N, KS, Tio, Ty, GATE, RAG, MODE>(x, dt, A, B, C, D, z, dt_bias, start, lens, y, fin,
+                                              dsum, ckpt, cumd, g, blockIdx.x);
 }
 
 // f(integral_constant<N>, io type)

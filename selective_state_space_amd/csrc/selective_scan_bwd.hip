@@ -48,12 +48,12 @@ struct BTile {
 };
 
 // The adjoint leaving a segment at its first token, started from zero after
-// its last one (segments 1 .. nseg-1).
+// its last one (segments 1 .. nseg-1; block blk of theirs).
 template <int N, int KS, typename Tio, bool GATE, bool RAG>
-__global__ __launch_bounds__(256) void sel_adj_kernel(
+__device__ __forceinline__ void sel_adj(
     const Tio *__restrict__ dt, const float *__restrict__ A, const Tio *__restrict__ C,
     const Tio *__restrict__ z, const float *__restrict__ dt_bias, const float *__restrict__ dy,
-    float *__restrict__ adj, SelGeom g) {
+    float *__restrict__ adj, const SelGeom &g, uint32_t blk) {
     typedef SelSplit<N, KS> Sp;
     typedef BTile<N, KS> Bt;
     constexpr int S = Sp::S, CPW = Sp::CPW, CB = Sp::CB;
@@ -61,8 +61,8 @@ __global__ __launch_bounds__(256) void sel_adj_kernel(
     __shared__ __align__(16) float sdy[2][TB][CB];   // d, dyp
     __shared__ __align__(16) float sc[TB][N];
     const int tid = threadIdx.x;
-    const uint32_t cb = blockIdx.x % (uint32_t)g.ncb;
-    const uint32_t rest = blockIdx.x / (uint32_t)g.ncb;
+    const uint32_t cb = blk % (uint32_t)g.ncb;
+    const uint32_t rest = blk / (uint32_t)g.ncb;
     const int64_t b = rest / (uint32_t)(g.nseg - 1);
     const int32_t seg = 1 + rest % (uint32_t)(g.nseg - 1);
     const int64_t t0 = seg * g.seg_len, t1 = min(g.T, t0 + g.seg_len);
@@ -130,6 +130,25 @@ __global__ __launch_bounds__(256) void sel_adj_kernel(
     }
     if (c < g.Dm)
         store_ks(adj + (((b * g.nseg) + seg) * g.Dm + c) * N + KS * s, car);
+}
+
+// Both passes over the segments in one launch, as neither needs the other: the
+// first `scans` blocks checkpoint the states, the rest form the adjoints (all
+// gradients of 2 x 333 tokens, 777 channels, N 32: 47 us, in two launches 53;
+// 4 x 2048 x 2048, N 16: 365 us, 372).
+template <int N, int KS, typename Tio, bool GATE, bool RAG>
+__global__ __launch_bounds__(256) void sel_ends_kernel(
+    const Tio *__restrict__ x, const Tio *__restrict__ dt, const float *__restrict__ A,
+    const Tio *__restrict__ B, const Tio *__restrict__ C, const Tio *__restrict__ z,
+    const float *__restrict__ dt_bias, const float *__restrict__ dy, float *__restrict__ hseg,
+    float *__restrict__ dsum, float *__restrict__ ckpt, float *__restrict__ cumd,
+    float *__restrict__ adj, uint32_t scans, SelGeom g) {
+    if (blockIdx.x < scans)
+        sel_scan<N, KS, Tio, float, false, RAG, SCAN_CKPT>(
+            x, dt, A, B, nullptr, nullptr, nullptr, dt_bias, nullptr, nullptr, nullptr, hseg, dsum,
+            ckpt, cumd, g, blockIdx.x);
+    else
+        sel_adj<N, KS, Tio, GATE, RAG>(dt, A, C, z, dt_bias, dy, adj, g, blockIdx.x - scans);
 }
 
 // Both chains over the segments: the states entering each (hseg, in place of
@@ -655,9 +674,9 @@ __global__ __launch_bounds__(256) void sel_sum_kernel(SumJobs jobs) {
 //     tile, less where more workgroups hide their waits (58 us with 2048, 75
 //     with 512);
 //   * 2 states per lane take 0.62 of 4.
-// The cheapest is taken (8 x 1024 tokens, 5120 channels: 958 us whole, 860 us
-// in 4 segments; 16 x 512 x 2048: 317 us whole, 372 in 4; 4 x 2048 x 2048: 925
-// whole, 405 in 4, 374 in 16).
+// The cheapest is taken (8 x 1024 tokens, 5120 channels: 934 us whole, 851 us
+// in 4 segments; 16 x 512 x 2048: 320 us whole, 361 in 4; 4 x 2048 x 2048: 883
+// whole, 390 in 4, 374 in 16).
 // (N 8 with 4 states per lane would spill registers)
 constexpr int bwd_most_ks(int N) { return N == 8 ? 2 : 4; }
 struct BwdPlan {
@@ -725,7 +744,7 @@ bool selective_scan_bwd_fits(const SelArgs &a) {
     // the widest of the passes, the chain over segments and the last sums
     const double sums = ((double)a.Bt * (double)a.T * 2.0 + (double)a.Dm) * a.N / 64.0 +
                         (double)a.Dm / 32.0 + 4.0;
-    return (double)a.Bt * (double)p.nseg * (double)p.ncb <= (double)kMaxBlocks &&
+    return (double)a.Bt * (2.0 * (double)p.nseg - 1.0) * (double)p.ncb <= (double)kMaxBlocks &&
            (double)a.Bt * (double)a.Dm * (double)a.N <= 256.0 * (double)kMaxBlocks &&
            sums <= (double)kMaxBlocks;
 }
@@ -760,25 +779,27 @@ hipError_t launch_selective_scan_bwd(const SelArgs &a, hipStream_t st) {
                 });
             });
         };
-        each([&](auto n, auto ks, auto io, auto r) {
-            typedef decltype(io) Tio;
-            sel_scan_kernel<decltype(n)::value, decltype(ks)::value, Tio, float, false,
-                            decltype(r)::value, SCAN_CKPT>
-                <<<dim3((uint32_t)(rows * g.ncb)), 256, 0, st>>>(
+        const uint32_t scans = (uint32_t)(rows * g.ncb);
+        if (!split) {
+            each([&](auto n, auto ks, auto io, auto r) {
+                typedef decltype(io) Tio;
+                sel_scan_kernel<decltype(n)::value, decltype(ks)::value, Tio, float, false,
+                                decltype(r)::value, SCAN_CKPT><<<dim3(scans), 256, 0, st>>>(
                     (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B, nullptr, nullptr,
-                    nullptr, a.dt_bias, split ? nullptr : a.init, nullptr, nullptr, ws + p.hseg,
-                    ws + p.dsum, ws + p.ckpt, ws + p.cumd, g);
-        });
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        if (split) {
+                    nullptr, a.dt_bias, a.init, nullptr, nullptr, ws + p.hseg, ws + p.dsum,
+                    ws + p.ckpt, ws + p.cumd, g);
+            });
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        } else {
             each([&](auto n, auto ks, auto io, auto r) {
                 typedef decltype(io) Tio;
                 by_flag(a.z != nullptr, [&](auto gate) {
-                    sel_adj_kernel<decltype(n)::value, decltype(ks)::value, Tio,
-                                   decltype(gate)::value, decltype(r)::value>
-                        <<<dim3((uint32_t)(a.Bt * (p.nseg - 1) * g.ncb)), 256, 0, st>>>(
-                            (const Tio *)a.dt, a.A, (const Tio *)a.C, (const Tio *)a.z, a.dt_bias,
-                            a.dy, ws + p.adj, g);
+                    sel_ends_kernel<decltype(n)::value, decltype(ks)::value, Tio,
+                                    decltype(gate)::value, decltype(r)::value>
+                        <<<dim3(scans + (uint32_t)(a.Bt * (p.nseg - 1) * g.ncb)), 256, 0, st>>>(
+                            (const Tio *)a.x, (const Tio *)a.dt, a.A, (const Tio *)a.B,
+                            (const Tio *)a.C, (const Tio *)a.z, a.dt_bias, a.dy, ws + p.hseg,
+                            ws + p.dsum, ws + p.ckpt, ws + p.cumd, ws + p.adj, scans, g);
                 });
             });
             if ((e = hipGetLastError()) != hipSuccess) return e;
