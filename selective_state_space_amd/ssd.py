@@ -614,15 +614,16 @@ def _current_stream(dev: torch.device) -> int:
 
 
 # torch's raw handle of the current stream (what current_stream wraps, at a tenth of its
-# cost per call), where this torch has it
+# cost per call) and its current device, where this torch has them
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(fn: str, dev: torch.device, *args):
     """One library call on dev's current stream, with dev the current device."""
     f = getattr(load_library(), fn)
     stream = _current_stream(dev) if _raw_stream is None else _raw_stream(dev.index)
-    if torch.cuda.current_device() == dev.index:
+    if _raw_device() == dev.index:
         st = f(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -679,9 +680,11 @@ def _conv_args(x, weight, bias, splits, silu, tokens: int):
     return dims, x, weight, bias, splits, dev
 
 
+# (torch.empty takes sizes one by one faster than as a tuple, 1.0 us against 1.4: of a short
+# call's 14 us two thirds are the host's)
 def _outs(y, name, dtype, shapes, dev):
     if y is None:
-        return tuple([torch.empty(s, dtype=dtype, device=dev) for s in shapes])
+        return tuple([torch.empty(*s, dtype=dtype, device=dev) for s in shapes])
     if isinstance(y, torch.Tensor):
         y = (y,)
     if len(y) != len(shapes):
@@ -711,9 +714,9 @@ def ssd_conv1d_fwd(x, weight, bias=None, silu: bool = True, splits=None, init_st
     if final_state is not None:
         final_state = _need_out(final_state, "final_state", x.dtype, (Bt, W - 1, C), dev)
     elif want_final:
-        final_state = torch.empty((Bt, W - 1, C), dtype=x.dtype, device=dev)
+        final_state = torch.empty(Bt, W - 1, C, dtype=x.dtype, device=dev)
     y = _outs(y, "y", x.dtype, [(Bt, T, c) for c in splits], dev)
-    _call("ssd_conv1d_fwd", dev, _addr(x), _addr(weight), _addr(bias), _addr(init_state),
+    _call("ssd_conv1d_fwd", dev, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(init_state),
           _addr(seq_lens), _parts3(y + (None,) * (3 - len(y))), _addr(final_state),
           ctypes.byref(dims))
     return y, final_state
@@ -736,8 +739,8 @@ def ssd_conv1d_step(conv_state, x_t, weight, bias=None, silu: bool = True, split
                            (conv_state.shape[0], weight.shape[1] - 1, C), dev)
     slots = _opt(slots, "slots", torch.int32, (Bt,), dev)
     y_t = _outs(y_t, "y_t", x_t.dtype, [(Bt, c) for c in splits], dev)
-    _call("ssd_conv1d_step", dev, _addr(conv_state), conv_state.shape[0], _addr(slots),
-          _addr(x_t), _addr(weight), _addr(bias), _parts3(y_t + (None,) * (3 - len(y_t))),
+    _call("ssd_conv1d_step", dev, conv_state.data_ptr(), conv_state.shape[0], _addr(slots),
+          x_t.data_ptr(), weight.data_ptr(), _addr(bias), _parts3(y_t + (None,) * (3 - len(y_t))),
           ctypes.byref(dims))
     return y_t
 
@@ -765,12 +768,12 @@ def ssd_conv1d_bwd(x, weight, dy, bias=None, silu: bool = True, init_state=None,
         workspace = torch.empty(max(ssd_conv1d_bwd_workspace_size(dims), 16), dtype=torch.uint8,
                                 device=dev)
     f32 = dict(dtype=torch.float32, device=dev)
-    out = dict(dx=torch.empty((Bt, T, C), **f32), dweight=torch.empty((C, W), **f32),
-               dbias=None if bias is None else torch.empty((C,), **f32),
-               dinit=torch.empty((Bt, W - 1, C), **f32) if want_dinit else None)
-    _call("ssd_conv1d_bwd", dev, _addr(x), _addr(weight), _addr(bias), _addr(init_state),
-          _parts3(dy + (None,) * (3 - len(dy))), _addr(dfinal), _addr(out["dx"]),
-          _addr(out["dweight"]), _addr(out["dbias"]), _addr(out["dinit"]), ctypes.byref(dims),
+    out = dict(dx=torch.empty(Bt, T, C, **f32), dweight=torch.empty(C, W, **f32),
+               dbias=None if bias is None else torch.empty(C, **f32),
+               dinit=torch.empty(Bt, W - 1, C, **f32) if want_dinit else None)
+    _call("ssd_conv1d_bwd", dev, x.data_ptr(), weight.data_ptr(), _addr(bias), _addr(init_state),
+          _parts3(dy + (None,) * (3 - len(dy))), _addr(dfinal), out["dx"].data_ptr(),
+          out["dweight"].data_ptr(), _addr(out["dbias"]), _addr(out["dinit"]), ctypes.byref(dims),
           _addr(workspace), workspace.numel() * workspace.element_size())
     return out
 
@@ -827,17 +830,18 @@ def ssd_selective_scan_fwd(x, dt, A, B, C, D, init_state=None, y=None, final_sta
     init_state = _opt(init_state, "init_state", torch.float32, (Bt, Dm, N), dev)
     seq_lens = _opt(seq_lens, "seq_lens", torch.int32, (Bt,), dev)
     ydt = x.dtype if y_io_dtype else torch.float32
-    y = (torch.empty((Bt, T, Dm), dtype=ydt, device=dev) if y is None
+    y = (torch.empty(Bt, T, Dm, dtype=ydt, device=dev) if y is None
          else _need_out(y, "y", ydt, (Bt, T, Dm), dev))
     if final_state is not None:
         final_state = _need_out(final_state, "final_state", torch.float32, (Bt, Dm, N), dev)
     elif want_final:
-        final_state = torch.empty((Bt, Dm, N), dtype=torch.float32, device=dev)
+        final_state = torch.empty(Bt, Dm, N, dtype=torch.float32, device=dev)
     if workspace is None:
         need = ssd_selective_scan_workspace_size(dims)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call("ssd_selective_scan_fwd", dev, _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
-          _addr(D), _addr(init_state), _addr(seq_lens), _addr(y), _addr(final_state),
+    _call("ssd_selective_scan_fwd", dev, x.data_ptr(), dt.data_ptr(), A.data_ptr(),
+          B.data_ptr(), C.data_ptr(), D.data_ptr(), _addr(init_state), _addr(seq_lens),
+          y.data_ptr(), _addr(final_state),
           None if opts is None else ctypes.byref(opts), ctypes.byref(dims), _addr(workspace),
           0 if workspace is None else workspace.numel() * workspace.element_size())
     return y, final_state
@@ -864,11 +868,12 @@ def ssd_selective_scan_step(state, x_t, dt_t, A, B_t, C_t, D, slots=None, y_t=No
     slots = _opt(slots, "slots", torch.int32, (Bt,), dev)
     opts, dt_bias, z_t = _scan_layer(x_t, dt_bias, dt_softplus, z_t, "z_t", y_io_dtype, Dm, dev)
     ydt = x_t.dtype if y_io_dtype else torch.float32
-    y_t = (torch.empty((Bt, Dm), dtype=ydt, device=dev) if y_t is None
+    y_t = (torch.empty(Bt, Dm, dtype=ydt, device=dev) if y_t is None
            else _need_out(y_t, "y_t", ydt, (Bt, Dm), dev))
     dims = ScanDims(Bt, 1, Dm, N, _io_code(x_t.dtype))
-    _call("ssd_selective_scan_step", dev, _addr(state), state.shape[0], _addr(slots), _addr(x_t),
-          _addr(dt_t), _addr(A), _addr(B_t), _addr(C_t), _addr(D), _addr(y_t),
+    _call("ssd_selective_scan_step", dev, state.data_ptr(), state.shape[0], _addr(slots),
+          x_t.data_ptr(), dt_t.data_ptr(), A.data_ptr(), B_t.data_ptr(), C_t.data_ptr(),
+          D.data_ptr(), y_t.data_ptr(),
           None if opts is None else ctypes.byref(opts), ctypes.byref(dims))
     return y_t
 
@@ -898,16 +903,17 @@ def ssd_selective_scan_bwd(x, dt, A, B, C, D, dy, init_state=None, dfinal=None, 
         workspace = torch.empty(max(ssd_selective_scan_bwd_workspace_size(dims), 16),
                                 dtype=torch.uint8, device=dev)
     f32 = dict(dtype=torch.float32, device=dev)
-    out = dict(dx=torch.empty((Bt, T, Dm), **f32), ddt=torch.empty((Bt, T, Dm), **f32),
-               dA=torch.empty((Dm, N), **f32), dB=torch.empty((Bt, T, N), **f32),
-               dC=torch.empty((Bt, T, N), **f32), dD=torch.empty((Dm,), **f32),
-               ddt_bias=None if dt_bias is None else torch.empty((Dm,), **f32),
-               dz=None if z is None else torch.empty((Bt, T, Dm), **f32),
-               dinit=torch.empty((Bt, Dm, N), **f32) if want_dinit else None)
-    _call("ssd_selective_scan_bwd", dev, _addr(x), _addr(dt), _addr(A), _addr(B), _addr(C),
-          _addr(D), _addr(init_state), _addr(dy), _addr(dfinal), _addr(out["dx"]),
-          _addr(out["ddt"]), _addr(out["dA"]), _addr(out["dB"]), _addr(out["dC"]),
-          _addr(out["dD"]), _addr(out["ddt_bias"]), _addr(out["dz"]), _addr(out["dinit"]),
+    out = dict(dx=torch.empty(Bt, T, Dm, **f32), ddt=torch.empty(Bt, T, Dm, **f32),
+               dA=torch.empty(Dm, N, **f32), dB=torch.empty(Bt, T, N, **f32),
+               dC=torch.empty(Bt, T, N, **f32), dD=torch.empty(Dm, **f32),
+               ddt_bias=None if dt_bias is None else torch.empty(Dm, **f32),
+               dz=None if z is None else torch.empty(Bt, T, Dm, **f32),
+               dinit=torch.empty(Bt, Dm, N, **f32) if want_dinit else None)
+    _call("ssd_selective_scan_bwd", dev, x.data_ptr(), dt.data_ptr(), A.data_ptr(),
+          B.data_ptr(), C.data_ptr(), D.data_ptr(), _addr(init_state), dy.data_ptr(),
+          _addr(dfinal), out["dx"].data_ptr(),
+          out["ddt"].data_ptr(), out["dA"].data_ptr(), out["dB"].data_ptr(), out["dC"].data_ptr(),
+          out["dD"].data_ptr(), _addr(out["ddt_bias"]), _addr(out["dz"]), _addr(out["dinit"]),
           None if opts is None else ctypes.byref(opts), ctypes.byref(dims), _addr(workspace),
           workspace.numel() * workspace.element_size())
     return out
@@ -937,8 +943,8 @@ def ssd_cache_write(state, codes, scales, slots=None):
         raise ValueError("a state holds %d elements, the pool's rows %d"
                          % (state.numel() // max(n, 1), size))
     slots = _opt(slots, "slots", torch.int32, (n,), dev)
-    _call("ssd_cache_write", dev, _addr(state), n, size, _addr(slots), codes.shape[0],
-          _addr(codes), _addr(scales), CACHE_FORMATS[codes.dtype])
+    _call("ssd_cache_write", dev, state.data_ptr(), n, size, _addr(slots), codes.shape[0],
+          codes.data_ptr(), scales.data_ptr(), CACHE_FORMATS[codes.dtype])
 
 
 def ssd_cache_read(codes, scales, slots=None, shape=None, state=None):
@@ -950,11 +956,11 @@ def ssd_cache_read(codes, scales, slots=None, shape=None, state=None):
     n = codes.shape[0] if slots is None else slots.shape[0]
     slots = _opt(slots, "slots", torch.int32, (n,), dev)
     full = (n, size) if shape is None else (n,) + tuple(shape)
-    state = (torch.empty(full, dtype=torch.float32, device=dev) if state is None
+    state = (torch.empty(*full, dtype=torch.float32, device=dev) if state is None
              else _need_out(state, "state", torch.float32, full, dev))
     if state.numel() != n * size:
         raise ValueError("a state of shape %s does not hold the pool's %d elements"
                          % (full[1:], size))
-    _call("ssd_cache_read", dev, _addr(codes), _addr(scales), n, size, _addr(slots),
-          codes.shape[0], _addr(state), CACHE_FORMATS[codes.dtype])
+    _call("ssd_cache_read", dev, codes.data_ptr(), scales.data_ptr(), n, size, _addr(slots),
+          codes.shape[0], state.data_ptr(), CACHE_FORMATS[codes.dtype])
     return state
