@@ -197,3 +197,39 @@ def test_chained_gradients(kind):
     log("chained gradients", kind)
     for k, t in zip(("dx", "dweight", "dbias"), leaf):
         assert_close(host(got[k]), t.grad.numpy(), gen.F32, k)
+
+
+def test_calls_at_once_on_two_streams():
+    """Calls in flight on two streams, each with workspaces of its own, equal the same calls
+    one after another."""
+    torch.manual_seed(21)
+    bf = torch.bfloat16
+    sets = []
+    for T in (2049, 1111):
+        x, z = (torch.randn(1, T, 96, device="cuda").to(bf) for _ in range(2))
+        B, C = (torch.randn(1, T, 16, device="cuda").to(bf) for _ in range(2))
+        sets.append(dict(x=x, dt=(torch.randn(1, T, 96, device="cuda") - 3).to(bf),
+                         A=-torch.rand(96, 16, device="cuda"), B=B, C=C,
+                         D=torch.randn(96, device="cuda"), z=z, dt_softplus=True))
+    w = torch.randn(96, 4, device="cuda")
+    dy = [torch.randn(1, m["x"].shape[1], 96, device="cuda") for m in sets]
+
+    def calls(m, g):
+        (u,), _ = ssd.ssd_conv1d_fwd(m["x"], w)
+        n = dict(m, x=u)
+        y, fin = ssd.ssd_selective_scan_fwd(**n)
+        out = ssd.ssd_selective_scan_bwd(dy=g, **n)
+        return [u, y, fin] + [out[k] for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz")]
+
+    want = [calls(m, g) for m, g in zip(sets, dy)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(4):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(calls(sets[i], dy[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for one in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(one, want[i]))
