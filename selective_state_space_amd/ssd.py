@@ -214,6 +214,19 @@ def _need_out(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device) -> 
     return _need(t, name, dtype, shape, device)
 
 
+def _own_workspace(t: torch.Tensor, device) -> torch.Tensor:
+    """A workspace of the caller's.  The library checks its size and alignment but sees
+    an address alone: that the memory is the GPU's, and as long as its element count
+    says, is checked here."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError("workspace is on %s, expected %s" % (t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t
+
+
 def fwd_dims(x: torch.Tensor, B: torch.Tensor) -> Dims:
     Bt, T, H, P = x.shape
     G, N = B.shape[2], B.shape[3]
@@ -272,6 +285,8 @@ class FwdArgs:
         need = ssd_chunked_fwd_workspace_size(self.dims, self.L)
         if workspace is None:
             workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        else:
+            workspace = _own_workspace(workspace, dev)
         self.ws = workspace
         self.device = dev
 
@@ -585,6 +600,8 @@ def ssd_chunked_bwd(x, dt, A, B, C, D, chunk_size, dy, init_state=None, dfinal=N
     need = ssd_chunked_bwd_workspace_size(a.dims, a.L)
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    else:
+        workspace = _own_workspace(workspace, dev)
     f32 = dict(dtype=torch.float32, device=dev)
     out = dict(dx=torch.empty((Bt, T, H, P), **f32), ddt=torch.empty((Bt, T, H), **f32),
                dA=torch.empty((H,), **f32), dB=torch.empty((Bt, T, G, N), **f32),
@@ -767,6 +784,8 @@ def ssd_conv1d_bwd(x, weight, dy, bias=None, silu: bool = True, init_state=None,
     if workspace is None:
         workspace = torch.empty(max(ssd_conv1d_bwd_workspace_size(dims), 16), dtype=torch.uint8,
                                 device=dev)
+    else:
+        workspace = _own_workspace(workspace, dev)
     f32 = dict(dtype=torch.float32, device=dev)
     out = dict(dx=torch.empty(Bt, T, C, **f32), dweight=torch.empty(C, W, **f32),
                dbias=None if bias is None else torch.empty(C, **f32),
@@ -839,6 +858,8 @@ def ssd_selective_scan_fwd(x, dt, A, B, C, D, init_state=None, y=None, final_sta
     if workspace is None:
         need = ssd_selective_scan_workspace_size(dims)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        workspace = _own_workspace(workspace, dev)
     _call("ssd_selective_scan_fwd", dev, x.data_ptr(), dt.data_ptr(), A.data_ptr(),
           B.data_ptr(), C.data_ptr(), D.data_ptr(), _addr(init_state), _addr(seq_lens),
           y.data_ptr(), _addr(final_state),
@@ -902,6 +923,8 @@ def ssd_selective_scan_bwd(x, dt, A, B, C, D, dy, init_state=None, dfinal=None, 
     if workspace is None:
         workspace = torch.empty(max(ssd_selective_scan_bwd_workspace_size(dims), 16),
                                 dtype=torch.uint8, device=dev)
+    else:
+        workspace = _own_workspace(workspace, dev)
     f32 = dict(dtype=torch.float32, device=dev)
     out = dict(dx=torch.empty(Bt, T, Dm, **f32), ddt=torch.empty(Bt, T, Dm, **f32),
                dA=torch.empty(Dm, N, **f32), dB=torch.empty(Bt, T, N, **f32),
