@@ -108,11 +108,11 @@ __device__ __forceinline__ void store4(uint16_t *p, float4 v, int n) {
 // d = log(1 + e^r) = max(r, 0) + log(1 + e^-|r|); above 20 that is r in
 // float32.  e^-|r| as a power of two (of hi, with the rest of the argument put
 // back to first order), and log(1 + e) with the rounding of 1 + e put back, so
-// small results keep their relative accuracy.  The maxima let NaN through, and
-// keep -inf out of the products.  w = 1 + e, for the derivative below.
+// small results keep their relative accuracy.  |r| is held to 126, where e^-|r|
+// is 0 next to anything: hi stays finite up to r = +-inf.  The minimum and the
+// maximum let NaN through.  w = 1 + e, for the derivative below.
 __device__ __forceinline__ float softplus_f(float r, float &e, float &w) {
-    r = __builtin_elementwise_maximum(r, -126.f);
-    const float q = -fabsf(r), hi = q * kLog2e;
+    const float q = -__builtin_elementwise_minimum(fabsf(r), 126.f), hi = q * kLog2e;
     e = fast_exp2(hi);
     e = fmaf(e, fmaf(hi, -kLn2, q), e);
     w = 1.f + e;

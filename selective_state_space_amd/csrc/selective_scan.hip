@@ -107,7 +107,9 @@ __global__ __launch_bounds__(256) void sel_step_kernel(
         if (live) {
             float d = dv[r] + bias[r];
             if (softplus) d = softplus_f(d);
-            const float u = d * xv[r], d2 = d * kLog2e;
+            // (finite up to the largest d: no decay, A = 0, takes 0 d2)
+            const float d2 = __builtin_elementwise_minimum(d * kLog2e, 0x1.fffffep127f);
+            const float u = d * xv[r];
             float4 h = hv[r];
             h.x = fmaf(fast_exp2(d2 * av[r].x), h.x, u * bv.x);
             h.y = fmaf(fast_exp2(d2 * av[r].y), h.y, u * bv.y);
