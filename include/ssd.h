@@ -511,7 +511,8 @@ ssd_status ssd_conv1d_bwd(const void *x, const float *weight, const float *bias,
  *     y[c]   = sum_n h[c,n] C_t[n] + D_c x[c]      (then y silu(z), with opts->z)
  *
  *   x, dt       [Bt, T, Dm]  io dtype  in
- *   A           [Dm, N]      float32   in   natural-log decay rates (<= 0)
+ *   A           [Dm, N]      float32   in   natural-log decay rates (<= 0; those
+ *               below -2^127 count as -2^127)
  *   B, C        [Bt, T, N]   io dtype  in
  *   D           [Dm]         float32   in
  *   init_state  [Bt, Dm, N]  float32   in   NULL = zeros

@@ -134,6 +134,12 @@ __device__ __forceinline__ float sigmoid_f(float v) {
     return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * v));
 }
 
+// A rate for exponentials to base 2.  Held where the product is finite (-2^127), so
+// that a step of d = 0 leaves the state as it is at any rate; NaN passes.
+__device__ __forceinline__ float rate2(float A) {
+    return __builtin_elementwise_maximum(A, -0x1p127f) * kLog2e;
+}
+
 // Sum over the S lanes of a channel, in every one of them.
 template <int S>
 __device__ __forceinline__ float chan_sum(float v) {
@@ -351,7 +357,7 @@ __device__ __forceinline__ void sel_scan(
     if (c < g.Dm) {
         load_ks(A + (int64_t)c * N + KS * s, a2);
 #pragma unroll
-        for (int i = 0; i < KS; ++i) a2[i] *= kLog2e;
+        for (int i = 0; i < KS; ++i) a2[i] = rate2(a2[i]);
         if (start)   // [Bt][nseg][Dm][N]: with one segment the initial state
             load_ks(start + (((b * g.nseg) + seg) * g.Dm + c) * N + KS * s, h);
     }

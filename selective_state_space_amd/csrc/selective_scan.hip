@@ -38,7 +38,7 @@ __global__ __launch_bounds__(256) void sel_chain_kernel(float *__restrict__ seg,
     const int64_t per = (int64_t)Dm * N;
     const int64_t b = i / per, cn = i % per;
     const int64_t c = cn / N;
-    const float a2 = A[cn] * kLog2e;
+    const float a2 = rate2(A[cn]);
     float h = init ? init[i] : 0.f;
     float *p = seg + b * nseg * per + cn;
     const float *q = dsum + b * nseg * Dm + c;

@@ -79,7 +79,7 @@ __device__ __forceinline__ void sel_adj(
     if (c < g.Dm) {
         load_ks(A + (int64_t)c * N + KS * s, a2);
 #pragma unroll
-        for (int i = 0; i < KS; ++i) a2[i] *= kLog2e;
+        for (int i = 0; i < KS; ++i) a2[i] = rate2(a2[i]);
     }
     const int64_t ntile = (t1 - t0 + TB - 1) / TB;
     for (int64_t k = ntile - 1; k >= 0; --k) {
@@ -161,7 +161,7 @@ __global__ __launch_bounds__(256) void sel_chain_bwd_kernel(
     if (i >= total) return;
     const int64_t per = (int64_t)Dm * N;
     const int64_t b = i / per, cn = i % per;
-    const float a2 = A[cn] * kLog2e;
+    const float a2 = rate2(A[cn]);
     const float *q = dsum + b * nseg * Dm + cn / N;
     float *p = hseg + b * nseg * per + cn;
     float h = init ? init[i] : 0.f;
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(256, 2) void sel_bwd_kernel(
     if (c < g.Dm) {
         load_ks(A + (int64_t)c * N + KS * s, a2);
 #pragma unroll
-        for (int i = 0; i < KS; ++i) a2[i] *= kLog2e;
+        for (int i = 0; i < KS; ++i) a2[i] = rate2(a2[i]);
         const int64_t u = ((int64_t)rest * g.Dm + c) * N + KS * s;
         if (right) load_ks(right + u, car);   // [Bt][nseg][Dm][N]: with one segment dfinal
         if (g.nseg > 1) load_ks(hseg + u, hs);

@@ -78,3 +78,26 @@ def test_gradients_of_the_largest_steps(io, Bt, T, Dm, N):
     out = run_bwd(m, dfinal=False)
     for k, (ref, bound) in gradients(m, dfinal=False).items():
         check(out[k], ref, bound, k)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("Bt,T,Dm,N", SIZES)
+@pytest.mark.parametrize("gate", [True, False])
+def test_decay_rates_at_the_lowest_value(io, Bt, T, Dm, N, gate):
+    """A rate of the type's lowest value forgets the state at any step, and keeps it where
+    d = 0 (an input at -inf); the tokens past the end of a sequence's last tile too."""
+    log("lowest decay rates", io, Bt, T, Dm, N)
+    m = make(Bt, T, Dm, N, io, seed=34, gate=gate)
+    m["A"][1::3] = torch.finfo(torch.float32).min
+    m["A"][2, ::2] = torch.finfo(torch.float32).min
+    m["dt"][:, T // 2] = -INF
+    m["dt"][:, T - 1, 1::2] = -INF
+    y, ey, h, E, _ = forward(m)
+    got, fin = run_fwd(m)
+    check(got, y, ey, "y")
+    check(fin, h, E, "final")
+    # d A is 0 or below -1e30 here, so decay and its bound are exact: 1 or 0
+    out = run_bwd(m)
+    ref = gradients(m)
+    for k in ("dx", "dB", "dC", "dD", "dinit") + (("dz",) if gate else ()):
+        check(out[k], *ref[k], k)
