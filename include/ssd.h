@@ -598,7 +598,8 @@ ssd_status ssd_selective_scan_bwd(const void *x, const void *dt, const float *A,
  * be shorter) has one float32 scale:
  *     scale = max|v| / q,  code = v q / max|v| rounded to the nearest code,
  *     ties to even;  q = 127 (SSD_CACHE_INT8) or 448 (SSD_CACHE_FP8, e4m3)
- * and reads back as code * scale.  A block whose largest magnitude is below
+ * and reads back as code * scale (the scale is rounded to nearest, or down
+ * where q * scale would overflow).  A block whose largest magnitude is below
  * 2^-100 is stored as zeros.  A block that holds an infinity or a NaN reads
  * back as NaN.
  *

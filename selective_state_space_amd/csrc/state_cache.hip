@@ -108,6 +108,9 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const float *__restric
             scale = 0.f;
         } else {
             scale = amax / q;
+            // (at the top of the range the rounded quotient may read back as infinity)
+            if (scale * q >= __uint_as_float(kInf))
+                scale = __uint_as_float(__float_as_uint(scale) - 1u);
             w = encode4<FP8>(v[k], q / amax, amax);
         }
         if (e < size) {

@@ -101,3 +101,27 @@ def test_decay_rates_at_the_lowest_value(io, Bt, T, Dm, N, gate):
     ref = gradients(m)
     for k in ("dx", "dB", "dC", "dD", "dinit") + (("dz",) if gate else ()):
         check(out[k], *ref[k], k)
+
+
+@pytest.mark.parametrize("fmt", [torch.int8, torch.float8_e4m3fn])
+def test_largest_states_read_back_finite(fmt):
+    """Blocks whose largest magnitude is next to the top of float32: scale and codes as
+    defined (the scale to an ulp), every value finite and within half a code's step."""
+    q = 127.0 if fmt == torch.int8 else 448.0
+    bits = torch.arange(0x7f7fffff - 127, 0x7f7fffff + 1, dtype=torch.int32)
+    amax = bits.view(torch.float32)
+    state = amax[:, None] * torch.linspace(-1, 1, 64)
+    state[:, 0] = amax
+    state[:, 63] = -amax
+    codes = torch.zeros(128, 64, dtype=torch.int8).view(fmt).cuda()
+    scales = torch.zeros(128, 1).cuda()
+    ssd.ssd_cache_write(state.cuda(), codes, scales)
+    back = ssd.ssd_cache_read(codes, scales).cpu().double()
+    want = amax.double()[:, None] / q
+    assert ((scales.cpu().double() - want).abs() <= 2.0 ** -23 * want).all()
+    assert back.isfinite().all()
+    # half a step (int8: of the scale; e4m3: 2^-4 of the value, or 2^-10 of the scale), an ulp
+    # of the scale and the rounding of the product
+    v = state.double()
+    step = want * 0.5 if fmt == torch.int8 else torch.maximum(2.0 ** -4 * v.abs(), want * 2.0 ** -10)
+    assert ((back - v).abs() <= step + 2.0 ** -22 * v.abs()).all()
