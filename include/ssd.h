@@ -494,6 +494,17 @@ ssd_status ssd_conv1d_step(void *conv_state, int64_t num_slots, const int32_t *s
  * identical.
  */
 size_t ssd_conv1d_bwd_workspace_size(const ssd_conv_dims *dims);
+
+/* How calls of these dims are laid over the chip, by rules on sizes alone: each
+ * size selects another form of a kernel.  For tests and timings.  Host only; no
+ * HIP call. */
+typedef struct {
+    int32_t fwd_run;    /* tokens that a lane walks in ssd_conv1d_fwd */
+    int32_t bwd_run;    /* and in ssd_conv1d_bwd */
+    int32_t step_rows;  /* sequences that a lane serves in ssd_conv1d_step */
+} ssd_conv_layout;
+ssd_status ssd_conv1d_layout(const ssd_conv_dims *dims, ssd_conv_layout *layout);
+
 ssd_status ssd_conv1d_bwd(const void *x, const float *weight, const float *bias,
                           const void *init_state, const float *const dy[3], const float *dfinal,
                           float *dx, float *dweight, float *dbias, float *dinit,
@@ -582,6 +593,17 @@ ssd_status ssd_selective_scan_step(float *state, int64_t num_slots, const int32_
  * are bitwise identical.
  */
 size_t ssd_selective_scan_bwd_workspace_size(const ssd_scan_dims *dims);
+
+/* How calls of these dims are laid over the chip, as ssd_conv1d_layout says it. */
+typedef struct {
+    int32_t fwd_states;     /* states of a lane in ssd_selective_scan_fwd: 2 or 4 */
+    int32_t bwd_states;     /* and in ssd_selective_scan_bwd */
+    int32_t step_channels;  /* channels of a lane in ssd_selective_scan_step: 1 or 2 */
+    int64_t fwd_segments;   /* parts that a sequence is cut into over time */
+    int64_t bwd_segments;
+} ssd_scan_layout;
+ssd_status ssd_selective_scan_layout(const ssd_scan_dims *dims, ssd_scan_layout *layout);
+
 ssd_status ssd_selective_scan_bwd(const void *x, const void *dt, const float *A, const void *B,
                                   const void *C, const float *D, const float *init_state,
                                   const float *dy, const float *dfinal, float *dx, float *ddt,

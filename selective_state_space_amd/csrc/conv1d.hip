@@ -557,12 +557,13 @@ void step_r(const ConvArgs &a, const ConvGeom &g, hipStream_t st) {
                                    a.bias, (Tio *)a.y[0], (Tio *)a.y[1], (Tio *)a.y[2], g);
     });
 }
+// 4 sequences per lane where that still leaves a wavefront on every other
+// SIMD (10240 channels: 64 sequences 4.2 us, one per lane 4.6; 256: 8.4, 10.5;
+// but 32, a wavefront on a third of them: 3.9, 3.7)
+int step_rows(const ConvArgs &a) { return a.Bt * vectors(a) >= int64_t(1) << 17 ? 4 : 1; }
 template <typename Tio>
 void step_t(const ConvArgs &a, const ConvGeom &g, hipStream_t st) {
-    // 4 sequences per lane where that still leaves a wavefront on every other
-    // SIMD (10240 channels: 64 sequences 4.2 us, one per lane 4.6; 256: 8.4,
-    // 10.5; but 32, a wavefront on a third of them: 3.9, 3.7)
-    if (a.Bt * (int64_t)g.nvec >= int64_t(1) << 17)
+    if (step_rows(a) == 4)
         step_r<Tio, 4>(a, g, st);
     else
         step_r<Tio, 1>(a, g, st);
@@ -591,6 +592,10 @@ bool conv1d_fits(const ConvArgs &a) {
     const double step = Bt * nvec / 256.0 + 1.0;
     const double most = (double)kMaxBlocks;
     return fwd <= most && bwd <= most && step <= most;
+}
+
+ConvLayout conv1d_layout(const ConvArgs &a) {
+    return ConvLayout{fwd_run(a), bwd_run(a), step_rows(a)};
 }
 
 hipError_t launch_conv1d_fwd(const ConvArgs &a, hipStream_t st) {

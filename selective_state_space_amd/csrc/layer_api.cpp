@@ -233,6 +233,18 @@ size_t ssd_conv1d_bwd_workspace_size(const ssd_conv_dims *dims) {
     return ssd::conv1d_bwd_workspace(a);
 }
 
+ssd_status ssd_conv1d_layout(const ssd_conv_dims *dims, ssd_conv_layout *layout) {
+    if (!layout) return fail(SSD_ERR_NULL, "layout is NULL");
+    ssd::ConvArgs a;
+    const ssd_status r = check_conv(dims, true, &a);
+    if (r != SSD_OK) return r;
+    const ssd::ConvLayout l = ssd::conv1d_layout(a);
+    layout->fwd_run = (int32_t)l.fwd_run;
+    layout->bwd_run = (int32_t)l.bwd_run;
+    layout->step_rows = l.step_rows;
+    return ok();
+}
+
 ssd_status ssd_conv1d_bwd(const void *x, const float *weight, const float *bias,
                           const void *init_state, const float *const dy[3], const float *dfinal,
                           float *dx, float *dweight, float *dbias, float *dinit,
@@ -358,6 +370,20 @@ size_t ssd_selective_scan_bwd_workspace_size(const ssd_scan_dims *dims) {
     ssd::SelArgs a;
     if (check_scan(dims, true, nullptr, ssd::selective_scan_bwd_fits, &a) != SSD_OK) return 0;
     return ssd::selective_scan_bwd_workspace(a);
+}
+
+ssd_status ssd_selective_scan_layout(const ssd_scan_dims *dims, ssd_scan_layout *layout) {
+    if (!layout) return fail(SSD_ERR_NULL, "layout is NULL");
+    ssd::SelArgs a;
+    const ssd_status r = check_scan(dims, true, nullptr, ssd::selective_scan_fits, &a);
+    if (r != SSD_OK) return r;
+    const ssd::SelLayout f = ssd::selective_scan_layout(a), b = ssd::selective_scan_bwd_layout(a);
+    layout->fwd_states = f.states;
+    layout->fwd_segments = f.segments;
+    layout->bwd_states = b.states;
+    layout->bwd_segments = b.segments;
+    layout->step_channels = ssd::selective_step_channels(a);
+    return ok();
 }
 
 ssd_status ssd_selective_scan_bwd(const void *x, const void *dt, const float *A, const void *B,

@@ -37,6 +37,11 @@ hipError_t launch_conv1d_fwd(const ConvArgs &a, hipStream_t st);
 hipError_t launch_conv1d_step(const ConvArgs &a, hipStream_t st);
 hipError_t launch_conv1d_bwd(const ConvArgs &a, hipStream_t st);
 size_t conv1d_bwd_workspace(const ConvArgs &a);
+struct ConvLayout {
+    int64_t fwd_run, bwd_run;   // tokens of a lane
+    int step_rows;              // sequences of a lane
+};
+ConvLayout conv1d_layout(const ConvArgs &a);
 // false: more workgroups than one launch holds
 bool conv1d_fits(const ConvArgs &a);
 
@@ -76,6 +81,13 @@ bool selective_scan_fits(const SelArgs &a);
 bool selective_step_fits(const SelArgs &a);
 bool selective_scan_bwd_fits(const SelArgs &a);
 size_t selective_scan_workspace(const SelArgs &a);
+struct SelLayout {
+    int states;         // of a lane
+    int64_t segments;   // of a sequence
+};
+SelLayout selective_scan_layout(const SelArgs &a);
+SelLayout selective_scan_bwd_layout(const SelArgs &a);
+int selective_step_channels(const SelArgs &a);   // of a lane
 hipError_t launch_selective_scan(const SelArgs &a, hipStream_t st);
 hipError_t launch_selective_step(const SelArgs &a, hipStream_t st);
 size_t selective_scan_bwd_workspace(const SelArgs &a);

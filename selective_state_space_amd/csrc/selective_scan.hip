@@ -203,6 +203,14 @@ size_t selective_scan_workspace(const SelArgs &a) {
     return b ? b + (size_t)(a.Bt * s.n * a.Dm) * sizeof(float) : 0;
 }
 
+SelLayout selective_scan_layout(const SelArgs &a) {
+    const Cut s = cut_of(a);
+    return SelLayout{s.ks, s.n};
+}
+
+// 2 channels per lane where that leaves 2 workgroups per CU
+int selective_step_channels(const SelArgs &a) { return a.Bt * chan_blocks(a) >= 2 * 512 ? 2 : 1; }
+
 hipError_t launch_selective_scan(const SelArgs &a, hipStream_t st) {
     const Cut sg = cut_of(a);
     SelGeom g;
@@ -265,8 +273,7 @@ hipError_t launch_selective_scan(const SelArgs &a, hipStream_t st) {
 
 hipError_t launch_selective_step(const SelArgs &a, hipStream_t st) {
     const int64_t one = chan_blocks(a);
-    // 2 channels per lane where that leaves 2 workgroups per CU
-    const bool two = a.Bt * one >= 2 * 512;
+    const bool two = selective_step_channels(a) == 2;
     const int64_t ncb = two ? cdiv64(one, 2) : one;
     const dim3 grid((uint32_t)(ncb * a.Bt));
     by_state(a, [&](auto n, auto io) {

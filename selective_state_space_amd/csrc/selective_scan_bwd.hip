@@ -749,6 +749,11 @@ bool selective_scan_bwd_fits(const SelArgs &a) {
            sums <= (double)kMaxBlocks;
 }
 
+SelLayout selective_scan_bwd_layout(const SelArgs &a) {
+    const BwdPlan p = plan(a);
+    return SelLayout{p.ks, p.nseg};
+}
+
 size_t selective_scan_bwd_workspace(const SelArgs &a) {
     return a.Bt > 0 ? plan(a).total * sizeof(float) : 0;
 }

@@ -31,7 +31,8 @@ The functions carry the C names:
 * :func:`ssd_chunked_fwd_workspace_size`, :func:`ssd_chunked_fwd_workspace_layout`,
   :func:`ssd_chunked_bwd_workspace_size`, :func:`fwd_path` and
   :func:`set_path_override` (which path the forward takes, and a switch for
-  tests).
+  tests); :func:`conv1d_layout` and :func:`selective_scan_layout` (which forms of
+  their kernels the convolution and the selective scan take).
 """
 
 from __future__ import annotations
@@ -98,6 +99,19 @@ class ScanDims(ctypes.Structure):
                 ("dstate", ctypes.c_int64), ("io_dtype", ctypes.c_int32)]
 
 
+class ConvLayout(ctypes.Structure):
+    """ssd_conv_layout."""
+    _fields_ = [("fwd_run", ctypes.c_int32), ("bwd_run", ctypes.c_int32),
+                ("step_rows", ctypes.c_int32)]
+
+
+class ScanLayout(ctypes.Structure):
+    """ssd_scan_layout."""
+    _fields_ = [("fwd_states", ctypes.c_int32), ("bwd_states", ctypes.c_int32),
+                ("step_channels", ctypes.c_int32), ("fwd_segments", ctypes.c_int64),
+                ("bwd_segments", ctypes.c_int64)]
+
+
 CACHE_BLOCK = 64   # SSD_CACHE_BLOCK
 CACHE_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}   # ssd_cache_format by the codes' dtype
 
@@ -145,6 +159,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "ssd_conv1d_fwd": ([vp, vp, vp, vp, vp, vp, vp, cdp, vp], st),
         "ssd_conv1d_step": ([vp, i64, vp, vp, vp, vp, vp, cdp, vp], st),
         "ssd_conv1d_bwd_workspace_size": ([cdp], sz),
+        "ssd_conv1d_layout": ([cdp, ctypes.POINTER(ConvLayout)], st),
+        "ssd_selective_scan_layout": ([sdp, ctypes.POINTER(ScanLayout)], st),
         "ssd_conv1d_bwd": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, cdp, vp, sz, vp], st),
         "ssd_selective_scan_workspace_size": ([sdp], sz),
         "ssd_selective_scan_fwd": ([vp] * 10 + [lop, sdp, vp, sz, vp], st),
@@ -766,6 +782,14 @@ def ssd_conv1d_bwd_workspace_size(dims: ConvDims) -> int:
     return int(load_library().ssd_conv1d_bwd_workspace_size(ctypes.byref(dims)))
 
 
+def conv1d_layout(dims: ConvDims) -> ConvLayout:
+    """How convolution calls of these dims are laid over the chip (ssd_conv1d_layout)."""
+    out = ConvLayout()
+    _check("ssd_conv1d_layout",
+           load_library().ssd_conv1d_layout(ctypes.byref(dims), ctypes.byref(out)))
+    return out
+
+
 def ssd_conv1d_bwd(x, weight, dy, bias=None, silu: bool = True, init_state=None, dfinal=None,
                    want_dinit: bool = True, workspace=None):
     """Gradients of ssd_conv1d_fwd (without seq_lens), float32: a dict of dx [Bt,T,C],
@@ -901,6 +925,15 @@ def ssd_selective_scan_step(state, x_t, dt_t, A, B_t, C_t, D, slots=None, y_t=No
 
 def ssd_selective_scan_bwd_workspace_size(dims: ScanDims) -> int:
     return int(load_library().ssd_selective_scan_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def selective_scan_layout(dims: ScanDims) -> ScanLayout:
+    """How selective-scan calls of these dims are laid over the chip
+    (ssd_selective_scan_layout)."""
+    out = ScanLayout()
+    _check("ssd_selective_scan_layout",
+           load_library().ssd_selective_scan_layout(ctypes.byref(dims), ctypes.byref(out)))
+    return out
 
 
 def ssd_selective_scan_bwd(x, dt, A, B, C, D, dy, init_state=None, dfinal=None, dt_bias=None,
