@@ -3,9 +3,10 @@
 // with the W-1 tokens before the first taken from a carried state.
 //
 // Every output needs 2W operations for 2 elements moved, so all three kernels
-// are bound by memory.  A lane owns 16 bytes of consecutive channels and walks
-// along the tokens with the last W-1 inputs in registers: x is read once (plus
-// W-1 rows per run of tokens), and each row of a wavefront is 1 KB contiguous.
+// are bound by memory.  A lane owns 4 consecutive channels and walks along the
+// tokens with the last W-1 inputs in registers: x is read once (plus W-1 rows per
+// run of tokens), and each row of a wavefront is 512 bytes (bf16) or 1 KB (float32)
+// contiguous.  The times below are those of replayed graphs on one card.
 // The outputs go to up to three dense tensors (x, B and C of the scan), so the
 // scan needs no copy of a strided slice; a lane's channels never cross from
 // one tensor into the next, and a lane whose channels run past a tensor's end
@@ -241,7 +242,8 @@ __global__ __launch_bounds__(256) void conv1d_fwd_kernel(
 // One token per sequence: the window is the slot's state and the new token;
 // the state moves up by one row in place.  A lane serves R sequences so that
 // its weights (as many bytes as a sequence's whole traffic) are read once for
-// all of them (256 sequences, 10240 channels, bf16: 9.4 us, 4.5 TB/s).
+// all of them (256 sequences, 10240 channels, bf16: 8.7 us, 4.8 TB/s; float32
+// 13.5 us, 6.2 TB/s, part of it from the memory-side cache).
 template <typename Tio, int W, int R, bool RAG>
 __global__ __launch_bounds__(256) void conv1d_step_kernel(
     Tio *__restrict__ state, const int32_t *__restrict__ slots, int64_t nslots,
@@ -307,7 +309,7 @@ __global__ __launch_bounds__(256) void conv1d_step_kernel(
 // tokens for the dx of its last ones.  dw and db are summed in registers over
 // the run, over the workgroup's 4 runs in LDS, and over the workgroups by
 // conv1d_bwd_reduce_kernel, always in the same order (4 x 2048 tokens, 2304
-// channels, bf16: 41 us, 4.6 TB/s, and 4 us for the reduction).
+// channels, bf16: 42 us with the 4 us of the reduction).
 template <typename Tio, int W, bool RAG>
 __global__ __launch_bounds__(256) void conv1d_bwd_kernel(
     const Tio *__restrict__ x, const float *__restrict__ weight, const float *__restrict__ bias,
@@ -477,12 +479,12 @@ int64_t vectors(const ConvArgs &a) {
 }
 // Tokens per lane: long runs reread few rows and weights, short ones fill the
 // chip when there are few sequences or channels.  Forward runs of 32 where that
-// leaves 2^18 lanes (half of the chip's; 8 x 4096 tokens, 5376 channels: 126 us,
-// runs of 16 135; 4 x 2048 tokens, 2304 channels, 2^17 lanes: 19.3, runs of 16
-// 18.1), runs under 16 only to reach 2^17 (1 x 1024 tokens, 5376 channels: 8.7
-// us in runs of 8, 2^17 lanes, 9.4 in 16, 10.4 in 4).  Backward, where a lane
-// holds twice the registers, 2^17 (4 x 2048 tokens, 2304 channels: 51 us in
-// runs of 32, 55 in runs of 16).
+// leaves 2^18 lanes (half of the chip's; 8 x 4096 tokens, 5376 channels: 137 us,
+// runs of 16 147, of 8 177; 4 x 2048 tokens, 2304 channels, 2^17 lanes: 20.5, runs
+// of 16 19.4, of 8 21.4), runs under 16 only to reach 2^17 (1 x 1024 tokens, 5376
+// channels: 9.0 us in runs of 8 and of 16, 10.6 in 4 and in 32).  Backward, where a
+// lane holds twice the registers, 2^17 (4 x 2048 tokens, 2304 channels: 42 us in
+// runs of 32, 46 in runs of 16).
 int64_t run_length(const ConvArgs &a, int64_t lanes) {
     int64_t tt = 32;
     while (tt > 4 &&
@@ -527,7 +529,7 @@ void by_width(const ConvArgs &a, F f) {
 
 // Outputs that outgrow the 256 MB memory-side cache are not found there by the
 // scan that reads them next: nontemporal stores (8 x 4096 tokens, 5376 channels,
-// 352 MB: 142 us, plain 148).  Smaller ones stay cached.
+// 352 MB: 137 us, plain 149).  Smaller ones stay cached.
 bool streams(const ConvArgs &a) {
     return a.Bt * a.T * a.C * (a.bf16 ? 2 : 4) > (int64_t(256) << 20);
 }
@@ -558,8 +560,8 @@ void step_r(const ConvArgs &a, const ConvGeom &g, hipStream_t st) {
     });
 }
 // 4 sequences per lane where that still leaves a wavefront on every other
-// SIMD (10240 channels: 64 sequences 4.2 us, one per lane 4.6; 256: 8.4, 10.5;
-// but 32, a wavefront on a third of them: 3.9, 3.7)
+// SIMD (10240 channels: 256 sequences 8.7 us, one per lane 11.2; 64: 4.7 both; but
+// 32, a wavefront on a third of them: 4.3, 3.8)
 int step_rows(const ConvArgs &a) { return a.Bt * vectors(a) >= int64_t(1) << 17 ? 4 : 1; }
 template <typename Tio>
 void step_t(const ConvArgs &a, const ConvGeom &g, hipStream_t st) {

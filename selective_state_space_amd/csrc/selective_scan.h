@@ -269,7 +269,7 @@ struct SelGeom {
     int64_t T, Bt;
     int32_t Dm, ncb;      // channels, channel blocks
     int32_t nseg;         // segments of a sequence
-    int64_t seg_len;      // tokens of a segment (a multiple of the tile)
+    int64_t seg_len;      // its tokens: a multiple of the tile, in the gradients of 16
     int32_t softplus;
 };
 

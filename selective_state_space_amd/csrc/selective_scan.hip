@@ -8,9 +8,11 @@
 // for every (channel, state), so unlike the scalar-decay scan no part of it is
 // a matrix product: each state element costs an exponential (two issue
 // slots) and four vector operations per token, and forming d, the gate and the
-// sums over n some 3 more.  The kernels are bound by vector issue: 8 x 4096
-// tokens of 5120 channels, N 16, take 705 us (1.9 TB/s), 640 of them vector
-// issue at 2.4 GHz; 1 x 65536 of 2048 take 838 us in two passes.
+// sums over n some 3 more.  Vector issue is the largest part of the time: 8 x 4096
+// tokens of 5120 channels, N 16, take 1.61 million cycles (700 us at 2.3 GHz, 1.9
+// TB/s), where the updates alone issue for 0.86 million (20.9 cycles per 64 states,
+// the rate of that mix with 4 wavefronts per SIMD) and the other instructions, at
+// 2.7 cycles each, for 0.36.  1 x 65536 of 2048 take 840 us in two passes.
 //
 // A sequence is walked in order, tile by tile (see selective_scan.h for the
 // split over lanes).  Where sequences and channels alone do not fill the chip
@@ -138,7 +140,11 @@ __global__ __launch_bounds__(256) void sel_step_kernel(
 //     (16 x 2048 tokens: 682 us against 759).
 //   * Else segments of at least 64 tokens, enough for 2048 workgroups of the
 //     4-state form (1 x 4096 tokens, 5120 channels: 144 us in 32 segments, 282
-//     us in one).
+//     us in one).  Three launches and a second pass pay from about 256 tokens on:
+//     one sequence of 2048 channels, N 16, cut and whole, 128 tokens 14.8 us and
+//     11.0, 192 15.0 and 15.6, 256 15.4 and 19.8, 512 18.6 and 37.0; of 5120, 128
+//     16.2 and 11.3, 256 20.4 and 19.9, 512 28.8 and 37.9; N 64, 2048 channels, 128
+//     20.5 and 18.1, 256 24.1 and 33.6.
 struct Cut {
     int ks;
     int64_t ncb, n, len;

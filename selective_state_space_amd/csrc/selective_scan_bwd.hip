@@ -22,7 +22,7 @@
 // N 16: the reverse pass takes 277 us, with the values swapped between lanes
 // 284, with matrix instructions that add them up 459.)
 //
-// With several segments per sequence (few rows, see segments() of the forward)
+// With several segments per sequence (few rows, see plan() below)
 // the first pass starts each segment from zero and the reverse pass adds the
 // decayed entry state to its checkpoints; the adjoints entering the segments
 // come from a reverse pass without outputs and a chain over segments.
@@ -677,12 +677,17 @@ __global__ __launch_bounds__(256) void sel_sum_kernel(SumJobs jobs) {
 // The cheapest is taken (8 x 1024 tokens, 5120 channels: 934 us whole, 851 us
 // in 4 segments; 16 x 512 x 2048: 320 us whole, 361 in 4; 4 x 2048 x 2048: 883
 // whole, 390 in 4, 374 in 16).
-// (N 8 with 4 states per lane would spill registers)
+// (N 8 with 4 states per lane would spill registers in every form.  Of the 4-state
+// forms kept, those with float32 io, a gate and an odd width spill 2 or 10 registers;
+// they still beat 2 states: 4 x 2048 tokens of 2047 channels, N 16, 456 us against
+// 510, 4 x 1024 of 1023, N 32, 196 against 256.)
 constexpr int bwd_most_ks(int N) { return N == 8 ? 2 : 4; }
 struct BwdPlan {
     int ks;
     int64_t nseg, seg_len, ncb;
-    // float offsets into the workspace
+    // float offsets into the workspace.  (pbc, a partial dB and dC of every channel
+    // block, grows with N^2: Dm N^2 / 128 bytes a token, 4 x 2048 tokens of 2048
+    // channels with N 64 0.54 GB of 0.81 GB.)
     size_t ckpt, cumd, hseg, adj, dsum, pbc, pA, pD, pbias, total;
 };
 BwdPlan plan(const SelArgs &a) {
