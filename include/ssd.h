@@ -648,6 +648,204 @@ ssd_status ssd_cache_read(const void *codes, const float *scales, int64_t n, int
                           const int32_t *slots, int64_t num_slots, float *state, int32_t format,
                           void *stream);
 
+/*
+ * Linear attention with a constant decay for each head: per batch row b and head
+ * h, with g = h / (H / G) the head's key and value head,
+ *
+ *     S_t = e^{log_decay_h} S_{t-1} + k_t (outer) v_t      state [K][V]
+ *     y_t = scale q_t S_t                                  output [V]
+ *
+ *   q           [Bt, T, H, K]     io dtype  in   a token's heads are consecutive;
+ *   k           [Bt, T, G, K]     io dtype  in   tokens and sequences lie the
+ *   v           [Bt, T, G, V]     io dtype  in   strides apart (slices of one
+ *               projection's rows are read in place); strides must be multiples
+ *               of 16 bytes
+ *   log_decay   [H]               float32   in   <= 0; 0 never forgets, and below
+ *               -1024 (-infinity included) a token forgets all before it
+ *   init_state  [Bt, H, K, V]     float32   in   NULL = zeros
+ *   seq_lens    [Bt]              int32     in   NULL = T for every sequence.
+ *               Right-padded batches: tokens at or past a sequence's length
+ *               (clamped to [0, T]) are not read, their y is written as zero,
+ *               and final_state is the state at the length.
+ *   y           [Bt, T, H, V]     io dtype  out  dense
+ *   final_state [Bt, H, K, V]     float32   out  NULL = not written; may equal
+ *               init_state
+ *
+ * K and V are multiples of 8 in [8, 256].  workspace:
+ * ssd_linear_attn_workspace_size(dims) bytes (0 where sequences and heads alone
+ * fill the chip; workspace may then be NULL).  With T = 0 final_state receives
+ * init_state (or zeros) and the token tensors may be NULL.  States, their
+ * updates and all sums are float32; for bf16 the weights of a chunk's pairs of
+ * tokens and the state as q's operand are rounded to bf16, and y once more.
+ * No atomics: reruns are bitwise identical.
+ */
+typedef struct {
+    int64_t batch;           /* Bt >= 0 */
+    int64_t seqlen;          /* T >= 0 (ignored by the step) */
+    int64_t nheads;          /* H in [1, 65536] */
+    int64_t ngroups;         /* G >= 1, H % G == 0: heads of k and v */
+    int64_t dim_k, dim_v;    /* K, V */
+    int64_t q_batch_stride, q_token_stride;   /* in elements, >= 0 */
+    int64_t k_batch_stride, k_token_stride;   /* (the step does not use token strides) */
+    int64_t v_batch_stride, v_token_stride;
+    int32_t io_dtype;        /* an ssd_dtype */
+    float scale;
+} ssd_attn_dims;
+
+size_t ssd_linear_attn_workspace_size(const ssd_attn_dims *dims);
+ssd_status ssd_linear_attn_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                               const float *init_state, const int32_t *seq_lens, void *y,
+                               float *final_state, const ssd_attn_dims *dims, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
+ * One token per sequence.  state [num_slots, H, K, V] (float32, in/out) is a pool
+ * of states; slots [Bt] int32 names each sequence's state (NULL = sequence b has
+ * state b, and num_slots >= Bt is required).  A slot outside [0, num_slots) marks
+ * a padded row: its y is zero and no state is touched.  A slot may be named once
+ * per call: with two rows on one slot that slot's state and the y of those rows
+ * are undefined.  q_t [Bt, H, K], k_t [Bt, G, K], v_t [Bt, G, V] at the batch
+ * strides; y_t [Bt, H, V] io dtype, dense.
+ */
+ssd_status ssd_linear_attn_step(float *state, int64_t num_slots, const int32_t *slots,
+                                const void *q_t, const void *k_t, const void *v_t,
+                                const float *log_decay, void *y_t, const ssd_attn_dims *dims,
+                                void *stream);
+
+/*
+ * Gradients of ssd_linear_attn_fwd (seq_lens included) for the loss sum(dy . y) +
+ * sum(dfinal . final_state).  The decays are constants of the model; no gradient
+ * of them is formed.
+ *   dy      [Bt, T, H, V]  io dtype  in   dense; not read past the lengths
+ *   dfinal  [Bt, H, K, V]  float32   in   NULL = 0
+ *   dq      [Bt, T, H, K]  io dtype  out  dense; zero past the lengths
+ *   dk, dv  [Bt, T, G, K], [Bt, T, G, V]  io dtype  out  likewise, summed in
+ *           float32 over the heads that share a head of k and v
+ *   dinit   [Bt, H, K, V]  float32   out  NULL = not written
+ * The states are formed again.  workspace: ssd_linear_attn_bwd_workspace_size(dims)
+ * bytes, 16-byte aligned (NULL where that is 0).  With T = 0 dinit = dfinal.  No
+ * atomics: reruns are bitwise identical.
+ */
+size_t ssd_linear_attn_bwd_workspace_size(const ssd_attn_dims *dims);
+ssd_status ssd_linear_attn_bwd(const void *q, const void *k, const void *v, const float *log_decay,
+                               const float *init_state, const int32_t *seq_lens, const void *dy,
+                               const float *dfinal, void *dq, void *dk, void *dv, float *dinit,
+                               const ssd_attn_dims *dims, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* How calls of these dims are laid over the chip, as ssd_conv1d_layout says it. */
+typedef struct {
+    int32_t fwd_cols;       /* columns of the state that a workgroup takes: 64 or 128 */
+    int32_t bwd_cols;
+    int64_t fwd_segments;   /* parts that a sequence is cut into over time */
+    int64_t bwd_segments;
+} ssd_attn_layout;
+ssd_status ssd_linear_attn_layout(const ssd_attn_dims *dims, ssd_attn_layout *layout);
+
+/*
+ * Group norm with an activation or a gate, channels last and token by token, as a
+ * mixer's output takes it: each token's C channels in `groups` groups of
+ * consecutive channels,
+ *
+ *     u = x, or x silu(z) with SSD_NORM_GATED_INPUT
+ *     n = (u - mean) / sqrt(var + eps) * weight + bias
+ *         (rms: u / sqrt(mean of u^2 + eps) * weight + bias)
+ *     y = n; silu(n) with SSD_NORM_SILU; n silu(z) with SSD_NORM_GATE
+ *
+ *   x      [Bt, T, C]  io dtype  in   a token's channels are consecutive, tokens
+ *   z      [Bt, T, C]  io dtype  in   and sequences lie the strides apart (slices of
+ *          a projection's rows are read in place; the alignment of the elements is
+ *          enough).  z is required with the two gated forms and NULL with the others.
+ *   weight [C]         float32   in   NULL = ones
+ *   bias   [C]         float32   in   NULL = zeros
+ *   seq_lens [Bt]      int32     in   NULL = T for every sequence.  Tokens at or past
+ *          a sequence's length are not read and their y is written as zero.
+ *   y      [Bt, T, C]  io dtype  out  dense
+ *
+ * C / groups in [1, 16384]; eps > 0.  Means, variances (about the mean) and sums
+ * are float32; one rounding to the io dtype.
+ */
+typedef enum {
+    SSD_NORM_PLAIN = 0,
+    SSD_NORM_SILU = 1,
+    SSD_NORM_GATE = 2,
+    SSD_NORM_GATED_INPUT = 3
+} ssd_norm_form;
+
+typedef struct {
+    int64_t batch;           /* Bt >= 0 */
+    int64_t seqlen;          /* T >= 0 */
+    int64_t channels;        /* C >= 1 */
+    int64_t groups;          /* >= 1, divides C */
+    int64_t x_batch_stride, x_token_stride;   /* in elements, >= 0 */
+    int64_t z_batch_stride, z_token_stride;
+    int32_t io_dtype;        /* an ssd_dtype */
+    int32_t form;            /* an ssd_norm_form */
+    int32_t rms;             /* nonzero: no mean is taken off */
+    float eps;
+} ssd_norm_dims;
+
+ssd_status ssd_group_norm_fwd(const void *x, const void *z, const float *weight, const float *bias,
+                              const int32_t *seq_lens, void *y, const ssd_norm_dims *dims,
+                              void *stream);
+
+/*
+ * Gradients of ssd_group_norm_fwd for the loss sum(dy . y).
+ *   dy       [Bt, T, C]  io dtype  in   dense; not read past the lengths
+ *   dx, dz   [Bt, T, C]  io dtype  out  dense, zero past the lengths; dz is required
+ *            with the gated forms, else unused
+ *   dweight, dbias [C]   float32   out  NULL = not written (defined for weight or
+ *            bias = NULL too)
+ * workspace: ssd_group_norm_bwd_workspace_size(dims) bytes, 16-byte aligned; needed
+ * where dweight or dbias is asked for.  With no tokens dweight and dbias are zero.
+ * No atomics: reruns are bitwise identical.
+ */
+size_t ssd_group_norm_bwd_workspace_size(const ssd_norm_dims *dims);
+ssd_status ssd_group_norm_bwd(const void *x, const void *z, const float *weight, const float *bias,
+                              const int32_t *seq_lens, const void *dy, void *dx, void *dz,
+                              float *dweight, float *dbias, const ssd_norm_dims *dims,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Projections with 4-bit weights, for the few rows of decoded tokens.  Per output
+ * and group of `group` (64 or 128) consecutive inputs one bfloat16 scale:
+ *     scale = max|w| / 7 rounded to bfloat16
+ *     code  = w / scale rounded to the nearest whole number, ties to even, plus 8
+ * and the weight is (code - 8) * scale.  A group whose largest magnitude is below
+ * 2^-100 is stored as zeros; one that holds an infinity or a NaN reads back as NaN.
+ *
+ *   codes  [outputs, inputs / 2]      uint8: input 2 i in the low half of byte i,
+ *          2 i + 1 in the high half (codes 0 to 15 are all read)
+ *   scales [outputs, inputs / group]  bfloat16
+ *
+ * ssd_w4_quantize reads weight [outputs, inputs] (float32 or bfloat16) and writes
+ * codes and scales; ssd_w4_dequantize writes the weights they stand for (for
+ * many rows: a library's matrix product), rounded once to the io dtype.
+ * ssd_w4_linear forms y = x w^T + bias:
+ *   x    [rows, inputs]   io dtype  in   rows x_row_stride elements apart (a
+ *        multiple of 16 bytes)
+ *   bias [outputs]        float32   in   NULL = none
+ *   y    [rows, outputs]  io dtype  out  dense
+ * Products are exact and sums float32; one rounding to the io dtype.  Any number
+ * of rows is computed; the weights are read once for every 64 of them.
+ * inputs is a multiple of group; outputs >= 1.
+ */
+typedef struct {
+    int64_t rows;            /* of x, >= 0 (ignored but by ssd_w4_linear) */
+    int64_t inputs;
+    int64_t outputs;
+    int64_t group;           /* 64 or 128 */
+    int64_t x_row_stride;    /* in elements, >= 0 */
+    int32_t io_dtype;        /* an ssd_dtype: of x and y, or of the weights */
+} ssd_w4_dims;
+
+ssd_status ssd_w4_quantize(const void *weight, void *codes, void *scales, const ssd_w4_dims *dims,
+                           void *stream);
+ssd_status ssd_w4_dequantize(const void *codes, const void *scales, void *weight,
+                             const ssd_w4_dims *dims, void *stream);
+ssd_status ssd_w4_linear(const void *x, const void *codes, const void *scales, const float *bias,
+                         void *y, const ssd_w4_dims *dims, void *stream);
+
 /* Static text for a status code. */
 const char *ssd_status_string(ssd_status status);
 

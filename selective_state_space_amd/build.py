@@ -24,8 +24,8 @@ ARCH = "gfx950"
 SOURCES = ["chunk_cumsum.hip", "chunk_state.hip", "state_passing.hip", "state_fwd.hip",
            "chunk_scan.hip", "fused_fwd.hip", "chunk_bwd.hip",
            "decode_step.hip", "decode_lowp.hip", "conv1d.hip", "selective_scan.hip",
-           "selective_scan_bwd.hip", "state_cache.hip", "ssd_api.cpp",
-           "layer_api.cpp"]
+           "selective_scan_bwd.hip", "state_cache.hip", "linear_attn.hip",
+           "group_norm.hip", "w4.hip", "ssd_api.cpp", "layer_api.cpp", "block_api.cpp"]
 
 # -packed-fp32-ops: keep the compiler from emitting packed fp32 VALU ops.
 FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH, "-Wall",

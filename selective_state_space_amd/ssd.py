@@ -28,11 +28,18 @@ The functions carry the C names:
   state;
 * :func:`ssd_cache_write`, :func:`ssd_cache_read` -- recurrent states in a slot
   pool at 8 bits per element;
+* :func:`ssd_linear_attn_fwd`, :func:`ssd_linear_attn_step`,
+  :func:`ssd_linear_attn_bwd` -- linear attention with a decay for each head;
+* :func:`ssd_group_norm_fwd`, :func:`ssd_group_norm_bwd` -- the group norm behind
+  a mixer, with its activation or gate;
+* :func:`ssd_w4_quantize`, :func:`ssd_w4_dequantize`, :func:`ssd_w4_linear` --
+  projections with 4-bit weights;
 * :func:`ssd_chunked_fwd_workspace_size`, :func:`ssd_chunked_fwd_workspace_layout`,
   :func:`ssd_chunked_bwd_workspace_size`, :func:`fwd_path` and
   :func:`set_path_override` (which path the forward takes, and a switch for
-  tests); :func:`conv1d_layout` and :func:`selective_scan_layout` (which forms of
-  their kernels the convolution and the selective scan take).
+  tests); :func:`conv1d_layout`, :func:`selective_scan_layout` and
+  :func:`linear_attn_layout` (which forms of their kernels the convolution, the
+  selective scan and linear attention take).
 """
 
 from __future__ import annotations
@@ -112,6 +119,37 @@ class ScanLayout(ctypes.Structure):
                 ("bwd_segments", ctypes.c_int64)]
 
 
+class AttnDims(ctypes.Structure):
+    """ssd_attn_dims."""
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("batch", "seqlen", "nheads", "ngroups", "dim_k", "dim_v", "q_batch_stride",
+                 "q_token_stride", "k_batch_stride", "k_token_stride", "v_batch_stride",
+                 "v_token_stride")] + [("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class AttnLayout(ctypes.Structure):
+    """ssd_attn_layout."""
+    _fields_ = [("fwd_cols", ctypes.c_int32), ("bwd_cols", ctypes.c_int32),
+                ("fwd_segments", ctypes.c_int64), ("bwd_segments", ctypes.c_int64)]
+
+
+class NormDims(ctypes.Structure):
+    """ssd_norm_dims."""
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("batch", "seqlen", "channels", "groups", "x_batch_stride", "x_token_stride",
+                 "z_batch_stride", "z_token_stride")] + \
+               [("io_dtype", ctypes.c_int32), ("form", ctypes.c_int32), ("rms", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class W4Dims(ctypes.Structure):
+    """ssd_w4_dims."""
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("rows", "inputs", "outputs", "group", "x_row_stride")] + \
+               [("io_dtype", ctypes.c_int32)]
+
+
+NORM_FORMS = {"plain": 0, "silu": 1, "gate": 2, "gated_input": 3}   # ssd_norm_form
 CACHE_BLOCK = 64   # SSD_CACHE_BLOCK
 CACHE_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}   # ssd_cache_format by the codes' dtype
 
@@ -130,6 +168,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     vp, i64, sz, dp = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(Dims)
     cdp, sdp = ctypes.POINTER(ConvDims), ctypes.POINTER(ScanDims)
     lop = ctypes.POINTER(LayerOpts)
+    adp, ndp, wdp = (ctypes.POINTER(c) for c in (AttnDims, NormDims, W4Dims))
     st = ctypes.c_int
     sig = {
         "ssd_chunked_fwd": ([vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, dp, vp, sz, vp], st),
@@ -169,6 +208,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "ssd_selective_scan_bwd": ([vp] * 18 + [lop, sdp, vp, sz, vp], st),
         "ssd_cache_write": ([vp, i64, i64, vp, i64, vp, vp, ctypes.c_int32, vp], st),
         "ssd_cache_read": ([vp, vp, i64, i64, vp, i64, vp, ctypes.c_int32, vp], st),
+        "ssd_linear_attn_workspace_size": ([adp], sz),
+        "ssd_linear_attn_bwd_workspace_size": ([adp], sz),
+        "ssd_linear_attn_layout": ([adp, ctypes.POINTER(AttnLayout)], st),
+        "ssd_linear_attn_fwd": ([vp] * 8 + [adp, vp, sz, vp], st),
+        "ssd_linear_attn_step": ([vp, i64] + [vp] * 6 + [adp, vp], st),
+        "ssd_linear_attn_bwd": ([vp] * 12 + [adp, vp, sz, vp], st),
+        "ssd_group_norm_fwd": ([vp] * 6 + [ndp, vp], st),
+        "ssd_group_norm_bwd_workspace_size": ([ndp], sz),
+        "ssd_group_norm_bwd": ([vp] * 10 + [ndp, vp, sz, vp], st),
+        "ssd_w4_quantize": ([vp] * 3 + [wdp, vp], st),
+        "ssd_w4_dequantize": ([vp] * 3 + [wdp, vp], st),
+        "ssd_w4_linear": ([vp] * 5 + [wdp, vp], st),
         "ssd_status_string": ([st], ctypes.c_char_p),
         "ssd_last_error_detail": ([], ctypes.c_char_p),
         "ssd_version": ([], ctypes.c_int),
@@ -1020,3 +1071,312 @@ def ssd_cache_read(codes, scales, slots=None, shape=None, state=None):
     _call("ssd_cache_read", dev, codes.data_ptr(), scales.data_ptr(), n, size, _addr(slots),
           codes.shape[0], state.data_ptr(), CACHE_FORMATS[codes.dtype])
     return state
+
+
+# ---------------------------------------------------------------------------
+# Linear attention, group norm, 4-bit projections.
+
+def _like(t, name, dtype, shape, device):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device):
+        _need(t, name, dtype, shape, device)
+
+
+def _heads_in(t, name, dtype, shape, device):
+    """(t, batch stride, token stride) of [Bt,T,heads,d] or [Bt,heads,d]: in place where a
+    token's heads are consecutive and every row starts on 16 bytes, else a dense copy."""
+    _like(t, name, dtype, shape, device)
+    mult = 16 // t.element_size()
+    heads, d = shape[-2:]
+    lead = [s if n > 1 else 0 for s, n in zip(t.stride()[:-2], shape[:-2])]
+    if (t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != d) or t.data_ptr() & 15
+            or any(s % mult for s in lead)):
+        t = t.contiguous()
+        if t.data_ptr() & 15:
+            t = t.clone()
+        lead = t.stride()[:-2]
+    return t, lead[0], lead[1] if len(lead) > 1 else 0
+
+
+def _attn_args(q, k, v, log_decay, scale, names):
+    """(dims, q, k, v, log_decay, dev) of [Bt,T,heads,d] or [Bt,heads,d] tensors."""
+    dev = _on_gpu(q, names[0])
+    for t, n in ((k, names[1]), (v, names[2])):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % n)
+        if t.dim() != q.dim():
+            raise ValueError("%s must have %d dimensions, as %s" % (n, q.dim(), names[0]))
+    io = _io_code(q.dtype)
+    lead, (H, K), (G, V) = tuple(q.shape[:-2]), q.shape[-2:], v.shape[-2:]
+    q, qb, qt = _heads_in(q, names[0], q.dtype, lead + (H, K), dev)
+    k, kb, kt = _heads_in(k, names[1], q.dtype, lead + (G, K), dev)
+    v, vb, vt = _heads_in(v, names[2], q.dtype, lead + (G, V), dev)
+    log_decay = _in(log_decay, "log_decay", torch.float32, (H,), dev)
+    scale = K ** -0.5 if scale is None else float(scale)
+    dims = AttnDims(lead[0], lead[1] if len(lead) > 1 else 1, H, G, K, V, qb, qt, kb, kt, vb, vt,
+                    io, scale)
+    return dims, q, k, v, log_decay, dev
+
+
+def linear_attn_layout(dims: AttnDims) -> AttnLayout:
+    """How linear-attention calls of these dims are laid over the chip
+    (ssd_linear_attn_layout)."""
+    out = AttnLayout()
+    _check("ssd_linear_attn_layout",
+           load_library().ssd_linear_attn_layout(ctypes.byref(dims), ctypes.byref(out)))
+    return out
+
+
+def ssd_linear_attn_workspace_size(dims: AttnDims) -> int:
+    return int(load_library().ssd_linear_attn_workspace_size(ctypes.byref(dims)))
+
+
+def ssd_linear_attn_fwd(q, k, v, log_decay, scale=None, init_state=None, y=None,
+                        final_state=None, want_final: bool = True, seq_lens=None,
+                        workspace=None):
+    """Linear attention of a prompt with a decay for each head.  Returns (y [Bt,T,H,V] in q's
+    dtype, final_state or None).
+
+    q [Bt,T,H,K], k [Bt,T,G,K], v [Bt,T,G,V] (float32 or bfloat16; G divides H: head h reads
+    head h // (H // G) of k and v; slices of one projection are read in place), K and V
+    multiples of 8 up to 256, log_decay [H] f32 (<= 0), ``scale`` of y (None = K ** -0.5),
+    init_state [Bt,H,K,V] f32 or None; ``final_state`` may be the same tensor.  ``seq_lens``
+    [Bt] int32: y past a sequence's length is zero and its final state is that at its length.
+    """
+    if q.dim() != 4:
+        raise ValueError("q must be [Bt,T,H,K]")
+    dims, q, k, v, log_decay, dev = _attn_args(q, k, v, log_decay, scale, ("q", "k", "v"))
+    Bt, T, H, K, V = dims.batch, dims.seqlen, dims.nheads, dims.dim_k, dims.dim_v
+    init_state = _opt(init_state, "init_state", torch.float32, (Bt, H, K, V), dev)
+    seq_lens = _opt(seq_lens, "seq_lens", torch.int32, (Bt,), dev)
+    y = (torch.empty(Bt, T, H, V, dtype=q.dtype, device=dev) if y is None
+         else _need_out(y, "y", q.dtype, (Bt, T, H, V), dev))
+    if final_state is not None:
+        final_state = _need_out(final_state, "final_state", torch.float32, (Bt, H, K, V), dev)
+    elif want_final:
+        final_state = torch.empty(Bt, H, K, V, dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = ssd_linear_attn_workspace_size(dims)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        workspace = _own_workspace(workspace, dev)
+    _call("ssd_linear_attn_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_decay.data_ptr(), _addr(init_state), _addr(seq_lens), y.data_ptr(),
+          _addr(final_state), ctypes.byref(dims), _addr(workspace),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
+    return y, final_state
+
+
+def ssd_linear_attn_step(state, q_t, k_t, v_t, log_decay, scale=None, slots=None, y_t=None):
+    """One token of linear attention per sequence; returns y_t [Bt,H,V] in q_t's dtype.
+
+    state [num_slots,H,K,V] f32 is updated in place; slots [Bt] int32 (None = sequence b has
+    state b): a slot outside the pool marks a padded row (y zero, no state touched); a slot
+    may be named once.  q_t [Bt,H,K], k_t [Bt,G,K], v_t [Bt,G,V] may be slices of wider rows.
+    """
+    if q_t.dim() != 3:
+        raise ValueError("q_t must be [Bt,H,K]")
+    dims, q_t, k_t, v_t, log_decay, dev = _attn_args(q_t, k_t, v_t, log_decay, scale,
+                                                     ("q_t", "k_t", "v_t"))
+    Bt, H, K, V = dims.batch, dims.nheads, dims.dim_k, dims.dim_v
+    if state.dim() != 4:
+        raise ValueError("state must be [num_slots,H,K,V]")
+    state = _need_out(state, "state", torch.float32, (state.shape[0], H, K, V), dev)
+    slots = _opt(slots, "slots", torch.int32, (Bt,), dev)
+    y_t = (torch.empty(Bt, H, V, dtype=q_t.dtype, device=dev) if y_t is None
+           else _need_out(y_t, "y_t", q_t.dtype, (Bt, H, V), dev))
+    _call("ssd_linear_attn_step", dev, state.data_ptr(), state.shape[0], _addr(slots),
+          q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), log_decay.data_ptr(), y_t.data_ptr(),
+          ctypes.byref(dims))
+    return y_t
+
+
+def ssd_linear_attn_bwd_workspace_size(dims: AttnDims) -> int:
+    return int(load_library().ssd_linear_attn_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def ssd_linear_attn_bwd(q, k, v, log_decay, dy, scale=None, init_state=None, dfinal=None,
+                        seq_lens=None, want_dinit: bool = True, workspace=None):
+    """Gradients of ssd_linear_attn_fwd: a dict of dq [Bt,T,H,K], dk [Bt,T,G,K], dv [Bt,T,G,V]
+    in q's dtype and dinit [Bt,H,K,V] f32 (None unless ``want_dinit``).  dy [Bt,T,H,V] in q's
+    dtype, dfinal [Bt,H,K,V] f32 or None.  The decays are constants."""
+    if q.dim() != 4:
+        raise ValueError("q must be [Bt,T,H,K]")
+    dims, q, k, v, log_decay, dev = _attn_args(q, k, v, log_decay, scale, ("q", "k", "v"))
+    Bt, T, H, G, K, V = (dims.batch, dims.seqlen, dims.nheads, dims.ngroups, dims.dim_k,
+                         dims.dim_v)
+    dy = _in(dy, "dy", q.dtype, (Bt, T, H, V), dev)
+    init_state = _opt(init_state, "init_state", torch.float32, (Bt, H, K, V), dev)
+    dfinal = _opt(dfinal, "dfinal", torch.float32, (Bt, H, K, V), dev)
+    seq_lens = _opt(seq_lens, "seq_lens", torch.int32, (Bt,), dev)
+    if workspace is None:
+        need = ssd_linear_attn_bwd_workspace_size(dims)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        workspace = _own_workspace(workspace, dev)
+    like = dict(dtype=q.dtype, device=dev)
+    out = dict(dq=torch.empty(Bt, T, H, K, **like), dk=torch.empty(Bt, T, G, K, **like),
+               dv=torch.empty(Bt, T, G, V, **like),
+               dinit=(torch.empty(Bt, H, K, V, dtype=torch.float32, device=dev) if want_dinit
+                      else None))
+    _call("ssd_linear_attn_bwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_decay.data_ptr(), _addr(init_state), _addr(seq_lens), dy.data_ptr(), _addr(dfinal),
+          out["dq"].data_ptr(), out["dk"].data_ptr(), out["dv"].data_ptr(), _addr(out["dinit"]),
+          ctypes.byref(dims), _addr(workspace),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
+    return out
+
+
+def _channels_in(t, name, dtype, shape, device):
+    """(t, batch stride, token stride) of [Bt,T,C]: in place where a token's channels are
+    consecutive, else a dense copy."""
+    _like(t, name, dtype, shape, device)
+    if shape[2] > 1 and t.stride(2) != 1:
+        t = t.contiguous()
+    return t, t.stride(0) if shape[0] > 1 else 0, t.stride(1) if shape[1] > 1 else 0
+
+
+def _norm_args(x, groups, weight, bias, z, form, rms, eps, seq_lens):
+    dev = _on_gpu(x, "x")
+    io = _io_code(x.dtype)
+    if form not in NORM_FORMS:
+        raise ValueError("form must be one of %s" % sorted(NORM_FORMS))
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [Bt,T,C] or [Bt,C]")
+    shape = tuple(x.shape)
+    if z is not None:
+        _like(z, "z", x.dtype, shape, dev)
+    if x.dim() == 2:
+        x, z = x[:, None], None if z is None else z[:, None]
+    Bt, T, C = x.shape
+    x, xb, xt = _channels_in(x, "x", x.dtype, (Bt, T, C), dev)
+    zb = zt = 0
+    if z is not None:
+        z, zb, zt = _channels_in(z, "z", x.dtype, (Bt, T, C), dev)
+    weight = _opt(weight, "weight", torch.float32, (C,), dev)
+    bias = _opt(bias, "bias", torch.float32, (C,), dev)
+    seq_lens = _opt(seq_lens, "seq_lens", torch.int32, (Bt,), dev)
+    dims = NormDims(Bt, T, C, groups, xb, xt, zb, zt, io, NORM_FORMS[form], 1 if rms else 0, eps)
+    return dims, x, weight, bias, z, seq_lens, shape, dev
+
+
+def ssd_group_norm_fwd(x, groups: int, weight=None, bias=None, z=None, form: str = "plain",
+                       rms: bool = False, eps: float = 1e-5, seq_lens=None, y=None):
+    """Group norm of each token's channels behind a mixer; returns y, dense, of x's shape.
+
+    x [Bt,T,C] or [Bt,C] (float32 or bfloat16; its channels consecutive, its rows at any
+    stride) in ``groups`` groups of consecutive channels, weight and bias [C] f32 or None.
+    ``form``: "plain"; "silu" (of the result); "gate" (the result times silu(z)); or
+    "gated_input" (the norm of x silu(z)), z of x's shape and dtype, at any row stride.
+    ``rms``: no mean is taken off.  ``seq_lens`` [Bt] int32: y past a length is zero.
+    """
+    dims, x, weight, bias, z, seq_lens, shape, dev = _norm_args(x, groups, weight, bias, z, form,
+                                                                rms, eps, seq_lens)
+    y = (torch.empty(*shape, dtype=x.dtype, device=dev) if y is None
+         else _need_out(y, "y", x.dtype, shape, dev))
+    _call("ssd_group_norm_fwd", dev, x.data_ptr(), _addr(z), _addr(weight), _addr(bias),
+          _addr(seq_lens), y.data_ptr(), ctypes.byref(dims))
+    return y
+
+
+def ssd_group_norm_bwd_workspace_size(dims: NormDims) -> int:
+    return int(load_library().ssd_group_norm_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def ssd_group_norm_bwd(x, groups: int, dy, weight=None, bias=None, z=None, form: str = "plain",
+                       rms: bool = False, eps: float = 1e-5, seq_lens=None, workspace=None):
+    """Gradients of ssd_group_norm_fwd: a dict of dx and dz (None without z) of x's shape and
+    dtype, dweight and dbias [C] f32 (None where weight or bias is).  dy of x's shape and
+    dtype."""
+    dims, x, weight, bias, z, seq_lens, shape, dev = _norm_args(x, groups, weight, bias, z, form,
+                                                                rms, eps, seq_lens)
+    dy = _in(dy, "dy", x.dtype, shape, dev)
+    if workspace is not None:
+        workspace = _own_workspace(workspace, dev)
+    elif weight is not None or bias is not None:
+        workspace = torch.empty(max(ssd_group_norm_bwd_workspace_size(dims), 16),
+                                dtype=torch.uint8, device=dev)
+    C = dims.channels
+    out = dict(dx=torch.empty(*shape, dtype=x.dtype, device=dev),
+               dz=None if z is None else torch.empty(*shape, dtype=x.dtype, device=dev),
+               dweight=(None if weight is None
+                        else torch.empty(C, dtype=torch.float32, device=dev)),
+               dbias=None if bias is None else torch.empty(C, dtype=torch.float32, device=dev))
+    _call("ssd_group_norm_bwd", dev, x.data_ptr(), _addr(z), _addr(weight), _addr(bias),
+          _addr(seq_lens), dy.data_ptr(), out["dx"].data_ptr(), _addr(out["dz"]),
+          _addr(out["dweight"]), _addr(out["dbias"]), ctypes.byref(dims), _addr(workspace),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
+    return out
+
+
+def ssd_w4_quantize(weight, group: int = 128, codes=None, scales=None):
+    """A projection's weights at 4 bits: returns (codes [O,K/2] uint8, scales [O,K/group]
+    bfloat16) of weight [O,K] (float32 or bfloat16); ``group`` (64 or 128) consecutive inputs
+    share a scale."""
+    dev = _on_gpu(weight, "weight")
+    io = _io_code(weight.dtype)
+    if weight.dim() != 2:
+        raise ValueError("weight must be [outputs,inputs]")
+    O, K = weight.shape
+    if group < 1 or K % group or K % 2:
+        raise ValueError("%d inputs do not make groups of %s" % (K, group))
+    weight = _in(weight, "weight", weight.dtype, (O, K), dev)
+    codes = (torch.empty(O, K // 2, dtype=torch.uint8, device=dev) if codes is None
+             else _need_out(codes, "codes", torch.uint8, (O, K // 2), dev))
+    scales = (torch.empty(O, K // group, dtype=torch.bfloat16, device=dev) if scales is None
+              else _need_out(scales, "scales", torch.bfloat16, (O, K // group), dev))
+    dims = W4Dims(0, K, O, group, 0, io)
+    _call("ssd_w4_quantize", dev, weight.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+          ctypes.byref(dims))
+    return codes, scales
+
+
+def _w4_weights(codes, scales, dev):
+    """(codes, scales, inputs, outputs, group)"""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise ValueError("codes must be [outputs,inputs/2]")
+    if not isinstance(scales, torch.Tensor) or scales.dim() != 2 or not scales.shape[1]:
+        raise ValueError("scales must be [outputs,inputs/group]")
+    O, K, n = codes.shape[0], 2 * codes.shape[1], scales.shape[1]
+    if K % n:
+        raise ValueError("%d inputs do not make %d groups" % (K, n))
+    return (_in(codes, "codes", torch.uint8, (O, K // 2), dev),
+            _in(scales, "scales", torch.bfloat16, (O, n), dev), K, O, K // n)
+
+
+def ssd_w4_dequantize(codes, scales, dtype=torch.bfloat16, weight=None):
+    """The weights [O,K] that codes [O,K/2] and scales [O,K/group] stand for, in ``dtype``
+    (float32 or bfloat16)."""
+    dev = _on_gpu(codes, "codes")
+    codes, scales, K, O, group = _w4_weights(codes, scales, dev)
+    dims = W4Dims(0, K, O, group, 0, _io_code(dtype))
+    weight = (torch.empty(O, K, dtype=dtype, device=dev) if weight is None
+              else _need_out(weight, "weight", dtype, (O, K), dev))
+    _call("ssd_w4_dequantize", dev, codes.data_ptr(), scales.data_ptr(), weight.data_ptr(),
+          ctypes.byref(dims))
+    return weight
+
+
+def ssd_w4_linear(x, codes, scales, bias=None, y=None):
+    """y = x w^T + bias for 4-bit weights: x [rows,K] or [K] (float32 or bfloat16, rows at any
+    stride), codes [O,K/2] and scales [O,K/group] as ssd_w4_quantize makes them, bias [O] f32
+    or None; y [rows,O] or [O] in x's dtype."""
+    dev = _on_gpu(x, "x")
+    io = _io_code(x.dtype)
+    codes, scales, K, O, group = _w4_weights(codes, scales, dev)
+    if x.dim() not in (1, 2) or x.shape[-1] != K:
+        raise ValueError("x must be [rows,%d] or [%d], got %s" % (K, K, tuple(x.shape)))
+    lead = tuple(x.shape[:-1])
+    rows = lead[0] if lead else 1
+    stride = x.stride(0) if lead and rows > 1 else 0
+    if x.stride(-1) != 1 or x.data_ptr() & 15 or stride * x.element_size() & 15:
+        x = x.contiguous()
+        x = x.clone() if x.data_ptr() & 15 else x
+        stride = K
+    bias = _opt(bias, "bias", torch.float32, (O,), dev)
+    y = (torch.empty(*lead, O, dtype=x.dtype, device=dev) if y is None
+         else _need_out(y, "y", x.dtype, lead + (O,), dev))
+    dims = W4Dims(rows, K, O, group, stride, io)
+    _call("ssd_w4_linear", dev, x.data_ptr(), codes.data_ptr(), scales.data_ptr(), _addr(bias),
+          y.data_ptr(), ctypes.byref(dims))
+    return y
