@@ -19,6 +19,7 @@ using ssd::kMaxDim;
 using ssd::ok;
 
 constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxTokenStride = int64_t(1) << 24;   // a chunk of tokens spans 32-bit offsets
 
 ssd_status check_io(int32_t io) {
     if (io != SSD_F32 && io != SSD_BF16)
@@ -47,8 +48,8 @@ ssd_status check_range(const char *name, int64_t v, int64_t lo, int64_t hi) {
     } while (0)
 
 // strides of a tensor that is read 16 bytes at a time
-ssd_status check_stride(const char *name, int64_t v, int64_t multiple) {
-    CHECK(check_range(name, v, 0, kMaxStride));
+ssd_status check_stride(const char *name, int64_t v, int64_t multiple, int64_t most = kMaxStride) {
+    CHECK(check_range(name, v, 0, most));
     if (v % multiple)
         return fail(SSD_ERR_ALIGN, "%s = %lld is not a multiple of %lld elements (16 bytes)", name,
                     (long long)v, (long long)multiple);
@@ -84,9 +85,9 @@ ssd_status check_attn(const ssd_attn_dims *d, bool need_seq, ssd::AttnArgs *a) {
     CHECK(check_stride("k_batch_stride", d->k_batch_stride, multiple));
     CHECK(check_stride("v_batch_stride", d->v_batch_stride, multiple));
     if (need_seq) {
-        CHECK(check_stride("q_token_stride", d->q_token_stride, multiple));
-        CHECK(check_stride("k_token_stride", d->k_token_stride, multiple));
-        CHECK(check_stride("v_token_stride", d->v_token_stride, multiple));
+        CHECK(check_stride("q_token_stride", d->q_token_stride, multiple, kMaxTokenStride));
+        CHECK(check_stride("k_token_stride", d->k_token_stride, multiple, kMaxTokenStride));
+        CHECK(check_stride("v_token_stride", d->v_token_stride, multiple, kMaxTokenStride));
     }
     *a = ssd::AttnArgs{};
     a->Bt = d->batch;

@@ -54,7 +54,7 @@ struct Job {
     float pair, up, inter;
     bool qgroup, kgroup, vgroup;
     bool reverse;               // late, and backwards in time
-    bool wide;                  // out is float32 whatever the io dtype
+    bool wide;                  // out is float32 whatever the io dtype (kOutWide)
 };
 constexpr int kMaxJobs = 3;
 struct Jobs {
@@ -65,6 +65,8 @@ struct Jobs {
     int32_t H, G, nseg, njobs, slices, state_size;
 };
 
+constexpr int kChunk = 32;   // tokens of a chunk
+
 // Matrix operands.  A wavefront's operand register holds, for row (or column)
 // lane % 16, kRun contraction indices from kRun (lane / 16); the accumulator of
 // a 16 x 16 tile holds rows 4 (lane / 16) + 0..3 of column lane % 16.
@@ -72,7 +74,6 @@ template <typename T>
 struct Mat;
 template <>
 struct Mat<uint16_t> {
-    static constexpr int kChunk = 64;    // tokens of a chunk
     static constexpr int kDepth = 32;    // contraction indices of one operand
     static constexpr int kRun = 8;
     typedef bf16x8 Frag;
@@ -90,7 +91,6 @@ struct Mat<uint16_t> {
 };
 template <>
 struct Mat<float> {
-    static constexpr int kChunk = 32;
     static constexpr int kDepth = 16;
     static constexpr int kRun = 4;
     typedef f32x4 Frag;
@@ -102,50 +102,73 @@ struct Mat<float> {
     }
 };
 
-// Operands out of row-major tiles in LDS.  natural(): rows r0.. are the operand's
-// rows, contraction along the tile's columns from c0.
-template <typename T>
-__device__ __forceinline__ typename Mat<T>::Frag natural(const T *tile, int stride, int r0, int c0,
-                                                         int lane) {
-    const T *p = tile + (r0 + (lane & 15)) * stride + c0 + Mat<T>::kRun * (lane >> 4);
-    return *reinterpret_cast<const typename Mat<T>::Frag *>(p);
+// A tile of tokens in LDS: rows of COLS elements without a gap, their 16-byte pieces
+// in an order of the row's own (piece p at p ^ order(row)), so chosen that both ways of
+// reading below find their 16 lanes on 16 different banks' groups.  (Rows one piece
+// longer instead cost 5.0e7 conflict cycles of 9.0e7 in all, at 8 x 4096 tokens of 40
+// heads of 128.)
+template <typename T, int COLS>
+struct Lds {
+    static constexpr int kVec = 16 / sizeof(T);
+    static constexpr int kPerRow = COLS / kVec;
+    static constexpr int kSize = kChunk * COLS;
+    static __device__ __forceinline__ int order(int row) {
+        if constexpr (sizeof(T) == 4) return row & 15;
+        else if constexpr (kPerRow == 8) return (row << 1 & 4) | (row >> 2 & 3);
+        else return (row << 2 & 12) | (row >> 2 & 3);
+    }
+};
+
+// Operands out of such tiles.  natural(): row `row` for the operand's row lane % 16,
+// contraction along the tile's columns from c0 (a multiple of kDepth).
+template <typename T, int COLS>
+__device__ __forceinline__ typename Mat<T>::Frag natural(const T *tile, int row, int c0, int lane) {
+    typedef Lds<T, COLS> S;
+    const int piece = (lane >> 4) ^ S::order(row) ^ (c0 / S::kVec);
+    return *reinterpret_cast<const typename Mat<T>::Frag *>(tile + row * COLS + piece * S::kVec);
 }
-// across(): contraction along the tile's rows from r0; the operand's row m is
-// column c0 + step * (m / 4) + m % 4.
-template <int STEP>
-__device__ __forceinline__ bf16x8 across(const uint16_t *tile, int stride, int r0, int c0,
-                                         int lane) {
-    const uint16_t *p = tile + (r0 + 8 * (lane >> 4) + ((lane & 15) >> 2)) * stride + c0 +
-                        STEP * (lane & 3);
-    const u32x2 lo = Mat<uint16_t>::cols4(p), hi = Mat<uint16_t>::cols4(p + 4 * stride);
+// across(): contraction along the tile's rows from r0; the operand's row m is column
+// c0 + STEP (m / 4) + m % 4.
+template <int COLS, int STEP>
+__device__ __forceinline__ bf16x8 across(const uint16_t *tile, int r0, int c0, int lane) {
+    typedef Lds<uint16_t, COLS> S;
+    const int row = 8 * (lane >> 4) + (lane >> 2 & 3), c = c0 + STEP * (lane & 3);
+    auto at = [&](int r) {
+        return tile + (r0 + r) * COLS + ((c >> 3) ^ S::order(r)) * 8 + (c & 4);
+    };
+    const u32x2 lo = Mat<uint16_t>::cols4(at(row)), hi = Mat<uint16_t>::cols4(at(row + 4));
     return as_bf16x8(make_uint4(lo[0], lo[1], hi[0], hi[1]));
 }
-template <int STEP>
-__device__ __forceinline__ f32x4 across(const float *tile, int stride, int r0, int c0, int lane) {
-    const int m = lane & 15;
-    const float *p = tile + (r0 + 4 * (lane >> 4)) * stride + c0 + STEP * (m >> 2) + (m & 3);
+template <int COLS, int STEP>
+__device__ __forceinline__ f32x4 across(const float *tile, int r0, int c0, int lane) {
+    typedef Lds<float, COLS> S;
+    const int m = lane & 15, c = c0 + STEP * (m >> 2) + (m & 3);
     f32x4 v;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = p[r * stride];
+    for (int e = 0; e < 4; ++e) {
+        const int row = r0 + 4 * (lane >> 4) + e;
+        v[e] = tile[row * COLS + ((c >> 2) ^ S::order(row)) * 4 + (c & 3)];
+    }
     return v;
 }
 
-// The row of the state that accumulator row m of tile t holds: so chosen that the
-// tiles of one contraction step hold kRun consecutive rows per lane, as natural()
-// reads q.
+// What accumulator row m of tile t stands for where the accumulators become an operand
+// themselves (the state's rows; the keys of a chunk's pairs): so chosen that the tiles
+// of one contraction step hold kRun consecutive ones per lane, as the other operand
+// has them.
 template <typename T>
-__device__ __forceinline__ int state_row(int t, int m) {
+__device__ __forceinline__ int tile_row(int t, int m) {
     if constexpr (sizeof(T) == 2) return 32 * (t >> 1) + 8 * (m >> 2) + 4 * (t & 1) + (m & 3);
     else return 16 * t + m;
 }
 // k across its tokens, as the operand whose rows are those of state tile t
-template <typename T>
-__device__ __forceinline__ typename Mat<T>::Frag state_cols(const T *tile, int stride, int r0,
-                                                            int t, int lane) {
+template <typename T, int COLS>
+__device__ __forceinline__ typename Mat<T>::Frag state_cols(const T *tile, int r0, int t,
+                                                            int lane) {
     if constexpr (sizeof(T) == 2)
-        return across<8>(tile, stride, r0, 32 * (t >> 1) + 4 * (t & 1), lane);
+        return across<COLS, 8>(tile, r0, 32 * (t >> 1) + 4 * (t & 1), lane);
     else
-        return across<4>(tile, stride, r0, 16 * t, lane);
+        return across<COLS, 4>(tile, r0, 16 * t, lane);
 }
 
 __device__ __forceinline__ float frag_at(bf16x8 f, int e) {
@@ -153,9 +176,10 @@ __device__ __forceinline__ float frag_at(bf16x8 f, int e) {
 }
 
 // S += (k across) (w v): for bf16 the weighted v is split into three bf16 terms,
-// v w = hi + mid + lo to 2^-24, so that the state keeps float32's precision at
+// v w = hi + mid + lo to 2^-22, so that the state keeps float32's precision at
 // three matrix instructions for one; the single rounding that one term would take
-// (2^-8 of each product) would stay in the state for as long as it lives.
+// (2^-8 of each product) would stay in the state for as long as it lives.  hi and
+// mid are cut, not rounded (their packing is one byte permutation), lo is rounded.
 template <int N>
 struct Weighted {
     bf16x8 t[N];
@@ -163,14 +187,15 @@ struct Weighted {
 __device__ __forceinline__ Weighted<3> weighted(bf16x8 v, const float *w) {
     Weighted<3> r;
     uint32_t hi[4], mid[4], lo[4];
+    auto top = [](float f) { return __uint_as_float(__float_as_uint(f) & 0xffff0000u); };
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         float a = frag_at(v, 2 * e) * w[2 * e], b = frag_at(v, 2 * e + 1) * w[2 * e + 1];
-        hi[e] = pack_bf16x2(a, b);
-        a -= bf16_lo(hi[e]);
-        b -= bf16_hi(hi[e]);
-        mid[e] = pack_bf16x2(a, b);
-        lo[e] = pack_bf16x2(a - bf16_lo(mid[e]), b - bf16_hi(mid[e]));
+        hi[e] = pair_hi(__float_as_uint(a), __float_as_uint(b));
+        a -= top(a);
+        b -= top(b);
+        mid[e] = pair_hi(__float_as_uint(a), __float_as_uint(b));
+        lo[e] = pack_bf16x2(a - top(a), b - top(b));
     }
     r.t[0] = as_bf16x8(make_uint4(hi[0], hi[1], hi[2], hi[3]));
     r.t[1] = as_bf16x8(make_uint4(mid[0], mid[1], mid[2], mid[3]));
@@ -191,81 +216,124 @@ __device__ __forceinline__ f32x4 mma_weighted(f32x4 a, f32x4 b, f32x4 c) {
     return Mat<float>::mma(a, b, c);
 }
 
-// The state as an operand of q S: rounded to bf16 for bf16 calls (2^-8 of each
-// term, as y itself is rounded).
+// Accumulators as an operand: rounded to bf16 for bf16 calls (2^-8 of each term, as y
+// itself is rounded).
 template <int NT>
-__device__ __forceinline__ bf16x8 state_frag(const f32x4 (&s)[NT], int ks, uint16_t) {
-    const f32x4 a = s[2 * ks], b = s[2 * ks + 1];
+__device__ __forceinline__ bf16x8 tile_frag(const f32x4 (&s)[NT], int k, uint16_t) {
+    const f32x4 a = s[2 * k], b = s[2 * k + 1];
     return as_bf16x8(make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
                                 pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])));
 }
 template <int NT>
-__device__ __forceinline__ f32x4 state_frag(const f32x4 (&s)[NT], int ks, float) {
-    return s[ks];
+__device__ __forceinline__ f32x4 tile_frag(const f32x4 (&s)[NT], int k, float) {
+    return s[k];
 }
+
+__device__ __forceinline__ f32x4 f4(const float *v) { return f32x4{v[0], v[1], v[2], v[3]}; }
 
 __device__ __forceinline__ void put4(uint16_t *p, f32x4 v) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 __device__ __forceinline__ void put4(float *p, f32x4 v) { *reinterpret_cast<f32x4 *>(p) = v; }
 
-// A tile of tokens on its way from memory to LDS: 16-byte pieces, row by row.
+// A chunk's rows of one tensor, loaded from memory into LDS directly, 16 bytes a lane
+// (a wavefront's 64 pieces lie in LDS as its lanes do, so the order within a row is
+// made by which piece a lane loads).  Rows past the chunk's tokens and columns past
+// the tensor's arrive as zeros: their lanes' offsets lie outside the buffer.
 template <typename T, int COLS>
 struct Tile {
-    static constexpr int kVec = 16 / sizeof(T);
-    static constexpr int kPerRow = COLS / kVec;
-    static constexpr int kPieces = Mat<T>::kChunk * kPerRow / 256;
-    static constexpr int kStride = COLS + kVec;     // of a row in LDS
-    static constexpr int kSize = Mat<T>::kChunk * kStride;
-    uint4 v[kPieces];
-    // rows [0, n) at base + row * stride, columns [0, cols); zeros elsewhere
-    __device__ __forceinline__ void load(const T *base, int64_t stride, int n, int cols) {
+    typedef Lds<T, COLS> S;
+    static constexpr int kVec = S::kVec, kPerRow = S::kPerRow, kSize = S::kSize;
+    static constexpr int kPieces = kChunk * kPerRow / 256;    // loads of a lane
+    static_assert(kChunk * kPerRow % 256 == 0, "whole wavefronts");
+    static constexpr uint32_t kNowhere = 0xffffffffu;
+    const T *base;        // of the next chunk to be loaded
+    int64_t turn;         // elements from one chunk to the next
+    uint32_t at[kPieces]; // byte offsets of this lane's pieces
+    static __device__ __forceinline__ int row(int p) { return (threadIdx.x + 256 * p) / kPerRow; }
+    // p: the walk's first token; step +1 or -1 tokens of `stride` elements
+    __device__ __forceinline__ void start(const T *p, int64_t stride, bool reverse, int cols) {
+        base = reverse ? p - (kChunk - 1) * stride : p;
+        turn = reverse ? -kChunk * stride : kChunk * stride;
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-            const int x = threadIdx.x + 256 * p, row = x / kPerRow, c = x % kPerRow * kVec;
-            v[p] = make_uint4(0, 0, 0, 0);
-            if (row < n && c < cols)
-                v[p] = *reinterpret_cast<const uint4 *>(base + row * stride + c);
+        for (int i = 0; i < kPieces; ++i) {
+            const int r = reverse ? kChunk - 1 - row(i) : row(i);
+            const int col = ((threadIdx.x + 256 * i) % kPerRow ^ S::order(row(i))) * kVec;
+            at[i] = col < cols ? (uint32_t)((r * (uint64_t)stride + col) * sizeof(T)) : kNowhere;
         }
     }
-    __device__ __forceinline__ void keep(T *lds) const {
+    // rows [0, n) of the next chunk
+    __device__ __forceinline__ void load(T *lds, int n, int wave) {
+#ifdef __HIP_DEVICE_COMPILE__   // (16 bytes a lane are gfx950's: not known to the host's pass)
+        typedef __attribute__((address_space(3))) T lds_t;
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, 0xfffffff0u);
+        base += turn;
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-            const int x = threadIdx.x + 256 * p, row = x / kPerRow, c = x % kPerRow * kVec;
-            *reinterpret_cast<uint4 *>(lds + row * kStride + c) = v[p];
-        }
+        for (int i = 0; i < kPieces; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rs, (lds_t *)(lds + (256 * i + 64 * wave) * kVec), 16,
+                row(i) < n ? at[i] : kNowhere, 0, 0, 0);
+#endif
     }
 };
 
-// One workgroup walks the chunks of one segment of one sequence and head, for 64 NV
-// columns of the state, which stay in accumulators; a wavefront owns 16 NV columns.
-// OUT = false: only the state at the segment's end, from zero.
-template <typename T, int KD, int NV, bool OUT>
-__global__ __launch_bounds__(256) void attn_kernel(const Jobs a) {
+// at most N of the wavefront's vector memory accesses are still on their way
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    static_assert(N < 64, "");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <bool B>
+struct Const {
+    static constexpr bool value = B;
+};
+
+// One workgroup walks the chunks of one segment of one sequence and head, for 16 NV
+// columns of the state per wavefront, which stay in accumulators.  OUT = false:
+// only the state at the segment's end, from zero.
+//
+// A chunk's tiles are loaded into LDS kAhead chunks before the walk comes to it, so
+// that a load has kAhead chunks' time; one barrier a chunk lets the buffers turn.  Each
+// wavefront forms the chunk's pairs for itself (they are a fifth of its matrix
+// instructions): shared through LDS they needed a second barrier, and a wait for it.
+// Whole chunks run through one block of code without a branch, in which matrix and
+// vector instructions interleave.
+enum Mode { kStateOnly, kOut, kOutWide };
+
+template <typename T, int KD, int NV, int MODE>
+__global__ __launch_bounds__(256, 2) void attn_kernel(const Jobs a) {
     typedef Mat<T> M;
     typedef typename M::Frag Frag;
-    constexpr int L = M::kChunk, LT = L / 16, VS = 64 * NV;
+    constexpr bool OUT = MODE != kStateOnly;
+    constexpr int L = kChunk, LT = L / 16, VS = 64 * NV;
     constexpr int NT = KD / 16, KS = KD / M::kDepth, NB = L / M::kDepth;
-    constexpr int PS = L + 16 / sizeof(T);
+    constexpr uint32_t kNowhere = 0xffffffffu;
     typedef Tile<T, KD> KTile;
     typedef Tile<T, VS> VTile;
-    __shared__ __align__(16) T ks[KTile::kSize];
-    __shared__ __align__(16) T vs[VTile::kSize];
-    __shared__ __align__(16) T qs[OUT ? KTile::kSize : 1];
-    __shared__ __align__(16) T ps[OUT ? L * PS : 1];
+    // (three buffers of 256 columns leave a CU one workgroup, or do not fit)
+    constexpr int kAhead = KD == 256 ? 1 : 2, NBUF = kAhead + 1;
+    // (separate variables: so the compiler sees that reads of one buffer need not wait for
+    // loads into another)
+    constexpr int kK = OUT ? KTile::kSize : 0, kV = kK + KTile::kSize, kAll = kV + VTile::kSize;
+    __shared__ __align__(16) T tiles0[kAll];
+    __shared__ __align__(16) T tiles1[kAll];
+    __shared__ __align__(16) T tiles2[NBUF == 3 ? kAll : 8];
+    auto tiles = [&](int buf) -> T * { return buf == 0 ? tiles0 : buf == 1 ? tiles1 : tiles2; };
+    __shared__ __align__(16) float ws[2][L];    // weights of a whole and of a cut chunk
 
     // consecutive ids share an XCD, and the tokens that they read
     uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
     const int slice = id % a.slices;
     id /= a.slices;
-    const Job &job = a.job[id % a.njobs];
+    const Job job = a.job[id % a.njobs];
     id /= a.njobs;
     const int nbh = gridDim.x / (a.slices * a.njobs * a.nseg);
     const int bh = id % nbh, seg = id / nbh;
     const int b = bh / a.H, h = bh % a.H, hg = h / (a.H / a.G);
     const int v0 = slice * VS;
     if (v0 >= job.dv) return;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int m = lane & 15, q4 = 4 * (lane >> 4);
     const int late = job.reverse ? 1 : 0;
     const Rate rate(a.decay[h]);
@@ -279,202 +347,236 @@ __global__ __launch_bounds__(256) void attn_kernel(const Jobs a) {
     }
     // token r of the walk lies at first + r step
     const int64_t first = job.reverse ? len - 1 : 0, step = job.reverse ? -1 : 1;
-    const T *qp = static_cast<const T *>(job.q) + b * job.qb + first * job.qt +
-                  (job.qgroup ? hg : h) * job.dk;
-    const T *kp = static_cast<const T *>(job.k) + b * job.kb + first * job.kt +
-                  (job.kgroup ? hg : h) * job.dk;
-    const T *vp = static_cast<const T *>(job.v) + b * job.vb + first * job.vt +
-                  (job.vgroup ? hg : h) * job.dv + v0;
-    const int64_t qst = step * job.qt, kst = step * job.kt, vst = step * job.vt;
+    const int64_t t0 = first + step * r0;
+    KTile qt, kt;
+    VTile vt;
+    if constexpr (OUT)
+        qt.start(static_cast<const T *>(job.q) + b * job.qb + t0 * job.qt +
+                     (job.qgroup ? hg : h) * job.dk, job.qt, job.reverse, job.dk);
+    kt.start(static_cast<const T *>(job.k) + b * job.kb + t0 * job.kt +
+                 (job.kgroup ? hg : h) * job.dk, job.kt, job.reverse, job.dk);
+    vt.start(static_cast<const T *>(job.v) + b * job.vb + t0 * job.vt +
+                 (job.vgroup ? hg : h) * job.dv + v0, job.vt, job.reverse, job.dv - v0);
+    // the sequence's tokens in this segment: whole chunks and a cut one
+    const int64_t own = (len < r1 ? len : r1) - r0;
+    const int tokens = own < 0 ? 0 : (int)own, whole = tokens / L, cut = tokens % L;
+    int left = tokens;   // not yet on their way
+    auto fetch = [&](int buf) {
+        const int n = left < L ? left : L;
+        T *to = tiles(buf);
+        if constexpr (OUT) qt.load(to, n, wave);
+        kt.load(to + kK, n, wave);
+        vt.load(to + kV, n, wave);
+        left -= n;
+    };
 
+    const int vcol = v0 + 16 * NV * wave;    // the wavefront's first column
     f32x4 s[NV][NT];
     const int64_t sbase = (int64_t)bh * a.state_size + seg * a.seg_stride;
-    const bool given = OUT && job.s0;
+    // byte offset of element e of tile t in a state
+    auto place = [&](int v, int t, int e) {
+        const int row = tile_row<T>(t, q4 + e), col = vcol + 16 * v + m;
+        return row < job.dk && col < job.dv ? 4u * (row * job.rs + col * job.cs) : kNowhere;
+    };
 #pragma unroll
-    for (int nt = 0; nt < NV; ++nt)
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) s[nt][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (given) {
+        for (int t = 0; t < NT; ++t) s[v][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (OUT && job.s0) {
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(job.s0 + sbase, 4 * a.state_size);
 #pragma unroll
-        for (int nt = 0; nt < NV; ++nt) {
-            const int col = v0 + 16 * (NV * wave + nt) + m;
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = state_row<T>(t, q4 + r);
-                    if (row < job.dk && col < job.dv)
-                        s[nt][t][r] = job.s0[sbase + row * job.rs + col * job.cs];
-                }
-        }
+                for (int e = 0; e < 4; ++e)
+                    s[v][t][e] = __uint_as_float(
+                        __builtin_amdgcn_raw_buffer_load_b32(rs, place(v, t, e), 0, 0));
     }
 
-    float out_decay[LT], w[NB][M::kRun];
+    // outputs: a lane has 4 columns of one token of each tile
+    const bool wide = sizeof(T) == 4 || (MODE == kOutWide && job.wide);
+    const uint32_t osize = wide ? 4 : 2;
+    char *out = static_cast<char *>(job.out) +
+                (b * job.ob + (t0 - (job.reverse ? L - 1 : 0)) * job.ot + (int64_t)h * job.dv +
+                 vcol) * (int64_t)osize;      // of the chunk's lowest token
+    const int64_t out_turn = step * L * job.ot * (int64_t)osize;
+    uint32_t out_at[NV][LT];
+    float out_decay[LT], pair_decay[LT][LT][4];
     if constexpr (OUT) {
 #pragma unroll
-        for (int it = 0; it < LT; ++it)
+        for (int it = 0; it < LT; ++it) {
             out_decay[it] = job.inter * rate.over(16 * it + m + 1 - late);
-        // (pairs of a later key stay zero: no tile above the diagonal is written)
-        for (int x = threadIdx.x; x < L * PS; x += 256) ps[x] = 0;
-    }
-    auto weights = [&](int n) {   // of an update by n tokens
+            const int i = job.reverse ? L - 1 - 16 * it - m : 16 * it + m;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < M::kRun; ++e) {
-                const int j = M::kDepth * nb + M::kRun * (lane >> 4) + e;
-                w[nb][e] = j < n ? job.up * rate.over(n - 1 - j + late) : 0.f;
-            }
-    };
-    weights(L);
-    float turn = rate.over(L);
-
-    auto tokens = [&](int64_t r) {   // of the chunk at r that the sequence has
-        const int64_t n = (len < r1 ? len : r1) - r;
-        return (int)(n < 0 ? 0 : n < L ? n : L);
-    };
-    KTile qt, kt;
-    VTile vt;
-    auto fetch = [&](int64_t r) {
-        const int n = tokens(r);
-        if constexpr (OUT) qt.load(qp + r * qst, qst, n, job.dk);
-        kt.load(kp + r * kst, kst, n, job.dk);
-        vt.load(vp + r * vst, vst, n, job.dv - v0);
-    };
-    auto put = [&](int64_t t, int col, f32x4 v) {   // 4 columns of the output at token t
-        const int64_t at = b * job.ob + t * job.ot + (int64_t)h * job.dv + col;
-        if (sizeof(T) == 4 || job.wide)
-            put4(static_cast<float *>(job.out) + at, v);
-        else
-            put4(static_cast<uint16_t *>(job.out) + at, v);
-    };
-
-    bool live = given;
-    fetch(r0);
-    for (int64_t r = r0; r < r1; r += L) {
-        const int n = tokens(r);
-        const bool more = r + L < r1;
-        const int rows = (int)(r1 - r < L ? r1 - r : L);
-        lds_barrier();
-        if constexpr (OUT) qt.keep(qs);
-        kt.keep(ks);
-        vt.keep(vs);
-        if (more) fetch(r + L);
-        lds_barrier();
-        if constexpr (OUT) {
-            // pairs: tiles (token i, key j <= i), shared by the wavefronts in turn
-            int tile = 0;
-#pragma unroll
-            for (int it = 0; it < LT; ++it)
-#pragma unroll
-                for (int jt = 0; jt <= it; ++jt, ++tile) {
-                    if ((tile & 3) != wave || 16 * it >= n) continue;
-                    f32x4 p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int k = 0; k < KS; ++k)
-                        p = M::mma(natural<T>(ks, KTile::kStride, 16 * jt, M::kDepth * k, lane),
-                                   natural<T>(qs, KTile::kStride, 16 * it, M::kDepth * k, lane),
-                                   p);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int gap = 16 * (it - jt) + m - (q4 + e);
-                        p[e] = gap < 0 ? 0.f : p[e] * (job.pair * rate.over(gap));
-                    }
-                    put4(ps + (16 * it + m) * PS + 16 * jt + q4, p);
-                }
-            lds_barrier();
+            for (int v = 0; v < NV; ++v)
+                out_at[v][it] = vcol + 16 * v + q4 < job.dv
+                                    ? (uint32_t)(i * job.ot + 16 * v + q4) * osize : kNowhere;
         }
-        Frag vf[NB][NV];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int it = 0; it < LT; ++it)
 #pragma unroll
-            for (int nt = 0; nt < NV; ++nt)
-                vf[nb][nt] = across<4>(vs, VTile::kStride, M::kDepth * nb,
-                                       16 * (NV * wave + nt), lane);
+            for (int jt = 0; jt < LT; ++jt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int gap = 16 * it + m - tile_row<T>(jt, q4 + e);
+                    pair_decay[it][jt][e] = gap < 0 ? 0.f : job.pair * rate.over(gap);
+                }
+    }
+    auto put = [&](const __amdgpu_buffer_rsrc_t &rs, uint32_t at, f32x4 v) {
+        if (wide)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, at, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b64(
+                u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, rs, at, 0, 0);
+    };
+    if (threadIdx.x < 2 * L) {
+        const int j = threadIdx.x % L, n = threadIdx.x < L ? L : cut;
+        ws[threadIdx.x / L][j] = j < n ? job.up * rate.over(n - 1 - j + late) : 0.f;
+    }
+    const float turn_whole = rate.over(L), turn_cut = rate.over(cut);
+
+    // The next chunk's tiles have arrived, for all wavefronts, and this one's are free.
+    // Behind the next one's loads at least the later chunks' loads and this chunk's stores
+    // have been issued, and may still be on their way.
+    auto turn_buffers = [&](bool stored) {
+        constexpr int loads = (OUT ? KTile::kPieces : 0) + KTile::kPieces + VTile::kPieces;
+        constexpr int later = (kAhead - 1) * loads, stores = OUT ? NV * LT : 0;
+        __builtin_amdgcn_sched_barrier(0);
+        if (stored) wait_vmcnt<later + stores>();
+        else wait_vmcnt<later>();
+        lds_barrier();
+    };
+    // one chunk, whole or (the last) cut
+    auto chunk = [&](int buf, auto flag) {
+        constexpr bool WHOLE = decltype(flag)::value;
+        if constexpr (WHOLE) {
+            fetch(buf + kAhead < NBUF ? buf + kAhead : buf + kAhead - NBUF);
+            __builtin_amdgcn_sched_barrier(0);   // (left alone, the loads sink to the chunk's end)
+        }
+        const T *qc = tiles(buf), *kc = qc + kK, *vc = qc + kV;
+        Frag vf[NV][NB];
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+                vf[v][nb] = across<VS, 4>(vc, M::kDepth * nb, 16 * (NV * wave + v), lane);
         if constexpr (OUT) {
-            f32x4 o[LT][NV];
+            f32x4 o[NV][LT];
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int it = 0; it < LT; ++it) o[v][it] = f32x4{0.f, 0.f, 0.f, 0.f};
+            f32x4 p[LT][LT];    // weights of pairs: query tile, key tile
 #pragma unroll
             for (int it = 0; it < LT; ++it)
 #pragma unroll
-                for (int nt = 0; nt < NV; ++nt) o[it][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (live) {
+                for (int jt = 0; jt < LT; ++jt) p[it][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    Frag sf[NV];
+            for (int k = 0; k < KS; ++k) {
+                Frag qf[LT], kf[LT];
 #pragma unroll
-                    for (int nt = 0; nt < NV; ++nt) sf[nt] = state_frag(s[nt], k, T(0));
-#pragma unroll
-                    for (int it = 0; it < LT; ++it) {
-                        const Frag qf = natural<T>(qs, KTile::kStride, 16 * it, M::kDepth * k,
-                                                   lane);
-#pragma unroll
-                        for (int nt = 0; nt < NV; ++nt)
-                            o[it][nt] = M::mma(sf[nt], qf, o[it][nt]);
-                    }
+                for (int it = 0; it < LT; ++it) {
+                    qf[it] = natural<T, KD>(qc, 16 * it + m, M::kDepth * k, lane);
+                    kf[it] = natural<T, KD>(kc, tile_row<T>(it, m), M::kDepth * k, lane);
                 }
 #pragma unroll
                 for (int it = 0; it < LT; ++it)
 #pragma unroll
-                    for (int nt = 0; nt < NV; ++nt) o[it][nt] *= out_decay[it];
+                    for (int jt = 0; jt < LT; ++jt)
+                        if (sizeof(T) == 2 || jt <= it)
+                            p[it][jt] = M::mma(kf[jt], qf[it], p[it][jt]);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const Frag sf = tile_frag(s[v], k, T(0));
+#pragma unroll
+                    for (int it = 0; it < LT; ++it) o[v][it] = M::mma(sf, qf[it], o[v][it]);
+                }
             }
 #pragma unroll
-            for (int it = 0; it < LT; ++it)
+            for (int it = 0; it < LT; ++it) {
+#pragma unroll
+                for (int jt = 0; jt < LT; ++jt) p[it][jt] *= f4(pair_decay[it][jt]);
+#pragma unroll
+                for (int v = 0; v < NV; ++v) o[v][it] *= out_decay[it];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     if (M::kDepth * nb > 16 * it) continue;
-                    const Frag pf = natural<T>(ps, PS, 16 * it, M::kDepth * nb, lane);
+                    const Frag pf = tile_frag(p[it], nb, T(0));
 #pragma unroll
-                    for (int nt = 0; nt < NV; ++nt) o[it][nt] = M::mma(vf[nb][nt], pf, o[it][nt]);
-                }
-#pragma unroll
-            for (int it = 0; it < LT; ++it) {
-                const int i = 16 * it + m;
-                const int64_t t = i < n ? first + step * (r + i) : r + i;
-#pragma unroll
-                for (int nt = 0; nt < NV; ++nt) {
-                    const int col = v0 + 16 * (NV * wave + nt) + q4;
-                    if (i < rows && col < job.dv)
-                        put(t, col, i < n ? o[it][nt] : f32x4{0.f, 0.f, 0.f, 0.f});
+                    for (int v = 0; v < NV; ++v) o[v][it] = M::mma(vf[v][nb], pf, o[v][it]);
                 }
             }
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(out, 0xfffffff0u);
+#pragma unroll
+            for (int it = 0; it < LT; ++it)
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    put(rs, WHOLE || 16 * it + m < cut ? out_at[v][it] : kNowhere, o[v][it]);
+            out += out_turn;
         }
-        if (n > 0 && (more || job.s1)) {
-            if (n < L) {
-                weights(n);
-                turn = rate.over(n);
-            }
+        if (WHOLE || job.s1) {
+            const float turn = WHOLE ? turn_whole : turn_cut;
+            const float *w = ws[!WHOLE] + M::kRun * (lane >> 4);
 #pragma unroll
-            for (int nt = 0; nt < NV; ++nt)
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) s[nt][t] *= turn;
+                for (int t = 0; t < NT; ++t) s[v][t] *= turn;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-                decltype(weighted(Frag(), w[0])) wv[NV];
+                decltype(weighted(Frag(), w)) wv[NV];
 #pragma unroll
-                for (int nt = 0; nt < NV; ++nt) wv[nt] = weighted(vf[nb][nt], w[nb]);
+                for (int v = 0; v < NV; ++v) wv[v] = weighted(vf[v][nb], w + M::kDepth * nb);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const Frag kf = state_cols<T>(ks, KTile::kStride, M::kDepth * nb, t, lane);
+                    const Frag kf = state_cols<T, KD>(kc, M::kDepth * nb, t, lane);
 #pragma unroll
-                    for (int nt = 0; nt < NV; ++nt) s[nt][t] = mma_weighted(kf, wv[nt], s[nt][t]);
+                    for (int v = 0; v < NV; ++v) s[v][t] = mma_weighted(kf, wv[v], s[v][t]);
                 }
             }
-            live = true;
         }
-    }
-    if (job.s1) {
+        if constexpr (WHOLE) {
+            turn_buffers(true);
+        }
+    };
+    if (tokens > 0) {
+        // (chunks past the last read as zeros)
 #pragma unroll
-        for (int nt = 0; nt < NV; ++nt) {
-            const int col = v0 + 16 * (NV * wave + nt) + m;
+        for (int i = 0; i < kAhead; ++i) fetch(i);
+        turn_buffers(false);
+        int c = 0;
+        for (; c + NBUF <= whole; c += NBUF)
+#pragma unroll
+            for (int i = 0; i < NBUF; ++i) chunk(i, Const<true>());
+        int buf = 0;
+        for (; c < whole; ++c, ++buf) chunk(buf, Const<true>());
+        if (cut) chunk(buf, Const<false>());
+    }
+    if constexpr (OUT)   // zeros behind the sequence
+        for (int64_t t = r0 + tokens; t < r1; t += L) {
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(
+                static_cast<char *>(job.out) +
+                    (b * job.ob + t * job.ot + (int64_t)h * job.dv + vcol) * (int64_t)osize,
+                0xfffffff0u);
+#pragma unroll
+            for (int it = 0; it < LT; ++it)
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+                    put(rs, t + 16 * it + m < r1 && out_at[v][it] != kNowhere
+                                ? (uint32_t)((16 * it + m) * job.ot + 16 * v + q4) * osize
+                                : kNowhere,
+                        f32x4{0.f, 0.f, 0.f, 0.f});
+        }
+    if (job.s1) {
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(job.s1 + sbase, 4 * a.state_size);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = state_row<T>(t, q4 + e);
-                    if (row < job.dk && col < job.dv)
-                        job.s1[sbase + row * job.rs + col * job.cs] = s[nt][t][e];
-                }
-        }
+                for (int e = 0; e < 4; ++e)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s[v][t][e]), rs,
+                                                          place(v, t, e), 0, 0);
     }
 }
 
@@ -538,22 +640,24 @@ __global__ __launch_bounds__(256) void attn_share_kernel(const float *__restrict
 int pad_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 template <typename T, int KD, int NV>
-void launch_jobs_t(const Jobs &j, bool out, uint32_t blocks, hipStream_t st) {
-    if (out)
-        attn_kernel<T, KD, NV, true><<<blocks, 256, 0, st>>>(j);
-    else
-        attn_kernel<T, KD, NV, false><<<blocks, 256, 0, st>>>(j);
+void launch_jobs_t(const Jobs &j, Mode mode, uint32_t blocks, hipStream_t st) {
+    if (mode == kStateOnly)
+        attn_kernel<T, KD, NV, kStateOnly><<<blocks, 256, 0, st>>>(j);
+    else if (mode == kOut || sizeof(T) == 4)
+        attn_kernel<T, KD, NV, kOut><<<blocks, 256, 0, st>>>(j);
+    else if constexpr (sizeof(T) == 2)
+        attn_kernel<T, KD, NV, kOutWide><<<blocks, 256, 0, st>>>(j);
 }
 template <typename T>
-void launch_jobs_kd(int kd, int nv, const Jobs &j, bool out, uint32_t blocks, hipStream_t st) {
+void launch_jobs_kd(int kd, int cols, const Jobs &j, Mode mode, uint32_t blocks, hipStream_t st) {
     if (kd == 64)
-        nv == 2 ? launch_jobs_t<T, 64, 2>(j, out, blocks, st)
-                : launch_jobs_t<T, 64, 1>(j, out, blocks, st);
+        cols == 128 ? launch_jobs_t<T, 64, 2>(j, mode, blocks, st)
+                    : launch_jobs_t<T, 64, 1>(j, mode, blocks, st);
     else if (kd == 128)
-        nv == 2 ? launch_jobs_t<T, 128, 2>(j, out, blocks, st)
-                : launch_jobs_t<T, 128, 1>(j, out, blocks, st);
+        cols == 128 ? launch_jobs_t<T, 128, 2>(j, mode, blocks, st)
+                    : launch_jobs_t<T, 128, 1>(j, mode, blocks, st);
     else
-        launch_jobs_t<T, 256, 1>(j, out, blocks, st);
+        launch_jobs_t<T, 256, 1>(j, mode, blocks, st);
 }
 
 // Launches all jobs, those of one padded row count together.
@@ -562,19 +666,21 @@ hipError_t launch_jobs(const AttnArgs &a, const Jobs &all, bool out, int v_cols,
         Jobs j = all;
         j.njobs = 0;
         int dv = 0;
+        Mode mode = out ? kOut : kStateOnly;
         for (int i = 0; i < all.njobs; ++i)
             if (pad_dim(all.job[i].dk) == kd) {
                 j.job[j.njobs++] = all.job[i];
                 dv = all.job[i].dv > dv ? all.job[i].dv : dv;
+                if (out && all.job[i].wide) mode = kOutWide;
             }
         if (!j.njobs) continue;
-        const int nv = kd == 256 ? 1 : v_cols / 64;
-        j.slices = (dv + 64 * nv - 1) / (64 * nv);
+        const int cols = kd == 256 ? 64 : v_cols;
+        j.slices = (dv + cols - 1) / cols;
         const uint32_t blocks = (uint32_t)(a.Bt * a.H * j.njobs * j.slices * j.nseg);
         if (a.bf16)
-            launch_jobs_kd<uint16_t>(kd, nv, j, out, blocks, st);
+            launch_jobs_kd<uint16_t>(kd, cols, j, mode, blocks, st);
         else
-            launch_jobs_kd<float>(kd, nv, j, out, blocks, st);
+            launch_jobs_kd<float>(kd, cols, j, mode, blocks, st);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -619,17 +725,16 @@ size_t state_floats(const AttnArgs &a) { return (size_t)(a.Bt * a.H) * a.K * a.V
 
 AttnLayout layout_of(const AttnArgs &a, int jobs) {
     AttnLayout l;
+    const int wide = jobs > 1 && a.K > a.V ? a.K : a.V;
     l.v_cols = 64;
-    const int64_t wide = a.K > a.V ? a.K : a.V;
-    const int64_t groups = a.Bt * a.H * jobs * ((jobs > 1 ? wide : a.V) + 63) / 64;
-    int64_t seg = groups ? (512 + groups - 1) / groups : 1;
-    const int64_t most = a.T / 512;
+    const int64_t groups = a.Bt * a.H * jobs * ((wide + l.v_cols - 1) / l.v_cols);
+    int64_t seg = groups ? 256 / groups : 1;
+    const int64_t most = a.T / 256;
     seg = seg < most ? seg : most;
     seg = seg < 1 ? 1 : seg;
     l.seg_tokens = (a.T + seg - 1) / seg;
-    l.seg_tokens = (l.seg_tokens + 63) / 64 * 64;
+    l.seg_tokens = (l.seg_tokens + kChunk - 1) / kChunk * kChunk;
     l.segments = l.seg_tokens ? (a.T + l.seg_tokens - 1) / l.seg_tokens : 1;
-    if (l.segments < 1) l.segments = 1;
     return l;
 }
 
