@@ -177,7 +177,7 @@ ssd_status check_w4(const ssd_w4_dims *d, bool linear, ssd::W4Args *a) {
     CHECK(check_range("outputs", d->outputs, 1, int64_t(1) << 24));
     CHECK(check_io(d->io_dtype));
     if (linear) CHECK(check_stride("x_row_stride", d->x_row_stride,
-                                   d->io_dtype == SSD_BF16 ? 8 : 4));
+                                   d->io_dtype == SSD_BF16 ? 8 : 4, kMaxTokenStride));
     *a = ssd::W4Args{};
     a->rows = linear ? d->rows : 0;
     a->inputs = d->inputs;
