@@ -325,19 +325,19 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void norm_bwd_kernel(const N
             if (at.in[k])
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    p[at.c[k] + e] = dw[k][e];
-                    p[a.C + at.c[k] + e] = db[k][e];
+                    if (a.dweight) p[at.c[k] + e] = dw[k][e];
+                    if (a.dbias) p[a.C + at.c[k] + e] = db[k][e];
                 }
     }
 }
 
-// dweight and dbias: the runs' sums in order, in double; 16 lanes share a channel's
-// runs, 16 channels a workgroup.
-__global__ __launch_bounds__(256) void norm_sum_kernel(const float *__restrict__ part,
-                                                       int64_t runs, int64_t C,
-                                                       float *__restrict__ dweight,
-                                                       float *__restrict__ dbias) {
-    __shared__ double sums[16][17];
+// dweight and dbias: the runs' sums in order, in double.  A workgroup takes 16 channels:
+// 16 lanes read them, 4 sets of lanes of each wavefront and 16 wavefronts share the runs.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(const float *__restrict__ part,
+                                                        int64_t runs, int64_t C,
+                                                        float *__restrict__ dweight,
+                                                        float *__restrict__ dbias) {
+    __shared__ double sums[64][17];
     float *out = blockIdx.y ? dbias : dweight;
     if (!out) return;
     const int i = threadIdx.x >> 4, m = threadIdx.x & 15;
@@ -345,39 +345,45 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(const float *__restrict__
     const float *p = part + blockIdx.y * C + c;
     double s = 0.0;
     if (c < C)
-        for (int64_t r = i; r < runs; r += 16) s += (double)p[r * 2 * C];
+#pragma unroll 4
+        for (int64_t r = i; r < runs; r += 64) s += (double)p[r * 2 * C];
     sums[i][m] = s;
     __syncthreads();
     if (i == 0 && c < C) {
-        for (int k = 1; k < 16; ++k) s += sums[k][m];
+        for (int k = 1; k < 64; ++k) s += sums[k][m];
         out[c] = (float)s;
     }
 }
 
 // How rows lie on lanes: accesses of 16 bytes where groups, strides and starts allow
-// them, else of single channels; as few lanes a row as hold it in 4 accesses each.
+// them, else of single channels; a wavefront or less holds a row in one access a lane, a
+// workgroup in up to 4 (4 x 2048 tokens of 2048 channels, gradients, 4 accesses on a
+// wavefront: 149 us, 1 on a workgroup: 54).
 struct NormShape {
     int vec, vpt, tpr;
 };
 bool aligned16(const void *p) { return !(reinterpret_cast<uintptr_t>(p) & 15u); }
-NormShape shape_of(const NormArgs &a, bool bwd) {
+NormShape shape_of(const NormArgs &a) {
     const int e = a.bf16 ? 2 : 4, v = 16 / e;
     const int64_t S = a.C / a.groups;
-    NormShape s;
     const bool wide = S % v == 0 && aligned16(a.x) && aligned16(a.z) && a.xb % v == 0 &&
                       a.xt % v == 0 && (!a.z || (a.zb % v == 0 && a.zt % v == 0));
+    NormShape s;
     s.vec = wide ? v : 1;
     const int64_t n = S / s.vec;
-    s.vpt = n <= 16 ? 1 : n <= 4096 ? 4 : 16;
-    s.tpr = n <= 64 ? 16 : n <= 256 ? 64 : n <= 1024 ? 256 : 1024;
-    (void)bwd;
+    s.tpr = n <= 16 ? 16 : n <= 64 ? 64 : n <= 1024 ? 256 : 1024;
+    const int64_t vpt = (n + s.tpr - 1) / s.tpr;
+    s.vpt = vpt <= 4 ? (int)vpt : 16;
     return s;
 }
+// Tokens of a lane's run: long ones load weights and leave partial sums seldom, but leave
+// CUs idle.  Forward, runs as long as leaves 1024 workgroups, up to 8 (4 x 2048 tokens of
+// 2048 channels, gated, whole calls: runs of 1, 4, 8, 16: 35, 22, 22, 32 us); gradients, 512
+// and 32 (runs of 4, 8, 16, 32: 59, 47, 47, 70 us).
 int64_t run_of(const NormArgs &a, const NormShape &s, bool bwd) {
     const int64_t rows = s.tpr >= 256 ? 1 : 256 / s.tpr;
-    const int64_t tokens = a.Bt * a.T;
-    int64_t run = tokens * a.groups / (rows * 2048);
-    const int64_t most = bwd ? 64 : 16;
+    const int64_t blocks = a.Bt * a.T * a.groups / rows;
+    const int64_t run = blocks / (bwd ? 512 : 1024), most = bwd ? 32 : 8;
     return run < 1 ? 1 : run > most ? most : run;
 }
 
@@ -412,12 +418,21 @@ void launch_form(const NormWork &w, hipStream_t st) {
 }
 template <typename T, int VEC, bool BWD>
 void launch_shape(const NormWork &w, const NormShape &s, hipStream_t st) {
-    if (s.vpt == 1) launch_form<T, VEC, 1, 16, BWD>(w, st);
-    else if (s.tpr == 16) launch_form<T, VEC, 4, 16, BWD>(w, st);
-    else if (s.tpr == 64) launch_form<T, VEC, 4, 64, BWD>(w, st);
-    else if (s.tpr == 256) launch_form<T, VEC, 4, 256, BWD>(w, st);
-    else if (s.vpt == 4) launch_form<T, VEC, 4, 1024, BWD>(w, st);
-    else if constexpr (VEC == 1) launch_form<T, 1, 16, 1024, BWD>(w, st);
+    if (s.tpr == 16)
+        launch_form<T, VEC, 1, 16, BWD>(w, st);
+    else if (s.tpr == 64)
+        launch_form<T, VEC, 1, 64, BWD>(w, st);
+    else if (s.tpr == 256) {
+        switch (s.vpt) {
+            case 1: launch_form<T, VEC, 1, 256, BWD>(w, st); break;
+            case 2: launch_form<T, VEC, 2, 256, BWD>(w, st); break;
+            case 3: launch_form<T, VEC, 3, 256, BWD>(w, st); break;
+            default: launch_form<T, VEC, 4, 256, BWD>(w, st); break;
+        }
+    } else if (s.vpt <= 4)
+        launch_form<T, VEC, 4, 1024, BWD>(w, st);
+    else if constexpr (VEC == 1)
+        launch_form<T, 1, 16, 1024, BWD>(w, st);
 }
 template <bool BWD>
 void launch_type(const NormWork &w, const NormShape &s, hipStream_t st) {
@@ -443,7 +458,7 @@ size_t norm_bwd_workspace(const NormArgs &a) {
         NormArgs b = a;
         b.x = b.z = nullptr;
         b.xb = b.xt = b.zb = b.zt = vec ? 0 : 1;
-        const NormShape s = shape_of(b, true);
+        const NormShape s = shape_of(b);
         const int64_t run = run_of(b, s, true), n = (a.Bt * a.T + run - 1) / run;
         most = n > most ? n : most;
     }
@@ -451,7 +466,7 @@ size_t norm_bwd_workspace(const NormArgs &a) {
 }
 
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t st) {
-    const NormShape s = shape_of(a, false);
+    const NormShape s = shape_of(a);
     launch_type<false>(work_of(a, s, false), s, st);
     return hipGetLastError();
 }
@@ -462,7 +477,7 @@ hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st) {
     if (!sums) b.part = nullptr;
     int64_t runs = 0;
     if (a.Bt > 0 && a.T > 0) {
-        const NormShape s = shape_of(b, true);
+        const NormShape s = shape_of(b);
         const NormWork w = work_of(b, s, true);
         runs = w.units / a.groups;
         launch_type<true>(w, s, st);
@@ -470,7 +485,7 @@ hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t st) {
         if (e != hipSuccess) return e;
     }
     if (sums)
-        norm_sum_kernel<<<dim3((uint32_t)((a.C + 15) / 16), 2), 256, 0, st>>>(
+        norm_sum_kernel<<<dim3((uint32_t)((a.C + 15) / 16), 2), 1024, 0, st>>>(
             a.part, runs, a.C, a.dweight, a.dbias);
     return hipGetLastError();
 }
