@@ -567,8 +567,10 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(const Jobs a) {
                                 : kNowhere,
                         f32x4{0.f, 0.f, 0.f, 0.f});
         }
-    if (job.s1) {
-        const __amdgpu_buffer_rsrc_t rs = make_rsrc(job.s1 + sbase, 4 * a.state_size);
+    // (with outputs, s1 is the state behind the last segment)
+    if (job.s1 && (!OUT || seg == a.nseg - 1)) {
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(
+            job.s1 + (OUT ? (int64_t)bh * a.state_size : sbase), 4 * a.state_size);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -580,12 +582,11 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(const Jobs a) {
     }
 }
 
-// The states before each segment from the segments' own ends (in place), and the
-// state behind the last: four elements of one (b, h) per lane, segments in order.
+// The states before each segment from the segments' own ends (in place; the last one's
+// end is not among them): four elements of one (b, h) per lane, segments in order.
 struct Chain {
     float *seg;                // [nseg][Bt H][K V]
     const float *start;        // [Bt H][K V] or NULL
-    float *end;                // [Bt H][K V] or NULL: then the last segment's end is not read
 };
 struct Chains {
     Chain c[2];
@@ -613,28 +614,32 @@ __global__ __launch_bounds__(256) void attn_chain_kernel(const Chains a) {
         int64_t n = len - sg * a.seg_tokens;
         n = n < 0 ? 0 : n < a.seg_tokens ? n : a.seg_tokens;
         f32x4 own = {0.f, 0.f, 0.f, 0.f};
-        if (sg + 1 < a.nseg || c.end) own = *reinterpret_cast<const f32x4 *>(p);
+        if (sg + 1 < a.nseg) own = *reinterpret_cast<const f32x4 *>(p);
         *reinterpret_cast<f32x4 *>(p) = cur;
-        const float d = rate.over((int)n);
-        cur = d * cur + own;
+        cur = rate.over((int)n) * cur + own;
     }
-    if (c.end) *reinterpret_cast<f32x4 *>(c.end + at) = cur;
 }
 
 // Sums of float32 rows over the heads that share a key or value head, four columns a
-// lane, heads in order.
+// lane, heads in order; dk and dv in one launch.
+struct Share {
+    const float *part[2];
+    void *out[2];
+    int64_t n4[2];
+    int32_t dim4[2];
+    int32_t rep;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void attn_share_kernel(const float *__restrict__ part,
-                                                         T *__restrict__ out, int64_t n4, int dim4,
-                                                         int G, int rep) {
+__global__ __launch_bounds__(256) void attn_share_kernel(const Share a) {
+    const int w = blockIdx.y;
     const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (x >= n4) return;
+    if (x >= a.n4[w]) return;
+    const int dim4 = a.dim4[w];
     const int64_t row = x / dim4;            // (token, group)
-    const int c = (int)(x % dim4);
-    const f32x4 *p = reinterpret_cast<const f32x4 *>(part) + row * rep * dim4 + c;
+    const f32x4 *p = reinterpret_cast<const f32x4 *>(a.part[w]) + row * a.rep * dim4 + x % dim4;
     f32x4 v = p[0];
-    for (int i = 1; i < rep; ++i) v += p[(int64_t)i * dim4];
-    put4(out + 4 * x, v);
+    for (int i = 1; i < a.rep; ++i) v += p[(int64_t)i * dim4];
+    put4(static_cast<T *>(a.out[w]) + 4 * x, v);
 }
 
 int pad_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
@@ -660,15 +665,23 @@ void launch_jobs_kd(int kd, int cols, const Jobs &j, Mode mode, uint32_t blocks,
         launch_jobs_t<T, 256, 1>(j, mode, blocks, st);
 }
 
-// Launches all jobs, those of one padded row count together.
+// Launches all jobs, those of one padded row count together; all of them where they do not
+// fill the chip, since then the launches' times add up and the padding costs nothing
+// (gradients of 2 x 333 tokens, 6 heads of 64 and 96, float32: 95 us in two launches).
 hipError_t launch_jobs(const AttnArgs &a, const Jobs &all, bool out, int v_cols, hipStream_t st) {
+    int widest = 0, most = 0;
+    for (int i = 0; i < all.njobs; ++i) {
+        widest = all.job[i].dk > widest ? all.job[i].dk : widest;
+        most = all.job[i].dv > most ? all.job[i].dv : most;
+    }
+    const bool together = a.Bt * a.H * all.njobs * all.nseg * ((most + 63) / 64) <= 256;
     for (int kd = 64; kd <= 256; kd *= 2) {
         Jobs j = all;
         j.njobs = 0;
         int dv = 0;
         Mode mode = out ? kOut : kStateOnly;
         for (int i = 0; i < all.njobs; ++i)
-            if (pad_dim(all.job[i].dk) == kd) {
+            if (pad_dim(together ? widest : all.job[i].dk) == kd) {
                 j.job[j.njobs++] = all.job[i];
                 dv = all.job[i].dv > dv ? all.job[i].dv : dv;
                 if (out && all.job[i].wide) mode = kOutWide;
@@ -723,17 +736,24 @@ Job fwd_job(const AttnArgs &a) {
 
 size_t state_floats(const AttnArgs &a) { return (size_t)(a.Bt * a.H) * a.K * a.V; }
 
+// 64 columns a workgroup, unless 128 leave between 6 and 8 workgroups for 8 CUs (5
+// sequences of 40 heads of 128, 4096 tokens: 228 us, with 64 columns 272; 8 sequences 422
+// and 390; 4 of 32 heads 218 and 151).
+// Segments where at most half the CUs would have one: then up to two a CU, of 256 tokens
+// or more, though keys and values are read and the states formed twice (1 x 65536 tokens of
+// 16 heads: 1, 4, 8, 16, 32 segments 1867, 743, 445, 415, 430 us; 1 x 2048: 1, 4, 8, 16:
+// 65, 40, 33, 36; 4 sequences of 32 heads, 256 workgroups, 1 and 2: 151 and 225).
 AttnLayout layout_of(const AttnArgs &a, int jobs) {
     AttnLayout l;
-    const int wide = jobs > 1 && a.K > a.V ? a.K : a.V;
-    l.v_cols = 64;
-    const int64_t groups = a.Bt * a.H * jobs * ((wide + l.v_cols - 1) / l.v_cols);
-    int64_t seg = groups ? 256 / groups : 1;
+    const int64_t wide = jobs > 1 && a.K > a.V ? a.K : a.V;
+    const int64_t rows = a.Bt * a.H * jobs, half = rows * ((wide + 127) / 128);
+    l.v_cols = wide > 64 && half > 192 && half <= 256 ? 128 : 64;
+    const int64_t groups = rows * ((wide + l.v_cols - 1) / l.v_cols);
+    int64_t seg = groups > 0 && groups <= 128 ? 512 / groups : 1;
     const int64_t most = a.T / 256;
     seg = seg < most ? seg : most;
     seg = seg < 1 ? 1 : seg;
-    l.seg_tokens = (a.T + seg - 1) / seg;
-    l.seg_tokens = (l.seg_tokens + kChunk - 1) / kChunk * kChunk;
+    l.seg_tokens = ((a.T + seg - 1) / seg + kChunk - 1) / kChunk * kChunk;
     l.segments = l.seg_tokens ? (a.T + l.seg_tokens - 1) / l.seg_tokens : 1;
     return l;
 }
@@ -753,14 +773,6 @@ hipError_t launch_chain(const AttnArgs &a, const AttnLayout &l, const Chain *c, 
     x.blocks = (x.state_size + 1023) / 1024;
     attn_chain_kernel<<<dim3((uint32_t)(a.Bt * a.H * x.blocks), n), 256, 0, st>>>(x);
     return hipGetLastError();
-}
-
-template <typename T>
-void launch_share_t(const float *part, void *out, int64_t rows, int dim, int64_t G, int rep,
-                    hipStream_t st) {
-    const int64_t n4 = rows * (dim / 4);
-    attn_share_kernel<T><<<(uint32_t)((n4 + 255) / 256), 256, 0, st>>>(
-        part, static_cast<T *>(out), n4, dim / 4, (int)G, rep);
 }
 
 }  // namespace
@@ -798,12 +810,12 @@ hipError_t launch_attn_fwd(const AttnArgs &a, hipStream_t st) {
         j.seg_stride = (int64_t)state_floats(a);
         Jobs s = j;
         s.job[0].s1 = seg;
+        --s.nseg;
         hipError_t e = launch_jobs(a, s, false, l.v_cols, st);
         if (e != hipSuccess) return e;
-        const Chain c = {seg, a.init, a.fin};
+        const Chain c = {seg, a.init};
         if ((e = launch_chain(a, l, &c, 1, st)) != hipSuccess) return e;
         j.job[0].s0 = seg;
-        j.job[0].s1 = nullptr;
     }
     return launch_jobs(a, j, true, l.v_cols, st);
 }
@@ -856,12 +868,12 @@ hipError_t launch_attn_bwd(const AttnArgs &a, hipStream_t st) {
         s.job[1] = dv;
         s.job[1].s1 = dseg;
         s.njobs = 2;
+        --s.nseg;
         if ((e = launch_jobs(a, s, false, l.v_cols, st)) != hipSuccess) return e;
-        const Chain c[2] = {{hseg, a.init, nullptr}, {dseg, a.dfinal, a.dinit}};
+        const Chain c[2] = {{hseg, a.init}, {dseg, a.dfinal}};
         if ((e = launch_chain(a, l, c, 2, st)) != hipSuccess) return e;
         dq.s0 = hseg;
         dk.s0 = dv.s0 = dseg;
-        dv.s1 = nullptr;
     }
     j.job[0] = dq;
     j.job[1] = dk;
@@ -870,15 +882,18 @@ hipError_t launch_attn_bwd(const AttnArgs &a, hipStream_t st) {
     if ((e = launch_jobs(a, j, true, l.v_cols, st)) != hipSuccess || !shared ||
         a.T == 0)
         return e;
-    const int rep = (int)(a.H / a.G);
+    Share x;
     const int64_t rows = a.Bt * a.T * a.G;
-    if (a.bf16) {
-        launch_share_t<uint16_t>(pk, a.dk, rows, a.K, a.G, rep, st);
-        launch_share_t<uint16_t>(pv, a.dv, rows, a.V, a.G, rep, st);
-    } else {
-        launch_share_t<float>(pk, a.dk, rows, a.K, a.G, rep, st);
-        launch_share_t<float>(pv, a.dv, rows, a.V, a.G, rep, st);
-    }
+    x.part[0] = pk, x.out[0] = a.dk, x.dim4[0] = a.K / 4;
+    x.part[1] = pv, x.out[1] = a.dv, x.dim4[1] = a.V / 4;
+    x.rep = (int32_t)(a.H / a.G);
+    for (int i = 0; i < 2; ++i) x.n4[i] = rows * x.dim4[i];
+    const int64_t n4 = x.n4[0] > x.n4[1] ? x.n4[0] : x.n4[1];
+    const dim3 grid((uint32_t)((n4 + 255) / 256), 2);
+    if (a.bf16)
+        attn_share_kernel<uint16_t><<<grid, 256, 0, st>>>(x);
+    else
+        attn_share_kernel<float><<<grid, 256, 0, st>>>(x);
     return hipGetLastError();
 }
 
@@ -890,7 +905,9 @@ namespace {
 // workgroup serves one (b, h): LPR lanes cover a row of the state with 16-byte
 // accesses, so 256 / LPR rows are in flight per access, kBatch accesses before
 // the first is used; a lane's four columns are summed over its rows in
-// registers and over the workgroup's rows through LDS, in a fixed order.
+// registers and over the workgroup's rows through LDS, in a fixed order.  (256 sequences
+// of 32 heads of 128 x 128: 206 us, 5.2 TB/s; kBatch 2, 8, 16: 209, 200, 228, and with 64 x
+// 64 states 103, 103, 105, 162 for 2, 4, 8, 16.)
 template <typename T, int LPR>
 __global__ __launch_bounds__(256) void attn_step_kernel(const AttnArgs a) {
     constexpr int RPI = 256 / LPR;     // rows per access of the workgroup
