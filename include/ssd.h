@@ -659,7 +659,7 @@ ssd_status ssd_cache_read(const void *codes, const float *scales, int64_t n, int
  *   k           [Bt, T, G, K]     io dtype  in   tokens and sequences lie the
  *   v           [Bt, T, G, V]     io dtype  in   strides apart (slices of one
  *               projection's rows are read in place); strides must be multiples
- *               of 16 bytes
+ *               of 16 bytes, those between tokens at most 2^24 elements
  *   log_decay   [H]               float32   in   <= 0; 0 never forgets, and below
  *               -1024 (-infinity included) a token forgets all before it
  *   init_state  [Bt, H, K, V]     float32   in   NULL = zeros
@@ -677,7 +677,10 @@ ssd_status ssd_cache_read(const void *codes, const float *scales, int64_t n, int
  * init_state (or zeros) and the token tensors may be NULL.  States, their
  * updates and all sums are float32; for bf16 the weights of a chunk's pairs of
  * tokens and the state as q's operand are rounded to bf16, and y once more.
- * No atomics: reruns are bitwise identical.
+ * No atomics: reruns are bitwise identical.  An infinity or a NaN in a token's q, k or v
+ * reaches no output of an earlier token, of another sequence or of a head that does not
+ * read it (the gradients: of a later token, likewise).  The products q_t.k_s of finite
+ * tokens must not overflow, those of s > t included.
  */
 typedef struct {
     int64_t batch;           /* Bt >= 0 */
@@ -823,11 +826,11 @@ ssd_status ssd_group_norm_bwd(const void *x, const void *z, const float *weight,
  * many rows: a library's matrix product), rounded once to the io dtype.
  * ssd_w4_linear forms y = x w^T + bias:
  *   x    [rows, inputs]   io dtype  in   rows x_row_stride elements apart (a
- *        multiple of 16 bytes)
+ *        multiple of 16 bytes, at most 2^24 elements)
  *   bias [outputs]        float32   in   NULL = none
  *   y    [rows, outputs]  io dtype  out  dense
- * Products are exact and sums float32; one rounding to the io dtype.  Any number
- * of rows is computed; the weights are read once for every 64 of them.
+ * Products are exact and sums float32; one rounding to the io dtype.  Up to 2^20 - 16
+ * rows are computed; the weights are read once for every 64 of them (float32: 32).
  * inputs is a multiple of group; outputs >= 1.
  */
 typedef struct {

@@ -29,10 +29,6 @@ __device__ __forceinline__ float sigm(float z) {
     return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * z));
 }
 
-template <typename T, int VEC>
-struct Lane {
-    float v[VEC];
-};
 template <int VEC, typename T>
 __device__ __forceinline__ void load_vec(float *v, const T *p) {
     if constexpr (VEC == 1) {
@@ -376,6 +372,12 @@ NormShape shape_of(const NormArgs &a) {
     s.vpt = vpt <= 4 ? (int)vpt : 16;
     return s;
 }
+// the shape with strides that do, or do not, allow wide accesses
+NormShape any_shape(NormArgs a, bool wide) {
+    a.x = a.z = nullptr;
+    a.xb = a.xt = a.zb = a.zt = wide ? 0 : 1;
+    return shape_of(a);
+}
 // Tokens of a lane's run: long ones load weights and leave partial sums seldom, but leave
 // CUs idle.  Forward, runs as long as leaves 1024 workgroups, up to 8 (4 x 2048 tokens of
 // 2048 channels, gated, whole calls: runs of 1, 4, 8, 16: 35, 22, 22, 32 us); gradients, 512
@@ -447,7 +449,15 @@ void launch_type(const NormWork &w, const NormShape &s, hipStream_t st) {
 }  // namespace
 
 bool norm_fits(const NormArgs &a) {
-    return (double)a.Bt * a.T * a.groups <= (double)kMaxBlocks && a.C <= 16 * kMaxBlocks;
+    if ((double)a.Bt * a.T * a.groups > 1e12) return false;
+    // the most workgroups of any shape, forward, whose runs are the shorter ones
+    for (int vec = 0; vec < 2; ++vec) {
+        const NormShape s = any_shape(a, vec);
+        const int64_t rows = s.tpr >= 256 ? 1 : 256 / s.tpr, threads = s.tpr > 256 ? s.tpr : 256;
+        if ((work_of(a, s, false).units + rows - 1) / rows > kMaxBlocks * 256 / threads)
+            return false;
+    }
+    return true;
 }
 
 size_t norm_bwd_workspace(const NormArgs &a) {
@@ -455,11 +465,7 @@ size_t norm_bwd_workspace(const NormArgs &a) {
     // the most runs of any shape that the strides may lead to
     int64_t most = 0;
     for (int vec = 0; vec < 2; ++vec) {
-        NormArgs b = a;
-        b.x = b.z = nullptr;
-        b.xb = b.xt = b.zb = b.zt = vec ? 0 : 1;
-        const NormShape s = shape_of(b);
-        const int64_t run = run_of(b, s, true), n = (a.Bt * a.T + run - 1) / run;
+        const int64_t run = run_of(a, any_shape(a, vec), true), n = (a.Bt * a.T + run - 1) / run;
         most = n > most ? n : most;
     }
     return (size_t)most * 2 * a.C * 4;

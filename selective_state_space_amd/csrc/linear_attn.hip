@@ -152,6 +152,29 @@ __device__ __forceinline__ f32x4 across(const float *tile, int r0, int c0, int l
     return v;
 }
 
+// Single elements of such tiles: the product of two rows, four columns of one.
+template <typename T, int COLS>
+__device__ __forceinline__ f32x4 row4(const T *tile, int row, int c) {
+    typedef Lds<T, COLS> S;
+    const T *p = tile + row * COLS + ((c / S::kVec) ^ S::order(row)) * S::kVec + c % S::kVec;
+    if constexpr (sizeof(T) == 4) {
+        return *reinterpret_cast<const f32x4 *>(p);
+    } else {
+        const u32x2 u = *reinterpret_cast<const u32x2 *>(p);
+        return f32x4{bf16_lo(u[0]), bf16_hi(u[0]), bf16_lo(u[1]), bf16_hi(u[1])};
+    }
+}
+template <typename T, int COLS>
+__device__ __forceinline__ float dot_rows(const T *a, int i, const T *b, int j) {
+    float s = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < COLS; c += 4) {
+        const f32x4 x = row4<T, COLS>(a, i, c), y = row4<T, COLS>(b, j, c);
+        for (int e = 0; e < 4; ++e) s = fmaf(x[e], y[e], s);
+    }
+    return s;
+}
+
 // What accumulator row m of tile t stands for where the accumulators become an operand
 // themselves (the state's rows; the keys of a chunk's pairs): so chosen that the tiles
 // of one contraction step hold kRun consecutive ones per lane, as the other operand
@@ -297,8 +320,8 @@ struct Const {
 // that a load has kAhead chunks' time; one barrier a chunk lets the buffers turn.  Each
 // wavefront forms the chunk's pairs for itself (they are a fifth of its matrix
 // instructions): shared through LDS they needed a second barrier, and a wait for it.
-// Whole chunks run through one block of code without a branch, in which matrix and
-// vector instructions interleave.
+// Whole chunks run through one block of code whose only branch is the one for tokens that
+// are not finite, in which matrix and vector instructions interleave.
 enum Mode { kStateOnly, kOut, kOutWide };
 
 template <typename T, int KD, int NV, int MODE>
@@ -462,7 +485,7 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(const Jobs a) {
             for (int nb = 0; nb < NB; ++nb)
                 vf[v][nb] = across<VS, 4>(vc, M::kDepth * nb, 16 * (NV * wave + v), lane);
         if constexpr (OUT) {
-            f32x4 o[NV][LT];
+            f32x4 o[NV][LT], y[NV][LT];   // of the state, and with the chunk's own tokens
 #pragma unroll
             for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -498,13 +521,52 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(const Jobs a) {
 #pragma unroll
                 for (int jt = 0; jt < LT; ++jt) p[it][jt] *= f4(pair_decay[it][jt]);
 #pragma unroll
-                for (int v = 0; v < NV; ++v) o[v][it] *= out_decay[it];
+                for (int v = 0; v < NV; ++v) {
+                    o[v][it] *= out_decay[it];
+                    y[v][it] = o[v][it];
+                }
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     if (M::kDepth * nb > 16 * it) continue;
                     const Frag pf = tile_frag(p[it], nb, T(0));
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) o[v][it] = M::mma(vf[v][nb], pf, o[v][it]);
+                    for (int v = 0; v < NV; ++v) y[v][it] = M::mma(vf[v][nb], pf, y[v][it]);
+                }
+            }
+            // A token's masked pairs are weights of 0, which an infinity or a NaN in a later
+            // key or value turns into NaN: of the tokens that share a contraction with it
+            // the first has it masked, and shows it.
+            float bad = 0.f;
+#pragma unroll
+            for (int it = 0; it < LT; it += M::kDepth / 16)
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) bad = fmaf(y[v][it][e], 0.f, bad);
+            if (__builtin_expect(__ballot(!(bad == 0.f)) != 0, 0)) {
+                bool lost = false;     // what the state alone does not make of it
+#pragma unroll
+                for (int it = 0; it < LT; ++it)
+#pragma unroll
+                    for (int v = 0; v < NV; ++v)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            lost |= !(y[v][it][e] * 0.f == 0.f) && o[v][it][e] * 0.f == 0.f;
+                if (__ballot(lost)) {
+#pragma unroll
+                    for (int it = 0; it < LT; ++it) {
+#pragma unroll
+                        for (int v = 0; v < NV; ++v) y[v][it] = o[v][it];
+                        const int i = 16 * it + m;
+#pragma unroll 1
+                        for (int j = 0; j <= i; ++j) {
+                            const float w =
+                                dot_rows<T, KD>(qc, i, kc, j) * job.pair * rate.over(i - j);
+#pragma unroll
+                            for (int v = 0; v < NV; ++v)
+                                y[v][it] += w * row4<T, VS>(vc, j, 16 * (NV * wave + v) + q4);
+                        }
+                    }
                 }
             }
             const __amdgpu_buffer_rsrc_t rs = make_rsrc(out, 0xfffffff0u);
@@ -512,7 +574,7 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(const Jobs a) {
             for (int it = 0; it < LT; ++it)
 #pragma unroll
                 for (int v = 0; v < NV; ++v)
-                    put(rs, WHOLE || 16 * it + m < cut ? out_at[v][it] : kNowhere, o[v][it]);
+                    put(rs, WHOLE || 16 * it + m < cut ? out_at[v][it] : kNowhere, y[v][it]);
             out += out_turn;
         }
         if (WHOLE || job.s1) {
@@ -782,10 +844,11 @@ AttnLayout attn_bwd_layout(const AttnArgs &a) { return layout_of(a, 3); }
 
 bool attn_fits(const AttnArgs &a) {
     const double heads = (double)a.Bt * (double)a.H, wide = a.K > a.V ? a.K : a.V;
-    // the most workgroups of the recurrences (3 jobs, 4 slices; segments only while
-    // there are fewer than 512), of the chains, and of the shared heads' sums
-    return heads * 12 + 1024 <= (double)kMaxBlocks && heads * 64 <= (double)kMaxBlocks &&
-           (double)a.Bt * a.T * a.G * (wide / 1024) + 1 <= (double)kMaxBlocks;
+    // the most workgroups of the recurrences (3 jobs, 4 slices), and of the shared heads'
+    // sums (segments, and the chains between them, are taken for at most 128 workgroups);
+    // and sizes that 64 bits hold
+    return heads * 12 <= (double)kMaxBlocks && heads * (double)a.T <= 0x1p40 &&
+           (a.G == a.H || (double)a.Bt * a.T * a.G * (wide / 1024) + 1 <= (double)kMaxBlocks);
 }
 
 size_t attn_workspace(const AttnArgs &a) {

@@ -1082,6 +1082,9 @@ def _like(t, name, dtype, shape, device):
         _need(t, name, dtype, shape, device)
 
 
+_MAX_ROW_STRIDE = 1 << 24   # elements, between rows that one access may span
+
+
 def _heads_in(t, name, dtype, shape, device):
     """(t, batch stride, token stride) of [Bt,T,heads,d] or [Bt,heads,d]: in place where a
     token's heads are consecutive and every row starts on 16 bytes, else a dense copy."""
@@ -1090,7 +1093,7 @@ def _heads_in(t, name, dtype, shape, device):
     heads, d = shape[-2:]
     lead = [s if n > 1 else 0 for s, n in zip(t.stride()[:-2], shape[:-2])]
     if (t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != d) or t.data_ptr() & 15
-            or any(s % mult for s in lead)):
+            or any(s % mult for s in lead) or any(s > _MAX_ROW_STRIDE for s in lead[1:])):
         t = t.contiguous()
         if t.data_ptr() & 15:
             t = t.clone()
@@ -1369,7 +1372,8 @@ def ssd_w4_linear(x, codes, scales, bias=None, y=None):
     lead = tuple(x.shape[:-1])
     rows = lead[0] if lead else 1
     stride = x.stride(0) if lead and rows > 1 else 0
-    if x.stride(-1) != 1 or x.data_ptr() & 15 or stride * x.element_size() & 15:
+    if (x.stride(-1) != 1 or x.data_ptr() & 15 or stride * x.element_size() & 15
+            or stride > _MAX_ROW_STRIDE):
         x = x.contiguous()
         x = x.clone() if x.data_ptr() & 15 else x
         stride = K

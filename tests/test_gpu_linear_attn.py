@@ -301,3 +301,48 @@ def test_step_empty_and_decays():
     ssd.ssd_linear_attn_step(state, z(1, 2, 64), torch.ones(1, 2, 64, device="cuda"), v, decay)
     assert torch.equal(state[0, 0], before[0, 0] + v[0, 0])
     assert torch.equal(state[0, 1], v[0, 1].expand(64, 64))
+
+
+BAD = [float("nan"), float("inf"), -float("inf")]
+
+
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 72), (136, 64), (64, 256)])
+@pytest.mark.parametrize("at", [0, 1, 15, 16, 17, 31, 32, 50, 69])
+def test_what_is_not_finite_stays_behind_its_token(at, K, V, io):
+    """An infinity or a NaN in token `at` of a key, a value or a query leaves the tokens before
+    it, other sequences and other heads as they are; in a value, the other columns too."""
+    T, H, G = 70, 4, 2
+    c, kw = attn_inputs(9, 2, T, H, G, K, V, TYPES[io], init=True, grads=True)
+    dy, df = c.pop("dy"), kw.pop("dfinal")
+    y, _ = ssd.ssd_linear_attn_fwd(**c, **kw)
+    bar = attn_bar(y.dtype, terms(T, K, V))
+    for i, name in enumerate("kvq"):
+        d = {n: t.clone() for n, t in c.items()}
+        d[name][1, at, 1, 3] = BAD[(i + at) % 3]
+        got, fin = ssd.ssd_linear_attn_fwd(**d, **kw)
+        heads = slice(1, 2) if name == "q" else slice(2, 4)     # that read it
+        others = [h for h in range(H) if not (heads.start <= h < heads.stop)]
+        assert torch.equal(got[0], y[0]) and torch.equal(got[1][:, others], y[1][:, others])
+        assert_near(got[1, :at, heads], y[1, :at, heads], 2 * bar, "%s before" % name)
+        if name == "v":
+            keep = [j for j in range(V) if j != 3]
+            assert_near(got[1][:, heads][..., keep], y[1][:, heads][..., keep], 2 * bar, "columns")
+            assert not torch.isfinite(got[1, at:, heads, 3]).any()
+        else:
+            assert not torch.isfinite(got[1, at, heads]).any()
+        if name == "q":
+            assert_near(got[1, at + 1:, heads], y[1, at + 1:, heads], 2 * bar, "after")
+            assert torch.isfinite(fin).all()
+    # backwards, a bad dy reaches dk and dv of the tokens up to it, and dq of its own alone
+    want = ssd.ssd_linear_attn_bwd(**c, dy=dy, dfinal=df, **kw)
+    bad = dy.clone()
+    bad[1, at, 1, 3] = float("nan")
+    got = ssd.ssd_linear_attn_bwd(**c, dy=bad, dfinal=df, **kw)
+    for n in ("dk", "dv"):
+        assert torch.equal(got[n][0], want[n][0])
+        assert torch.equal(got[n][1, :, 1:], want[n][1, :, 1:])
+        assert_near(got[n][1, at + 1:], want[n][1, at + 1:], 2 * bar, n + " behind")
+        assert not torch.isfinite(got[n][1, at, 0]).all()
+    assert_near(got["dq"][1, :at], want["dq"][1, :at], 2 * bar, "dq before")
+    assert_near(got["dq"][1, at + 1:], want["dq"][1, at + 1:], 2 * bar, "dq behind")
