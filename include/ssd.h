@@ -739,7 +739,7 @@ ssd_status ssd_linear_attn_bwd(const void *q, const void *k, const void *v, cons
 /* How calls of these dims are laid over the chip, as ssd_conv1d_layout says it. */
 typedef struct {
     int32_t fwd_cols;       /* columns of the state that a workgroup takes: 64 or 128 */
-    int32_t bwd_cols;
+    int32_t bwd_cols;       /* (64 in those recurrences whose state has over 128 rows) */
     int64_t fwd_segments;   /* parts that a sequence is cut into over time */
     int64_t bwd_segments;
 } ssd_attn_layout;

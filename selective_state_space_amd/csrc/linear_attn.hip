@@ -798,7 +798,8 @@ Job fwd_job(const AttnArgs &a) {
 
 size_t state_floats(const AttnArgs &a) { return (size_t)(a.Bt * a.H) * a.K * a.V; }
 
-// 64 columns a workgroup, unless 128 leave between 6 and 8 workgroups for 8 CUs (5
+// 64 columns a workgroup (states of more than 128 rows have registers for no more), unless
+// 128 leave between 6 and 8 workgroups for 8 CUs (5
 // sequences of 40 heads of 128, 4096 tokens: 228 us, with 64 columns 272; 8 sequences 422
 // and 390; 4 of 32 heads 218 and 151).
 // Segments where at most half the CUs would have one: then up to two a CU, of 256 tokens
@@ -809,7 +810,8 @@ AttnLayout layout_of(const AttnArgs &a, int jobs) {
     AttnLayout l;
     const int64_t wide = jobs > 1 && a.K > a.V ? a.K : a.V;
     const int64_t rows = a.Bt * a.H * jobs, half = rows * ((wide + 127) / 128);
-    l.v_cols = wide > 64 && half > 192 && half <= 256 ? 128 : 64;
+    const int64_t narrow = jobs > 1 && a.V < a.K ? a.V : a.K;    // the fewest state rows
+    l.v_cols = wide > 64 && narrow <= 128 && half > 192 && half <= 256 ? 128 : 64;
     const int64_t groups = rows * ((wide + l.v_cols - 1) / l.v_cols);
     int64_t seg = groups > 0 && groups <= 128 ? 512 / groups : 1;
     const int64_t most = a.T / 256;
