@@ -802,10 +802,15 @@ size_t state_floats(const AttnArgs &a) { return (size_t)(a.Bt * a.H) * a.K * a.V
 // 128 leave between 6 and 8 workgroups for 8 CUs (5
 // sequences of 40 heads of 128, 4096 tokens: 228 us, with 64 columns 272; 8 sequences 422
 // and 390; 4 of 32 heads 218 and 151).
-// Segments where at most half the CUs would have one: then up to two a CU, of 256 tokens
-// or more, though keys and values are read and the states formed twice (1 x 65536 tokens of
-// 16 heads: 1, 4, 8, 16, 32 segments 1867, 743, 445, 415, 430 us; 1 x 2048: 1, 4, 8, 16:
-// 65, 40, 33, 36; 4 sequences of 32 heads, 256 workgroups, 1 and 2: 151 and 225).
+// Segments, three or more, where at most half the CUs would have a workgroup, though keys
+// and values are read and the states formed twice.  bf16: up to two workgroups a CU, of 256
+// tokens or more (1 x 65536 tokens of 16 heads: 1, 4, 8, 16, 32 segments 1867, 743, 445,
+// 415, 430 us; 1 x 2048: 1, 4, 8, 16: 65, 40, 33, 36; 1 x 512 of 8 heads, 1 and 2: 19 and 25;
+// 4 sequences of 32 heads, 256 workgroups, 1 and 2: 151 and 225).  float32, whose matrix
+// instructions take 16 times as long: 64 tokens (2 x 256 of 4 heads, 1, 2, 4 segments: 44, 41,
+// 28; 2 x 160 of 6 heads of 64, 1 and 2: 17 and 20), and one workgroup a CU, since LDS holds
+// no more, unless that makes fewer than three (1 x 2048 of 16 heads, 8 and 16: 74 and 82;
+// gradients, 1, 4, 5: 317, 212, 179).
 AttnLayout layout_of(const AttnArgs &a, int jobs) {
     AttnLayout l;
     const int64_t wide = jobs > 1 && a.K > a.V ? a.K : a.V;
@@ -813,10 +818,11 @@ AttnLayout layout_of(const AttnArgs &a, int jobs) {
     const int64_t narrow = jobs > 1 && a.V < a.K ? a.V : a.K;    // the fewest state rows
     l.v_cols = wide > 64 && narrow <= 128 && half > 192 && half <= 256 ? 128 : 64;
     const int64_t groups = rows * ((wide + l.v_cols - 1) / l.v_cols);
+    const int64_t most = a.T / (a.bf16 ? 256 : 64);
     int64_t seg = groups > 0 && groups <= 128 ? 512 / groups : 1;
-    const int64_t most = a.T / 256;
+    if (!a.bf16 && seg >= 6) seg /= 2;
     seg = seg < most ? seg : most;
-    seg = seg < 1 ? 1 : seg;
+    seg = seg < 3 ? 1 : seg;
     l.seg_tokens = ((a.T + seg - 1) / seg + kChunk - 1) / kChunk * kChunk;
     l.segments = l.seg_tokens ? (a.T + l.seg_tokens - 1) / l.seg_tokens : 1;
     return l;

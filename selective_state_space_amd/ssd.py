@@ -1089,36 +1089,50 @@ def _heads_in(t, name, dtype, shape, device):
     """(t, batch stride, token stride) of [Bt,T,heads,d] or [Bt,heads,d]: in place where a
     token's heads are consecutive and every row starts on 16 bytes, else a dense copy."""
     _like(t, name, dtype, shape, device)
-    mult = 16 // t.element_size()
-    heads, d = shape[-2:]
-    lead = [s if n > 1 else 0 for s, n in zip(t.stride()[:-2], shape[:-2])]
-    if (t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != d) or t.data_ptr() & 15
-            or any(s % mult for s in lead) or any(s > _MAX_ROW_STRIDE for s in lead[1:])):
+    if len(shape) == 4:
+        sb, st, sh, s1 = t.stride()
+        if shape[1] <= 1:
+            st = 0
+    else:
+        sb, sh, s1 = t.stride()
+        st = 0
+    if shape[0] <= 1:
+        sb = 0
+    if (s1 != 1 or (sh != shape[-1] and shape[-2] > 1) or t.data_ptr() & 15
+            or (sb | st) & (7 if dtype is torch.bfloat16 else 3) or st > _MAX_ROW_STRIDE):
         t = t.contiguous()
         if t.data_ptr() & 15:
             t = t.clone()
-        lead = t.stride()[:-2]
-    return t, lead[0], lead[1] if len(lead) > 1 else 0
+        row = shape[-2] * shape[-1]
+        sb, st = (shape[1] * row, row) if len(shape) == 4 else (row, 0)
+    return t, sb, st
 
 
 def _attn_args(q, k, v, log_decay, scale, names):
     """(dims, q, k, v, log_decay, dev) of [Bt,T,heads,d] or [Bt,heads,d] tensors."""
     dev = _on_gpu(q, names[0])
-    for t, n in ((k, names[1]), (v, names[2])):
+    n = q.dim()
+    for t, name in ((k, names[1]), (v, names[2])):
         if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a torch.Tensor" % n)
-        if t.dim() != q.dim():
-            raise ValueError("%s must have %d dimensions, as %s" % (n, q.dim(), names[0]))
-    io = _io_code(q.dtype)
-    lead, (H, K), (G, V) = tuple(q.shape[:-2]), q.shape[-2:], v.shape[-2:]
-    q, qb, qt = _heads_in(q, names[0], q.dtype, lead + (H, K), dev)
-    k, kb, kt = _heads_in(k, names[1], q.dtype, lead + (G, K), dev)
-    v, vb, vt = _heads_in(v, names[2], q.dtype, lead + (G, V), dev)
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if t.dim() != n:
+            raise ValueError("%s must have %d dimensions, as %s" % (name, n, names[0]))
+    dtype = q.dtype
+    io = _io_code(dtype)
+    if n == 4:
+        Bt, T, H, K = q.shape
+        _, _, G, V = v.shape
+        kshape, vshape = (Bt, T, G, K), (Bt, T, G, V)
+    else:
+        (Bt, H, K), T = q.shape, 1
+        _, G, V = v.shape
+        kshape, vshape = (Bt, G, K), (Bt, G, V)
+    q, qb, qt = _heads_in(q, names[0], dtype, q.shape, dev)
+    k, kb, kt = _heads_in(k, names[1], dtype, kshape, dev)
+    v, vb, vt = _heads_in(v, names[2], dtype, vshape, dev)
     log_decay = _in(log_decay, "log_decay", torch.float32, (H,), dev)
-    scale = K ** -0.5 if scale is None else float(scale)
-    dims = AttnDims(lead[0], lead[1] if len(lead) > 1 else 1, H, G, K, V, qb, qt, kb, kt, vb, vt,
-                    io, scale)
-    return dims, q, k, v, log_decay, dev
+    return (AttnDims(Bt, T, H, G, K, V, qb, qt, kb, kt, vb, vt, io,
+                     K ** -0.5 if scale is None else float(scale)), q, k, v, log_decay, dev)
 
 
 def linear_attn_layout(dims: AttnDims) -> AttnLayout:
@@ -1231,35 +1245,38 @@ def ssd_linear_attn_bwd(q, k, v, log_decay, dy, scale=None, init_state=None, dfi
 
 
 def _channels_in(t, name, dtype, shape, device):
-    """(t, batch stride, token stride) of [Bt,T,C]: in place where a token's channels are
-    consecutive, else a dense copy."""
+    """(t, batch stride, token stride) of [Bt,T,C] or [Bt,C]: in place where a token's channels
+    are consecutive, else a dense copy."""
     _like(t, name, dtype, shape, device)
-    if shape[2] > 1 and t.stride(2) != 1:
+    if shape[-1] > 1 and t.stride(-1) != 1:
         t = t.contiguous()
-    return t, t.stride(0) if shape[0] > 1 else 0, t.stride(1) if shape[1] > 1 else 0
+    if len(shape) == 2:
+        return t, t.stride(0) if shape[0] > 1 else 0, 0
+    sb, st, _ = t.stride()
+    return t, sb if shape[0] > 1 else 0, st if shape[1] > 1 else 0
 
 
 def _norm_args(x, groups, weight, bias, z, form, rms, eps, seq_lens):
     dev = _on_gpu(x, "x")
-    io = _io_code(x.dtype)
-    if form not in NORM_FORMS:
+    dtype, shape = x.dtype, x.shape
+    io = _io_code(dtype)
+    code = NORM_FORMS.get(form)
+    if code is None:
         raise ValueError("form must be one of %s" % sorted(NORM_FORMS))
-    if x.dim() not in (2, 3):
+    if len(shape) == 3:
+        Bt, T, C = shape
+    elif len(shape) == 2:
+        (Bt, C), T = shape, 1
+    else:
         raise ValueError("x must be [Bt,T,C] or [Bt,C]")
-    shape = tuple(x.shape)
-    if z is not None:
-        _like(z, "z", x.dtype, shape, dev)
-    if x.dim() == 2:
-        x, z = x[:, None], None if z is None else z[:, None]
-    Bt, T, C = x.shape
-    x, xb, xt = _channels_in(x, "x", x.dtype, (Bt, T, C), dev)
+    x, xb, xt = _channels_in(x, "x", dtype, shape, dev)
     zb = zt = 0
     if z is not None:
-        z, zb, zt = _channels_in(z, "z", x.dtype, (Bt, T, C), dev)
+        z, zb, zt = _channels_in(z, "z", dtype, shape, dev)
     weight = _opt(weight, "weight", torch.float32, (C,), dev)
     bias = _opt(bias, "bias", torch.float32, (C,), dev)
     seq_lens = _opt(seq_lens, "seq_lens", torch.int32, (Bt,), dev)
-    dims = NormDims(Bt, T, C, groups, xb, xt, zb, zt, io, NORM_FORMS[form], 1 if rms else 0, eps)
+    dims = NormDims(Bt, T, C, groups, xb, xt, zb, zt, io, code, 1 if rms else 0, eps)
     return dims, x, weight, bias, z, seq_lens, shape, dev
 
 
@@ -1275,7 +1292,7 @@ def ssd_group_norm_fwd(x, groups: int, weight=None, bias=None, z=None, form: str
     """
     dims, x, weight, bias, z, seq_lens, shape, dev = _norm_args(x, groups, weight, bias, z, form,
                                                                 rms, eps, seq_lens)
-    y = (torch.empty(*shape, dtype=x.dtype, device=dev) if y is None
+    y = (torch.empty(shape, dtype=x.dtype, device=dev) if y is None
          else _need_out(y, "y", x.dtype, shape, dev))
     _call("ssd_group_norm_fwd", dev, x.data_ptr(), _addr(z), _addr(weight), _addr(bias),
           _addr(seq_lens), y.data_ptr(), ctypes.byref(dims))
@@ -1300,8 +1317,8 @@ def ssd_group_norm_bwd(x, groups: int, dy, weight=None, bias=None, z=None, form:
         workspace = torch.empty(max(ssd_group_norm_bwd_workspace_size(dims), 16),
                                 dtype=torch.uint8, device=dev)
     C = dims.channels
-    out = dict(dx=torch.empty(*shape, dtype=x.dtype, device=dev),
-               dz=None if z is None else torch.empty(*shape, dtype=x.dtype, device=dev),
+    out = dict(dx=torch.empty(shape, dtype=x.dtype, device=dev),
+               dz=None if z is None else torch.empty(shape, dtype=x.dtype, device=dev),
                dweight=(None if weight is None
                         else torch.empty(C, dtype=torch.float32, device=dev)),
                dbias=None if bias is None else torch.empty(C, dtype=torch.float32, device=dev))
