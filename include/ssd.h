@@ -830,7 +830,7 @@ ssd_status ssd_group_norm_bwd(const void *x, const void *z, const float *weight,
  *   bias [outputs]        float32   in   NULL = none
  *   y    [rows, outputs]  io dtype  out  dense
  * Products are exact and sums float32; one rounding to the io dtype.  Up to 2^20 - 16
- * rows are computed; the weights are read once for every 64 of them (float32: 32).
+ * rows are computed; the weights are read once for every 16 or 32 of them.
  * inputs is a multiple of group; outputs >= 1.
  */
 typedef struct {

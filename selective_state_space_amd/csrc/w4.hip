@@ -110,8 +110,11 @@ __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint8_t *__res
 // A wavefront takes NT tiles of 16 outputs over its share of the inputs, 64 at a time;
 // the shares of a workgroup's wavefronts are added through LDS, in order.  Rows and codes
 // are loaded into the wavefront's own part of LDS, whole lines at a time and three steps
-// ahead (one step ahead, 64 rows waited for each: 22 us): read straight into operands, 16 rows 16 bytes at a
-// time, they came at 11 bytes a cycle and CU (64 rows, 5120 inputs, 2560 outputs: 26 us).
+// ahead (64 rows, 5120 inputs, 2560 outputs: 14 us; one step ahead, 22): read straight into
+// operands, 16 rows 16 bytes at a time, they came at 11 bytes a cycle and CU (26 us).  What
+// bounds it is the reading of x, once for every 16 or 32 outputs, out of the L2 caches (48
+// rows: 79 MB in some 8 us); the codes' 6.6 MB alone would take 1.5.
+//
 // 8 inputs of one row: as they lie in LDS, and as operands in the codes' order (0 4 1 5 2 6 3 7).
 template <typename T>
 struct Rows;
@@ -491,10 +494,9 @@ __global__ __launch_bounds__(256) void w4_rows_kernel(const W4Args a) {
     }
 }
 
-// Row tiles that share a wavefront's weights (float32's three terms leave room for two),
-// and one or two tiles of outputs: two halve the reading of x, but also the workgroups, so
-// they are taken where one each would not be on the chip at once (48 rows x 5120 x 2560,
-// 160 workgroups: 13.0 us with one, 17.4 with two; 64 x 1664 x 32768, 2048: 63 and 48).
+// One or two tiles of outputs: two halve the reading of x, but also the workgroups, so they
+// are taken where one each would not be on the chip at once (48 rows x 5120 x 2560, 160
+// workgroups: 13.0 us with one, 17.4 with two; 64 x 1664 x 32768, 2048: 63 and 48).
 template <typename T, int RT>
 void launch_tiles(const W4Args &a, hipStream_t st) {
     constexpr int kLds = 4 * 4 * (16 * RT * 64 * sizeof(T) + 1024);
@@ -515,6 +517,12 @@ void launch_rows(const W4Args &a, hipStream_t st) {
 // matrix instructions 9.5 and 9.6; with 4 rows 12.2 and 9.9).  A wavefront there takes four
 // outputs where that leaves two workgroups a CU, else two (6592 x 8192: 9.5 us, with four
 // 12.2).
+// More rows in tiles of 16, one or two a workgroup (bf16; rows x inputs x outputs, us with
+// one and two): two halve the reading of codes and fill what they read of x (20 x 1664 x
+// 32768: 22.6, 19.8; 64 x 2560 x 10576: 25.5, 21.0; 128 x 5120 x 5120: 31.6, 28.6), unless a
+// tile of few would stay empty (48 x 5120 x 2560: 10.5, 13.2; x 5120: 14.9, 17.9) or CUs idle
+// (32 x 8192 x 1024, 128 workgroups of one: 10.7, 13.0).  float32 always in single ones: three
+// terms of two tiles leave a CU one workgroup (32 x 1664 x 32768: 40.7, 48.0).
 template <typename T>
 void launch_linear(const W4Args &a, hipStream_t st) {
     if (a.rows <= 2) {
@@ -525,19 +533,20 @@ void launch_linear(const W4Args &a, hipStream_t st) {
             four ? launch_rows<T, 2, 4>(a, st) : launch_rows<T, 2, 2>(a, st);
         return;
     }
-    if (a.rows <= 16) launch_tiles<T, 1>(a, st);
-    else if (sizeof(T) == 4 || a.rows <= 32) launch_tiles<T, 2>(a, st);
+    const int64_t rows16 = (a.rows + 15) / 16, blocks = (a.outputs + 15) / 16 * rows16;
+    if (sizeof(T) == 4 || rows16 == 1 || rows16 == 3 || blocks <= 256)
+        launch_tiles<T, 1>(a, st);
     else if constexpr (sizeof(T) == 2)
-        a.rows <= 48 ? launch_tiles<T, 3>(a, st) : launch_tiles<T, 4>(a, st);
+        launch_tiles<T, 2>(a, st);
 }
 
 }  // namespace
 
 bool w4_fits(const W4Args &a) {
     const double n = (double)a.inputs * (double)a.outputs;
-    // (grid.y holds 65535 blocks of 64 rows)
+    // (grid.y holds 65535 blocks of 16 rows)
     return n / 1024 + 1 <= (double)kMaxBlocks &&
-           ((double)a.outputs / 16 + 1) * ((double)a.rows / 64 + 1) * 4 <= (double)kMaxBlocks &&
+           ((double)a.outputs / 16 + 1) * ((double)a.rows / 16 + 1) <= (double)kMaxBlocks &&
            a.rows <= int64_t(65535) * 16;
 }
 

@@ -39,9 +39,9 @@ def test_linear_attn_bwd(sizes, io):
 # wavefront for one and two rows
 @pytest.mark.parametrize("io", TYPES)
 @pytest.mark.parametrize("rows,outputs", [(1, 8191), (1, 8193), (2, 8191), (2, 8195),
-                                          (9, 8100), (9, 12400), (9, 8300), (25, 4000), (25, 8300),
-                                          (40, 4000), (40, 4200), (60, 4000), (60, 4200),
-                                          (100, 2000), (100, 2100)])
+                                          (9, 8100), (9, 12400), (9, 8300), (25, 2000), (25, 4000),
+                                          (25, 8300), (40, 4000), (40, 4200), (60, 900),
+                                          (60, 4000), (60, 4200), (100, 500), (100, 2100)])
 def test_w4_linear(rows, outputs, io):
     g = gen(rows + outputs)
     codes, scales = packed(g, outputs, 192, 64)
