@@ -706,25 +706,27 @@ __global__ __launch_bounds__(256) void attn_share_kernel(const Share a) {
 
 int pad_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-template <typename T, int KD, int NV>
+template <typename T, int KD>
 void launch_jobs_t(const Jobs &j, Mode mode, uint32_t blocks, hipStream_t st) {
     if (mode == kStateOnly)
-        attn_kernel<T, KD, NV, kStateOnly><<<blocks, 256, 0, st>>>(j);
+        attn_kernel<T, KD, 1, kStateOnly><<<blocks, 256, 0, st>>>(j);
     else if (mode == kOut || sizeof(T) == 4)
-        attn_kernel<T, KD, NV, kOut><<<blocks, 256, 0, st>>>(j);
+        attn_kernel<T, KD, 1, kOut><<<blocks, 256, 0, st>>>(j);
     else if constexpr (sizeof(T) == 2)
-        attn_kernel<T, KD, NV, kOutWide><<<blocks, 256, 0, st>>>(j);
+        attn_kernel<T, KD, 1, kOutWide><<<blocks, 256, 0, st>>>(j);
 }
+// (sequences are not cut where 128 columns are taken, nor are those taken by bf16's shared
+// heads: layout_of)
 template <typename T>
 void launch_jobs_kd(int kd, int cols, const Jobs &j, Mode mode, uint32_t blocks, hipStream_t st) {
-    if (kd == 64)
-        cols == 128 ? launch_jobs_t<T, 64, 2>(j, mode, blocks, st)
-                    : launch_jobs_t<T, 64, 1>(j, mode, blocks, st);
+    if (kd == 256)
+        launch_jobs_t<T, 256>(j, mode, blocks, st);
     else if (kd == 128)
-        cols == 128 ? launch_jobs_t<T, 128, 2>(j, mode, blocks, st)
-                    : launch_jobs_t<T, 128, 1>(j, mode, blocks, st);
+        cols == 128 ? attn_kernel<T, 128, 2, kOut><<<blocks, 256, 0, st>>>(j)
+                    : launch_jobs_t<T, 128>(j, mode, blocks, st);
     else
-        launch_jobs_t<T, 256, 1>(j, mode, blocks, st);
+        cols == 128 ? attn_kernel<T, 64, 2, kOut><<<blocks, 256, 0, st>>>(j)
+                    : launch_jobs_t<T, 64>(j, mode, blocks, st);
 }
 
 // Launches all jobs, those of one padded row count together; all of them where they do not
@@ -799,9 +801,10 @@ Job fwd_job(const AttnArgs &a) {
 size_t state_floats(const AttnArgs &a) { return (size_t)(a.Bt * a.H) * a.K * a.V; }
 
 // 64 columns a workgroup (states of more than 128 rows have registers for no more), unless
-// 128 leave between 6 and 8 workgroups for 8 CUs (5
-// sequences of 40 heads of 128, 4096 tokens: 228 us, with 64 columns 272; 8 sequences 422
-// and 390; 4 of 32 heads 218 and 151).
+// 128 leave more than half the CUs one and none two (2048 tokens of heads of 128, us with 64
+// and 128: 160 sequences and heads 130, 108; 192: 132, 110; 224: 139, 116; of 4096 tokens
+// 128: 151, 218; 320: 390, 422; float32, 160: 637, 476).  Not in bf16 gradients (192
+// workgroups of the three recurrences: 104, 111; 216: 102, 102; float32 636, 459).
 // Segments, three or more, where at most half the CUs would have a workgroup, though keys
 // and values are read and the states formed twice.  bf16: up to two workgroups a CU, of 256
 // tokens or more (1 x 65536 tokens of 16 heads: 1, 4, 8, 16, 32 segments 1867, 743, 445,
@@ -816,7 +819,8 @@ AttnLayout layout_of(const AttnArgs &a, int jobs) {
     const int64_t wide = jobs > 1 && a.K > a.V ? a.K : a.V;
     const int64_t rows = a.Bt * a.H * jobs, half = rows * ((wide + 127) / 128);
     const int64_t narrow = jobs > 1 && a.V < a.K ? a.V : a.K;    // the fewest state rows
-    l.v_cols = wide > 64 && narrow <= 128 && half > 192 && half <= 256 ? 128 : 64;
+    l.v_cols = wide > 64 && narrow <= 128 && half > 128 && half <= 256 && !(a.bf16 && jobs > 1)
+                   ? 128 : 64;
     const int64_t groups = rows * ((wide + l.v_cols - 1) / l.v_cols);
     const int64_t most = a.T / (a.bf16 ? 256 : 64);
     int64_t seg = groups > 0 && groups <= 128 ? 512 / groups : 1;
