@@ -13,6 +13,19 @@
 // (dS_t is the adjoint that reaches token t's update, e^r dS_t what it passes on:
 // the state is used before its decay, hence late = 1).  So neither states nor
 // adjoints go through memory except at the ends of segments.
+//
+// Per 16 columns of a bf16 state of 128 rows a chunk of 32 tokens takes 34 matrix
+// instructions of 16 x 16 x 32 and each wavefront 16 more for the pairs; bytes bound it
+// below (8 x 4096 tokens of 40 heads of 128: 1.34 GB, 280 us at a copy's rate).  Reached:
+// 381 us there (3.5 TB/s; matrix instructions 31% of the cycles, vector ones 34%), 128
+// sequences and heads of 4096 tokens 151 (3.6 TB/s), 1 x 65536 tokens of 16 heads, in two
+// passes, 404; gradients of 4 x 2048 tokens of 16 heads 108 (235 MB, 49 at a copy's rate).
+// What bounds it is that a wavefront's chunk is a chain (operands out of LDS, products,
+// rounding, products) which two wavefronts a SIMD do not cover, and whole workgroups over
+// CUs (640 of them on 512 places).  Tried and slower than 390 us: chunks of 64 tokens
+// through registers (636), eight wavefronts of 16 columns (405), pairs shared through LDS
+// behind a second barrier (437), interleaving by hand (425 of 422 then), three workgroups a
+// CU (1140, spills).
 
 #include "block_launch.h"
 #include "layer_launch.h"
@@ -318,8 +331,8 @@ struct Const {
 //
 // A chunk's tiles are loaded into LDS kAhead chunks before the walk comes to it, so
 // that a load has kAhead chunks' time; one barrier a chunk lets the buffers turn.  Each
-// wavefront forms the chunk's pairs for itself (they are a fifth of its matrix
-// instructions): shared through LDS they needed a second barrier, and a wait for it.
+// wavefront forms the chunk's pairs for itself (16 of its 50 matrix instructions with 16
+// columns, of 84 with 32): shared through LDS they need a second barrier, and a wait for it.
 // Whole chunks run through one block of code whose only branch is the one for tokens that
 // are not finite, in which matrix and vector instructions interleave.
 enum Mode { kStateOnly, kOut, kOutWide };
