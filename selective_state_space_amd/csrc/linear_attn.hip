@@ -706,15 +706,16 @@ struct Share {
 };
 template <typename T>
 __global__ __launch_bounds__(256) void attn_share_kernel(const Share a) {
-    const int w = blockIdx.y;
-    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (x >= a.n4[w]) return;
-    const int dim4 = a.dim4[w];
-    const int64_t row = x / dim4;            // (token, group)
-    const f32x4 *p = reinterpret_cast<const f32x4 *>(a.part[w]) + row * a.rep * dim4 + x % dim4;
-    f32x4 v = p[0];
-    for (int i = 1; i < a.rep; ++i) v += p[(int64_t)i * dim4];
-    put4(static_cast<T *>(a.out[w]) + 4 * x, v);
+    const int w = blockIdx.y, dim4 = a.dim4[w];
+    for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < a.n4[w];
+         x += (int64_t)gridDim.x * 256) {
+        const int64_t row = x / dim4;            // (token, group)
+        const f32x4 *p =
+            reinterpret_cast<const f32x4 *>(a.part[w]) + row * a.rep * dim4 + x % dim4;
+        f32x4 v = p[0];
+        for (int i = 1; i < a.rep; ++i) v += p[(int64_t)i * dim4];
+        put4(static_cast<T *>(a.out[w]) + 4 * x, v);
+    }
 }
 
 int pad_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
@@ -868,12 +869,10 @@ AttnLayout attn_layout(const AttnArgs &a) { return layout_of(a, 1); }
 AttnLayout attn_bwd_layout(const AttnArgs &a) { return layout_of(a, 3); }
 
 bool attn_fits(const AttnArgs &a) {
-    const double heads = (double)a.Bt * (double)a.H, wide = a.K > a.V ? a.K : a.V;
-    // the most workgroups of the recurrences (3 jobs, 4 slices), and of the shared heads'
-    // sums (segments, and the chains between them, are taken for at most 128 workgroups);
-    // and sizes that 64 bits hold
-    return heads * 12 <= (double)kMaxBlocks && heads * (double)a.T <= 0x1p40 &&
-           (a.G == a.H || (double)a.Bt * a.T * a.G * (wide / 1024) + 1 <= (double)kMaxBlocks);
+    const double heads = (double)a.Bt * (double)a.H;
+    // the most workgroups of the recurrences (3 jobs, 4 slices; segments, and the chains
+    // between them, are taken for at most 128 workgroups), and sizes that 64 bits hold
+    return heads * 12 <= (double)kMaxBlocks && heads * (double)a.T <= 0x1p40;
 }
 
 size_t attn_workspace(const AttnArgs &a) {
@@ -977,7 +976,8 @@ hipError_t launch_attn_bwd(const AttnArgs &a, hipStream_t st) {
     x.rep = (int32_t)(a.H / a.G);
     for (int i = 0; i < 2; ++i) x.n4[i] = rows * x.dim4[i];
     const int64_t n4 = x.n4[0] > x.n4[1] ? x.n4[0] : x.n4[1];
-    const dim3 grid((uint32_t)((n4 + 255) / 256), 2);
+    const int64_t most = int64_t(1) << 20, blocks = (n4 + 255) / 256;
+    const dim3 grid((uint32_t)(blocks < most ? blocks : most), 2);
     if (a.bf16)
         attn_share_kernel<uint16_t><<<grid, 256, 0, st>>>(x);
     else

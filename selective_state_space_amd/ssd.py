@@ -1114,10 +1114,12 @@ def _heads_in(t, name, dtype, shape, device):
     return t, sb, st
 
 
-def _attn_args(q, k, v, log_decay, scale, names):
+def _attn_args(q, k, v, log_decay, scale, names, ndim=4):
     """(dims, q, k, v, log_decay, dev) of [Bt,T,heads,d] or [Bt,heads,d] tensors."""
     dev = _on_gpu(q, names[0])
     n = q.dim()
+    if n != ndim:
+        raise ValueError("%s must be [Bt,%sH,K]" % (names[0], "T," if ndim == 4 else ""))
     for t, name in ((k, names[1]), (v, names[2])):
         if not isinstance(t, torch.Tensor):
             raise TypeError("%s must be a torch.Tensor" % name)
@@ -1166,8 +1168,6 @@ def ssd_linear_attn_fwd(q, k, v, log_decay, scale=None, init_state=None, y=None,
     init_state [Bt,H,K,V] f32 or None; ``final_state`` may be the same tensor.  ``seq_lens``
     [Bt] int32: y past a sequence's length is zero and its final state is that at its length.
     """
-    if q.dim() != 4:
-        raise ValueError("q must be [Bt,T,H,K]")
     dims, q, k, v, log_decay, dev = _attn_args(q, k, v, log_decay, scale, ("q", "k", "v"))
     Bt, T, H, K, V = dims.batch, dims.seqlen, dims.nheads, dims.dim_k, dims.dim_v
     init_state = _opt(init_state, "init_state", torch.float32, (Bt, H, K, V), dev)
@@ -1197,12 +1197,10 @@ def ssd_linear_attn_step(state, q_t, k_t, v_t, log_decay, scale=None, slots=None
     state b): a slot outside the pool marks a padded row (y zero, no state touched); a slot
     may be named once.  q_t [Bt,H,K], k_t [Bt,G,K], v_t [Bt,G,V] may be slices of wider rows.
     """
-    if q_t.dim() != 3:
-        raise ValueError("q_t must be [Bt,H,K]")
     dims, q_t, k_t, v_t, log_decay, dev = _attn_args(q_t, k_t, v_t, log_decay, scale,
-                                                     ("q_t", "k_t", "v_t"))
+                                                     ("q_t", "k_t", "v_t"), 3)
     Bt, H, K, V = dims.batch, dims.nheads, dims.dim_k, dims.dim_v
-    if state.dim() != 4:
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be [num_slots,H,K,V]")
     state = _need_out(state, "state", torch.float32, (state.shape[0], H, K, V), dev)
     slots = _opt(slots, "slots", torch.int32, (Bt,), dev)
@@ -1223,8 +1221,6 @@ def ssd_linear_attn_bwd(q, k, v, log_decay, dy, scale=None, init_state=None, dfi
     """Gradients of ssd_linear_attn_fwd: a dict of dq [Bt,T,H,K], dk [Bt,T,G,K], dv [Bt,T,G,V]
     in q's dtype and dinit [Bt,H,K,V] f32 (None unless ``want_dinit``).  dy [Bt,T,H,V] in q's
     dtype, dfinal [Bt,H,K,V] f32 or None.  The decays are constants."""
-    if q.dim() != 4:
-        raise ValueError("q must be [Bt,T,H,K]")
     dims, q, k, v, log_decay, dev = _attn_args(q, k, v, log_decay, scale, ("q", "k", "v"))
     Bt, T, H, G, K, V = (dims.batch, dims.seqlen, dims.nheads, dims.ngroups, dims.dim_k,
                          dims.dim_v)

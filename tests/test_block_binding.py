@@ -78,6 +78,33 @@ def test_token_strides_past_the_limit():
     assert w4_linear(w4_dims(xs=top + 8)) == -2 and "x_row_stride" in detail()
 
 
+def test_binding_refuses_what_is_no_tensor(on_host):
+    q, r = torch.zeros(1, 2, 1, 8), torch.zeros(1)
+    for f in (lambda: ssd.ssd_linear_attn_fwd(q, None, q, r),
+              lambda: ssd.ssd_linear_attn_bwd(q, q, [1.0], r, q),
+              lambda: ssd.ssd_group_norm_fwd(q[0], 1, z=3.0, form="gate"),
+              lambda: ssd.ssd_linear_attn_fwd(q, q, q, 0.5)):
+        with pytest.raises((TypeError, ValueError)):
+            f()
+    for f in (lambda: ssd.ssd_linear_attn_step(None, q[0], q[0], q[0], r),
+              lambda: ssd.ssd_linear_attn_step(torch.zeros(1, 1, 8, 8), q, q, q, r),
+              lambda: ssd.ssd_linear_attn_fwd(q[0], q[0], q[0], r),
+              lambda: ssd.ssd_linear_attn_fwd(q[None], q[None], q[None], r)):
+        with pytest.raises(ValueError):
+            f()
+    assert not on_host
+
+
+def test_binding_refuses_a_first_argument_that_is_no_tensor():
+    q, r = torch.zeros(1, 2, 1, 8), torch.zeros(1)
+    for f in (lambda: ssd.ssd_linear_attn_fwd(None, q, q, r),
+              lambda: ssd.ssd_linear_attn_bwd([1.0], q, q, r, q),
+              lambda: ssd.ssd_group_norm_fwd(None, 1), lambda: ssd.ssd_w4_quantize(1.0, 64),
+              lambda: ssd.ssd_w4_linear(None, q, q)):
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            f()
+
+
 def test_binding_copies_rows_that_lie_far_apart(on_host):
     far = torch.empty(1).expand(1)     # (a shape alone: nothing of it is read)
     far = torch.as_strided(torch.empty((1 << 24) + 8 + 16, dtype=torch.bfloat16), (1, 2, 1, 16),
@@ -102,7 +129,7 @@ def test_sizes_that_one_launch_holds():
     anything is launched (a NULL tensor is found after the sizes)."""
     none = dict(q=None)
     for kw, code in ((dict(Bt=8192, H=32, G=32, T=4096), -1), (dict(Bt=1 << 21, H=8, G=8), -2),
-                     (dict(Bt=1 << 15, T=1 << 20), -2)):
+                     (dict(Bt=1 << 15, T=1 << 20), -1), (dict(Bt=1 << 15, T=1 << 25), -2)):
         assert attn_fwd(attn_dims(**kw), **none) == code, (kw, detail())
     for kw, code in ((dict(Bt=8, T=65536, C=5120, groups=40), -1),
                      (dict(Bt=8, T=1 << 20, C=2048, groups=1), -1),
