@@ -65,11 +65,12 @@ template <int TPR, int NS>
 __device__ __forceinline__ void row_sums(float *v, float *lds, int &turn) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-        v[i] = group_sum<16>(v[i]);
-        if constexpr (TPR >= 64) {
-            v[i] += __shfl_xor(v[i], 16, 64);
-            v[i] += __shfl_xor(v[i], 32, 64);
-        }
+        v[i] += dpp_mov<0xB1>(v[i]);                              // quad_perm [1,0,3,2]
+        v[i] += dpp_mov<0x4E>(v[i]);                              // quad_perm [2,3,0,1]
+        if constexpr (TPR >= 8) v[i] += dpp_mov<0x141>(v[i]);     // row_half_mirror
+        if constexpr (TPR >= 16) v[i] += dpp_mov<0x140>(v[i]);    // row_mirror
+        if constexpr (TPR >= 32) v[i] += __shfl_xor(v[i], 16, 64);
+        if constexpr (TPR >= 64) v[i] += __shfl_xor(v[i], 32, 64);
     }
     if constexpr (TPR > 64) {
         constexpr int W = TPR / 64;
@@ -355,9 +356,13 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float *__restrict_
 }
 
 // How rows lie on lanes: accesses of 16 bytes where groups, strides and starts allow
-// them, else of single channels; a wavefront or less holds a row in one access a lane, a
-// workgroup in up to 4 (4 x 2048 tokens of 2048 channels, gradients, 4 accesses on a
-// wavefront: 149 us, 1 on a workgroup: 54).
+// them, else of single channels; on as few lanes as hold a row in one access each (8 x 4096
+// tokens of 5120 channels, bf16, gated, groups of 16, 32, 64, 256 on 16, 16, 16, 64 lanes:
+// 840, 430, 236, 247 us; on 4, 4, 8, 32: 236, 195, 195, 196), a wavefront in up to two (groups
+// of 1024: 262 us on a workgroup, 205), a workgroup in up to 4 (4 x 2048 tokens of 2048
+// channels, gradients, 4 accesses on a wavefront: 149 us, 1 on a workgroup: 54); what is
+// longer on 1024 lanes (8 x 4096 x 5120, one group, float32 gradients: 713 us with 2
+// accesses, 1905 with registers for 4).
 struct NormShape {
     int vec, vpt, tpr;
 };
@@ -370,7 +375,8 @@ NormShape shape_of(const NormArgs &a) {
     NormShape s;
     s.vec = wide ? v : 1;
     const int64_t n = S / s.vec;
-    s.tpr = n <= 16 ? 16 : n <= 64 ? 64 : n <= 1024 ? 256 : 1024;
+    s.tpr = n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : n <= 128 ? 64
+            : n <= 1024 ? 256 : 1024;
     const int64_t vpt = (n + s.tpr - 1) / s.tpr;
     s.vpt = vpt <= 4 ? (int)vpt : 16;
     return s;
@@ -423,10 +429,17 @@ void launch_form(const NormWork &w, hipStream_t st) {
 }
 template <typename T, int VEC, bool BWD>
 void launch_shape(const NormWork &w, const NormShape &s, hipStream_t st) {
-    if (s.tpr == 16)
+    if (s.tpr == 4)
+        launch_form<T, VEC, 1, 4, BWD>(w, st);
+    else if (s.tpr == 8)
+        launch_form<T, VEC, 1, 8, BWD>(w, st);
+    else if (s.tpr == 16)
         launch_form<T, VEC, 1, 16, BWD>(w, st);
+    else if (s.tpr == 32)
+        launch_form<T, VEC, 1, 32, BWD>(w, st);
     else if (s.tpr == 64)
-        launch_form<T, VEC, 1, 64, BWD>(w, st);
+        s.vpt == 1 ? launch_form<T, VEC, 1, 64, BWD>(w, st)
+                   : launch_form<T, VEC, 2, 64, BWD>(w, st);
     else if (s.tpr == 256) {
         switch (s.vpt) {
             case 1: launch_form<T, VEC, 1, 256, BWD>(w, st); break;
@@ -434,10 +447,14 @@ void launch_shape(const NormWork &w, const NormShape &s, hipStream_t st) {
             case 3: launch_form<T, VEC, 3, 256, BWD>(w, st); break;
             default: launch_form<T, VEC, 4, 256, BWD>(w, st); break;
         }
-    } else if (s.vpt <= 4)
-        launch_form<T, VEC, 4, 1024, BWD>(w, st);
-    else if constexpr (VEC == 1)
-        launch_form<T, 1, 16, 1024, BWD>(w, st);
+    } else if (s.vpt <= 2)
+        launch_form<T, VEC, 2, 1024, BWD>(w, st);
+    else if constexpr (VEC < 8) {   // (8 x 2 x 1024 channels are the most)
+        if (s.vpt <= 4)
+            launch_form<T, VEC, 4, 1024, BWD>(w, st);
+        else if constexpr (VEC == 1)
+            launch_form<T, 1, 16, 1024, BWD>(w, st);
+    }
 }
 template <bool BWD>
 void launch_type(const NormWork &w, const NormShape &s, hipStream_t st) {

@@ -7,6 +7,7 @@ from selective_state_space_amd import ssd
 
 from _block import TYPES, attn_inputs, gen, randn
 from block_forms import ATTN_BWD, ATTN_FWD
+from test_gpu_group_norm import FORMS, check as check_norm, inputs as norm_inputs
 from test_gpu_linear_attn import check_bwd, check_fwd
 from test_gpu_w4 import check, packed
 
@@ -46,6 +47,61 @@ def test_w4_linear(rows, outputs, io):
     g = gen(rows + outputs)
     codes, scales = packed(g, outputs, 192, 64)
     check(randn(g, rows, 192, dtype=TYPES[io]), codes, scales, randn(g, outputs))
+
+
+# groups on 4, 8, 16, 32 and 64 lanes, 2 accesses on 64, workgroups of 256 and 1024 lanes; of
+# channels in 16-byte accesses of either type, and of single ones
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("groups,size", [
+    (9, 7), (11, 8), (7, 13), (9, 16), (5, 27), (7, 32), (3, 50), (5, 64), (3, 101),
+    (3, 128), (3, 200), (3, 256), (2, 301), (2, 512), (2, 1024), (2, 1200), (1, 1501), (1, 2501),
+    (1, 2600), (1, 6000), (1, 12000)])
+def test_group_norm(groups, size, io):
+    for form in FORMS:
+        x, kw, dy = norm_inputs(size, 3, 41, groups * size, TYPES[io], form)
+        lens = torch.tensor([41, 0, 17], dtype=torch.int32, device="cuda")
+        check_norm(x, groups, kw, dy, lens)
+
+
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("groups,size", [(37, 2), (21, 4)])
+def test_group_norm_of_a_few_channels(groups, size, io):
+    """Two or four channels may lie as near to each other as they like, and then u - mean, and
+    the terms of dx, cancel: a bar relative to the result holds for no arithmetic of 32 bits.
+    Errors are held to the terms instead.  With m the mean, x - m is off by some half steps of
+    |x| + |m|, so the normalised c by those of C = (|x| + |m|) rstd, and y = c w + b by those
+    of C |w| + |b|; rstd by a few relative half steps, since sum(x - m) = 0 takes the mean's
+    error out of the variance to first order.  dx = rstd (d - mean d - c mean(d c)) has the
+    terms |d|, mean |d|, C mean |d c| and |c| mean(|d| C), and the weights' gradients |dy| C and
+    |dy| summed.  Each passes through S + 32 roundings of independent signs, the sums over
+    tokens through as many more."""
+    io = TYPES[io]
+    x, kw, dy = norm_inputs(size, 3, 41, groups * size, io, "plain")
+    w, b = kw["weight"].double(), kw["bias"].double()
+    split = lambda t: t.unflatten(-1, (groups, size))
+    X = split(x.double())
+    m = X.mean(-1, keepdim=True)
+    rstd = ((X - m).square().mean(-1, keepdim=True) + 1e-5).rsqrt()
+    c, C, d = (X - m) * rstd, (X.abs() + m.abs()) * rstd, split(dy.double() * w)
+    mean = lambda t: t.mean(-1, keepdim=True)
+    tokens = lambda t: t.flatten(2).sum((0, 1))
+    D = split(dy.double())
+    y = ssd.ssd_group_norm_fwd(x, groups, **kw)
+    got = dict(ssd.ssd_group_norm_bwd(x, groups, dy, **kw), y=y)
+    n, f = x.shape[0] * x.shape[1], torch.float32
+    for name, ref, terms, count, out in (
+            ("y", c.flatten(2) * w + b, C.flatten(2) * w.abs() + b.abs(), size, io),
+            ("dx", (rstd * (d - mean(d) - c * mean(d * c))).flatten(2),
+             (rstd * (d.abs() + mean(d.abs()) + C * mean((d * c).abs())
+                      + c.abs() * mean(d.abs() * C))).flatten(2), size, io),
+            ("dweight", tokens(D * c), tokens(D.abs() * C), size + n, f),
+            ("dbias", tokens(D), tokens(D.abs()), size + n, f)):
+        bar = 2.0 ** -24 * (count + 32) ** 0.5 * float(terms.norm())
+        if out == torch.bfloat16:
+            bar += 2.0 ** -8 * float(ref.norm())
+        off = float((got[name].double() - ref).norm())
+        print("  %-8s off %.3g of %.3g" % (name, off, bar), flush=True)
+        assert off <= bar, name
 
 
 @pytest.mark.parametrize("io", TYPES)
