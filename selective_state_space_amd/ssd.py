@@ -1294,7 +1294,7 @@ def ssd_group_norm_fwd(x, groups: int, weight=None, bias=None, z=None, form: str
     """
     dims, x, weight, bias, z, seq_lens, shape, dev = _norm_args(x, groups, weight, bias, z, form,
                                                                 rms, eps, seq_lens)
-    y = (torch.empty(shape, dtype=x.dtype, device=dev) if y is None
+    y = (torch.empty(*shape, dtype=x.dtype, device=dev) if y is None
          else _need_out(y, "y", x.dtype, shape, dev))
     _call("ssd_group_norm_fwd", dev, x.data_ptr(), _addr(z), _addr(weight), _addr(bias),
           _addr(seq_lens), y.data_ptr(), ctypes.byref(dims))
@@ -1319,8 +1319,8 @@ def ssd_group_norm_bwd(x, groups: int, dy, weight=None, bias=None, z=None, form:
         workspace = torch.empty(max(ssd_group_norm_bwd_workspace_size(dims), 16),
                                 dtype=torch.uint8, device=dev)
     C = dims.channels
-    out = dict(dx=torch.empty(shape, dtype=x.dtype, device=dev),
-               dz=None if z is None else torch.empty(shape, dtype=x.dtype, device=dev),
+    out = dict(dx=torch.empty(*shape, dtype=x.dtype, device=dev),
+               dz=None if z is None else torch.empty(*shape, dtype=x.dtype, device=dev),
                dweight=(None if weight is None
                         else torch.empty(C, dtype=torch.float32, device=dev)),
                dbias=None if bias is None else torch.empty(C, dtype=torch.float32, device=dev))
