@@ -829,7 +829,9 @@ ssd_status ssd_group_norm_bwd(const void *x, const void *z, const float *weight,
  *        multiple of 16 bytes, at most 2^24 elements)
  *   bias [outputs]        float32   in   NULL = none
  *   y    [rows, outputs]  io dtype  out  dense
- * Products are exact and sums float32; one rounding to the io dtype.  Up to 2^20 - 16
+ * Products are exact and sums float32; one rounding to the io dtype.  (24 sum|x| over a
+ * group must be finite; an x that is not makes its own row's outputs infinite or NaN, and no
+ * other's.)  Up to 2^20 - 16
  * rows are computed; the weights are read once for every 16 or 32 of them.
  * inputs is a multiple of group; outputs >= 1.
  */

@@ -137,3 +137,23 @@ def test_sizes_that_one_launch_holds():
         assert norm_fwd(norm_dims(**kw), x=None, z=None) == code, (kw, detail())
     for kw, code in ((dict(rows=65535 * 16), -1), (dict(rows=65535 * 16 + 1), -2)):
         assert w4_linear(w4_dims(**kw), x=None) == code, (kw, detail())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [1, 2, 5, 20, 40])
+def test_a_row_that_is_not_finite_is_alone(rows):
+    """An infinity or a NaN in a row of x leaves the other rows' products as they are."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    codes, scales = ssd.ssd_w4_quantize(torch.randn(100, 256, generator=g, device="cuda"), 64)
+    for io in (torch.float32, torch.bfloat16):
+        x = torch.randn(rows, 256, generator=g, device="cuda").to(io)
+        want = ssd.ssd_w4_linear(x, codes, scales)
+        for bad in (float("inf"), float("nan")):
+            y = x.clone()
+            y[rows // 2, 70] = bad
+            got = ssd.ssd_w4_linear(y, codes, scales)
+            keep = [r for r in range(rows) if r != rows // 2]
+            assert torch.equal(got[keep], want[keep])
+            code = torch.stack([codes & 15, codes >> 4], -1).flatten(1)[:, 70]
+            assert not torch.isfinite(got[rows // 2][code != 8]).any()
