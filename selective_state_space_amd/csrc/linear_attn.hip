@@ -14,7 +14,7 @@
 // the state is used before its decay, hence late = 1).  So neither states nor
 // adjoints go through memory except at the ends of segments.
 //
-// Per 16 columns of a bf16 state of 128 rows a chunk of 32 tokens takes 34 matrix
+// Per 16 columns of a bf16 state of 128 rows a chunk of 32 tokens takes 44 matrix
 // instructions of 16 x 16 x 32 and each wavefront 16 more for the pairs; bytes bound it
 // below (8 x 4096 tokens of 40 heads of 128: 1.34 GB, 280 us at a copy's rate).  Reached:
 // 381 us there (3.5 TB/s; matrix instructions 31% of the cycles, vector ones 34%), 128
@@ -252,17 +252,40 @@ __device__ __forceinline__ f32x4 mma_weighted(f32x4 a, f32x4 b, f32x4 c) {
     return Mat<float>::mma(a, b, c);
 }
 
-// Accumulators as an operand: rounded to bf16 for bf16 calls (2^-8 of each term, as y
-// itself is rounded).
+// Accumulators as an operand (the state against q, the pairs' weights against the values):
+// for bf16 two terms, hi cut and lo rounded, which leave at most 2^-15 of each element, so that an
+// output is rounded to bf16 once, where it is stored.  (One term, 2^-9 of each element twice
+// over, was 0.0023 of the outputs' norm off where that one rounding is 0.0017, at, us with one
+// term and with two: 8 x 4096 tokens of 40 heads of 128 396 and 436, 1 x 65536 of 16 406 and
+// 438, gradients of 4 x 2048 of 16 100 and 121.)
+struct Halves {
+    bf16x8 hi, lo;
+};
 template <int NT>
-__device__ __forceinline__ bf16x8 tile_frag(const f32x4 (&s)[NT], int k, uint16_t) {
-    const f32x4 a = s[2 * k], b = s[2 * k + 1];
-    return as_bf16x8(make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
-                                pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3])));
+__device__ __forceinline__ Halves tile_frag(const f32x4 (&s)[NT], int k, uint16_t) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f32x4 t = s[2 * k + (i >> 1)];
+        const float a = t[2 * i & 3], b = t[(2 * i & 3) + 1];
+        hi[i] = pair_hi(__float_as_uint(a), __float_as_uint(b));
+        lo[i] = pack_bf16x2(a - bf16_hi(__float_as_uint(a)), b - bf16_hi(__float_as_uint(b)));
+    }
+    return {as_bf16x8(make_uint4(hi[0], hi[1], hi[2], hi[3])),
+            as_bf16x8(make_uint4(lo[0], lo[1], lo[2], lo[3]))};
 }
 template <int NT>
 __device__ __forceinline__ f32x4 tile_frag(const f32x4 (&s)[NT], int k, float) {
     return s[k];
+}
+__device__ __forceinline__ f32x4 mma_halves(const Halves &a, bf16x8 b, f32x4 c) {
+    return mfma16x16x32(a.hi, b, mfma16x16x32(a.lo, b, c));
+}
+__device__ __forceinline__ f32x4 mma_halves(bf16x8 a, const Halves &b, f32x4 c) {
+    return mfma16x16x32(a, b.hi, mfma16x16x32(a, b.lo, c));
+}
+__device__ __forceinline__ f32x4 mma_halves(f32x4 a, f32x4 b, f32x4 c) {
+    return Mat<float>::mma(a, b, c);
 }
 
 __device__ __forceinline__ f32x4 f4(const float *v) { return f32x4{v[0], v[1], v[2], v[3]}; }
@@ -331,8 +354,8 @@ struct Const {
 //
 // A chunk's tiles are loaded into LDS kAhead chunks before the walk comes to it, so
 // that a load has kAhead chunks' time; one barrier a chunk lets the buffers turn.  Each
-// wavefront forms the chunk's pairs for itself (16 of its 50 matrix instructions with 16
-// columns, of 84 with 32): shared through LDS they need a second barrier, and a wait for it.
+// wavefront forms the chunk's pairs for itself (16 of its 60 matrix instructions with 16
+// columns, of 104 with 32): shared through LDS they need a second barrier, and a wait for it.
 // Whole chunks run through one block of code whose only branch is the one for tokens that
 // are not finite, in which matrix and vector instructions interleave.
 enum Mode { kStateOnly, kOut, kOutWide };
@@ -508,14 +531,22 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(const Jobs a) {
             for (int it = 0; it < LT; ++it)
 #pragma unroll
                 for (int jt = 0; jt < LT; ++jt) p[it][jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                Frag qf[LT], kf[LT];
+            // (a step's operands are read one step ahead: left alone, the reads sink to where
+            // they are used, 126 us for 121 in gradients of 4 x 2048 tokens of 16 heads of 128)
+            Frag qs[2][LT], ks[2][LT];
+            auto read = [&](int k) {
 #pragma unroll
                 for (int it = 0; it < LT; ++it) {
-                    qf[it] = natural<T, KD>(qc, 16 * it + m, M::kDepth * k, lane);
-                    kf[it] = natural<T, KD>(kc, tile_row<T>(it, m), M::kDepth * k, lane);
+                    qs[k & 1][it] = natural<T, KD>(qc, 16 * it + m, M::kDepth * k, lane);
+                    ks[k & 1][it] = natural<T, KD>(kc, tile_row<T>(it, m), M::kDepth * k, lane);
                 }
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            read(0);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                if (k + 1 < KS) read(k + 1);
+                const Frag(&qf)[LT] = qs[k & 1], (&kf)[LT] = ks[k & 1];
 #pragma unroll
                 for (int it = 0; it < LT; ++it)
 #pragma unroll
@@ -524,9 +555,9 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(const Jobs a) {
                             p[it][jt] = M::mma(kf[jt], qf[it], p[it][jt]);
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    const Frag sf = tile_frag(s[v], k, T(0));
+                    const auto sf = tile_frag(s[v], k, T(0));
 #pragma unroll
-                    for (int it = 0; it < LT; ++it) o[v][it] = M::mma(sf, qf[it], o[v][it]);
+                    for (int it = 0; it < LT; ++it) o[v][it] = mma_halves(sf, qf[it], o[v][it]);
                 }
             }
 #pragma unroll
@@ -541,9 +572,9 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(const Jobs a) {
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
                     if (M::kDepth * nb > 16 * it) continue;
-                    const Frag pf = tile_frag(p[it], nb, T(0));
+                    const auto pf = tile_frag(p[it], nb, T(0));
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) y[v][it] = M::mma(vf[v][nb], pf, y[v][it]);
+                    for (int v = 0; v < NV; ++v) y[v][it] = mma_halves(vf[v][nb], pf, y[v][it]);
                 }
             }
             // A token's masked pairs are weights of 0, which an infinity or a NaN in a later
