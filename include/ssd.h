@@ -677,7 +677,9 @@ ssd_status ssd_cache_read(const void *codes, const float *scales, int64_t n, int
  * init_state (or zeros) and the token tensors may be NULL.  States, their
  * updates and all sums are float32; for bf16 the weights of a chunk's pairs of
  * tokens and the state as q's operand are taken to 2^-15 of each, and y is rounded
- * to bf16 once.
+ * to bf16 once.  A state is rounded once for every 32 tokens of a prompt and once a
+ * step; what a decay's float lacks of e^{r n} is made good, so that errors of long
+ * memories do not add up (a step that takes less than 2^-25 off a number leaves it).
  * No atomics: reruns are bitwise identical.  An infinity or a NaN in a token's q, k or v
  * reaches no output of an earlier token, of another sequence or of a head that does not
  * read it (the gradients: of a later token, likewise).  The products q_t.k_s of finite

@@ -27,6 +27,8 @@
 // behind a second barrier (437), interleaving by hand (425 of 422 then), three workgroups a
 // CU (1140, spills).
 
+#include <float.h>
+
 #include "block_launch.h"
 #include "layer_launch.h"
 #include "ssd_device.h"
@@ -35,14 +37,17 @@ namespace ssd {
 
 namespace {
 
+// Rates below -1024 count as it: e^-1024 is 0, and 0 tokens decay by 1 at any rate,
+// -infinity included.
+__device__ __forceinline__ float least_rate(float r) { return r < -1024.f ? -1024.f : r; }
+
 // e^{r n}.  r log2(e) is held in two floats, and what the product with n loses is put
 // back, so that far tokens' weights are as exact as near ones' (2^x alone would be
-// off by half a step of x: 1.3e-6 of e^-30).  e^-1024 is 0: rates below it count as
-// it, so that 0 tokens decay by 1 at any rate, -infinity included.
+// off by half a step of x: 1.3e-6 of e^-30).
 struct Rate {
     float hi, lo;
     __device__ __forceinline__ explicit Rate(float r) {
-        r = r < -1024.f ? -1024.f : r;
+        r = least_rate(r);
         hi = r * kLog2e;
         lo = fmaf(r, kLog2e, -hi) + r * 1.9259630e-8f;   // (what log2(e) as a float lacks)
     }
@@ -50,6 +55,29 @@ struct Rate {
         const float x = (float)n, p = x * hi, e = fmaf(x, lo, fmaf(x, hi, -p));
         const float v = fast_exp2(p);
         return fmaf(v * 0.6931472f, e, v);
+    }
+};
+
+// The factors by which one state is multiplied over and over, e^{r n} each time.  One float
+// for all of them would be off by the same 2^-25 every time, which adds up: over 65536 tokens
+// at r = -3e-6 the start state would weigh 5.7e-5 too much.  So what each factor leaves is
+// put into the next one, and the product of any number of them is off by half a step.  (The
+// exponential is taken in double, once a walk.)
+struct Turn {
+    float whole, less, by, left;   // e^{r n} as a float, what it lacks, 1 / whole; still owed
+    __device__ __forceinline__ Turn(float r, int64_t n) {
+        const double e = exp((double)least_rate(r) * (double)n);
+        whole = (float)e;
+        const bool held = whole > 0x1p-100f && whole < 0x1p100f;   // (else all is forgotten)
+        by = held ? 1.f / whole : 0.f;
+        less = held ? (float)(e - (double)whole) * by : 0.f;
+        left = 0.f;
+    }
+    __device__ __forceinline__ float next() {
+        left += less;
+        const float f = fmaf(whole, left, whole);
+        left -= (f - whole) * by;
+        return f;
     }
 };
 
@@ -493,7 +521,7 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(const Jobs a) {
         const int j = threadIdx.x % L, n = threadIdx.x < L ? L : cut;
         ws[threadIdx.x / L][j] = j < n ? job.up * rate.over(n - 1 - j + late) : 0.f;
     }
-    const float turn_whole = rate.over(L), turn_cut = rate.over(cut);
+    Turn turns(a.decay[h], L);
 
     // The next chunk's tiles have arrived, for all wavefronts, and this one's are free.
     // Behind the next one's loads at least the later chunks' loads and this chunk's stores
@@ -622,7 +650,7 @@ __global__ __launch_bounds__(256, 2) void attn_kernel(const Jobs a) {
             out += out_turn;
         }
         if (WHOLE || job.s1) {
-            const float turn = WHOLE ? turn_whole : turn_cut;
+            const float turn = WHOLE ? turns.next() : rate.over(cut);
             const float *w = ws[!WHOLE] + M::kRun * (lane >> 4);
 #pragma unroll
             for (int v = 0; v < NV; ++v)
@@ -707,6 +735,7 @@ __global__ __launch_bounds__(256) void attn_chain_kernel(const Chains a) {
     if (e >= a.state_size) return;
     const Chain c = a.c[blockIdx.y];
     const Rate rate(a.decay[bh % a.H]);
+    Turn turns(a.decay[bh % a.H], a.seg_tokens);
     int64_t len = a.T;
     if (a.lens) {
         const int64_t n = a.lens[bh / a.H];
@@ -722,7 +751,7 @@ __global__ __launch_bounds__(256) void attn_chain_kernel(const Chains a) {
         f32x4 own = {0.f, 0.f, 0.f, 0.f};
         if (sg + 1 < a.nseg) own = *reinterpret_cast<const f32x4 *>(p);
         *reinterpret_cast<f32x4 *>(p) = cur;
-        cur = rate.over((int)n) * cur + own;
+        cur = (n == a.seg_tokens ? turns.next() : rate.over((int)n)) * cur + own;
     }
 }
 
@@ -1024,7 +1053,8 @@ namespace {
 // workgroup serves one (b, h): LPR lanes cover a row of the state with 16-byte
 // accesses, so 256 / LPR rows are in flight per access, kBatch accesses before
 // the first is used; a lane's four columns are summed over its rows in
-// registers and over the workgroup's rows through LDS, in a fixed order.  (256 sequences
+// registers and over the workgroup's rows through LDS, in a fixed order.  e^r is two floats:
+// one alone is off by the same 2^-25 for every token that a state lives through.  (256 sequences
 // of 32 heads of 128 x 128: 206 us, 5.2 TB/s; kBatch 2, 8, 16: 209, 200, 228, and with 64 x
 // 64 states 103, 103, 105, 162 for 2, 4, 8, 16.)
 template <typename T, int LPR>
@@ -1046,7 +1076,12 @@ __global__ __launch_bounds__(256) void attn_step_kernel(const AttnArgs a) {
     const T *q = static_cast<const T *>(a.q) + b * a.qb + (int64_t)h * a.K;
     const T *k = static_cast<const T *>(a.k) + b * a.kb + (int64_t)hg * a.K;
     const T *v = static_cast<const T *>(a.v) + b * a.vb + (int64_t)hg * a.V;
-    const float d = Rate(a.decay[h]).over(1);
+    const double e = exp((double)least_rate(a.decay[h]));
+    const float d = (float)e, less = (float)(e - (double)d);
+    // (an infinity times what d lacks would be one of either sign, or NaN)
+    auto decayed = [&](float s, float add) {
+        return fmaf(s, d, fmaf(fminf(fmaxf(s, -FLT_MAX), FLT_MAX), less, add));
+    };
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < a.V) {
         const float4 vv = load4(v + col);
@@ -1069,10 +1104,10 @@ __global__ __launch_bounds__(256) void attn_step_kernel(const AttnArgs a) {
             for (int i = 0; i < kBatch; ++i) {
                 const int row = r0 + i * RPI;
                 float4 n;
-                n.x = d * s[i].x + kk[i] * vv.x;
-                n.y = d * s[i].y + kk[i] * vv.y;
-                n.z = d * s[i].z + kk[i] * vv.z;
-                n.w = d * s[i].w + kk[i] * vv.w;
+                n.x = decayed(s[i].x, kk[i] * vv.x);
+                n.y = decayed(s[i].y, kk[i] * vv.y);
+                n.z = decayed(s[i].z, kk[i] * vv.z);
+                n.w = decayed(s[i].w, kk[i] * vv.w);
                 sum.x += qq[i] * n.x;
                 sum.y += qq[i] * n.y;
                 sum.z += qq[i] * n.z;
