@@ -669,7 +669,7 @@ ssd_status ssd_cache_read(const void *codes, const float *scales, int64_t n, int
  *               and final_state is the state at the length.
  *   y           [Bt, T, H, V]     io dtype  out  dense
  *   final_state [Bt, H, K, V]     float32   out  NULL = not written; may equal
- *               init_state
+ *               init_state, and may not overlap it otherwise (SSD_ERR_UNSUPPORTED)
  *
  * K and V are multiples of 8 in [8, 256].  workspace:
  * ssd_linear_attn_workspace_size(dims) bytes (0 where sequences and heads alone
@@ -727,7 +727,8 @@ ssd_status ssd_linear_attn_step(float *state, int64_t num_slots, const int32_t *
  *   dq      [Bt, T, H, K]  io dtype  out  dense; zero past the lengths
  *   dk, dv  [Bt, T, G, K], [Bt, T, G, V]  io dtype  out  likewise, summed in
  *           float32 over the heads that share a head of k and v
- *   dinit   [Bt, H, K, V]  float32   out  NULL = not written
+ *   dinit   [Bt, H, K, V]  float32   out  NULL = not written; an overlap with dfinal or
+ *           init_state is refused (SSD_ERR_UNSUPPORTED)
  * The states are formed again.  workspace: ssd_linear_attn_bwd_workspace_size(dims)
  * bytes, 16-byte aligned (NULL where that is 0).  With T = 0 dinit = dfinal.  No
  * atomics: reruns are bitwise identical.

@@ -65,6 +65,16 @@ ssd_status check_workspace(void *workspace, size_t bytes, size_t need) {
     return SSD_OK;
 }
 
+// States that a launch writes at its workgroups' ends while others may still be to read theirs.
+ssd_status check_states_apart(const char *out_name, const float *out, const char *in_name,
+                              const float *in, const ssd::AttnArgs &a) {
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+    const uint64_t bytes = (uint64_t)(a.Bt * a.H) * (uint64_t)(a.K * a.V) * sizeof(float);
+    if (out && in && (o < i ? i - o : o - i) < bytes)
+        return fail(SSD_ERR_UNSUPPORTED, "%s overlaps %s", out_name, in_name);
+    return SSD_OK;
+}
+
 ssd_status check_attn(const ssd_attn_dims *d, bool need_seq, ssd::AttnArgs *a) {
     if (!d) return fail(SSD_ERR_NULL, "dims is NULL");
     CHECK(check_range("batch", d->batch, 0, kMaxDim));
@@ -236,6 +246,8 @@ ssd_status ssd_linear_attn_fwd(const void *q, const void *k, const void *v, cons
     OPTIONAL_PTR(seq_lens);
     OPTIONAL_PTR(final_state);
     CHECK(check_workspace(workspace, workspace_bytes, ssd::attn_workspace(a)));
+    if (final_state != init_state)
+        CHECK(check_states_apart("final_state", final_state, "init_state", init_state, a));
     if (a.Bt == 0 || (a.T == 0 && !final_state)) return ok();
     a.q = q;
     a.k = k;
@@ -303,6 +315,8 @@ ssd_status ssd_linear_attn_bwd(const void *q, const void *k, const void *v, cons
     OPTIONAL_PTR(dfinal);
     OPTIONAL_PTR(dinit);
     CHECK(check_workspace(workspace, workspace_bytes, ssd::attn_bwd_workspace(a)));
+    CHECK(check_states_apart("dinit", dinit, "dfinal", dfinal, a));
+    CHECK(check_states_apart("dinit", dinit, "init_state", init_state, a));
     if (a.Bt == 0 || (a.T == 0 && !dinit)) return ok();
     a.q = q;
     a.k = k;
