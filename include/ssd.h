@@ -680,10 +680,10 @@ ssd_status ssd_cache_read(const void *codes, const float *scales, int64_t n, int
  * to bf16 once.  A state is rounded once for every 32 tokens of a prompt and once a
  * step; what a decay's float lacks of e^{r n} is made good, so that errors of long
  * memories do not add up (a step that takes less than 2^-25 off a number leaves it).
- * No atomics: reruns are bitwise identical.  An infinity or a NaN in a token's q, k or v
- * reaches no output of an earlier token, of another sequence or of a head that does not
- * read it (the gradients: of a later token, likewise).  The products q_t.k_s of finite
- * tokens must not overflow, those of s > t included.
+ * No atomics: reruns are bitwise identical.  An infinity or a NaN in a token's k or v
+ * reaches its own and later tokens' y, in q its own alone, and no other sequence or head
+ * that does not read it; what it reaches is infinite or NaN.  The products q_t.k_s of
+ * finite tokens must not overflow, those of s > t included.
  */
 typedef struct {
     int64_t batch;           /* Bt >= 0 */
@@ -731,7 +731,11 @@ ssd_status ssd_linear_attn_step(float *state, int64_t num_slots, const int32_t *
  *           init_state is refused (SSD_ERR_UNSUPPORTED)
  * The states are formed again.  workspace: ssd_linear_attn_bwd_workspace_size(dims)
  * bytes, 16-byte aligned (NULL where that is 0).  With T = 0 dinit = dfinal.  No
- * atomics: reruns are bitwise identical.
+ * atomics: reruns are bitwise identical.  An infinity or a NaN in a token's k or v
+ * reaches dq of its own and later tokens, in q or dy dk and dv of its own and earlier
+ * ones, and dinit; in dy dq, in v dk and in k dv it reaches at its own token alone.  The
+ * products q_t.k_s and dy_t.v_s of finite tokens must not overflow, those of s > t
+ * included.
  */
 size_t ssd_linear_attn_bwd_workspace_size(const ssd_attn_dims *dims);
 ssd_status ssd_linear_attn_bwd(const void *q, const void *k, const void *v, const float *log_decay,
