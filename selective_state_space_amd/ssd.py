@@ -34,12 +34,6 @@ The functions carry the C names:
   mixer, with its activation or gate;
 * :func:`ssd_w4_quantize`, :func:`ssd_w4_dequantize`, :func:`ssd_w4_linear` --
   projections with 4-bit weights;
-* :func:`ssd_linear_attn_fwd`, :func:`ssd_linear_attn_step`,
-  :func:`ssd_linear_attn_bwd` -- linear attention with a decay for each head;
-* :func:`ssd_group_norm_fwd`, :func:`ssd_group_norm_bwd` -- the group norm behind
-  a mixer, with its activation or gate;
-* :func:`ssd_w4_quantize`, :func:`ssd_w4_dequantize`, :func:`ssd_w4_linear` --
-  projections with 4-bit weights;
 * :func:`ssd_chunked_fwd_workspace_size`, :func:`ssd_chunked_fwd_workspace_layout`,
   :func:`ssd_chunked_bwd_workspace_size`, :func:`fwd_path` and
   :func:`set_path_override` (which path the forward takes, and a switch for
