@@ -874,27 +874,33 @@ Job fwd_job(const AttnArgs &a) {
 
 size_t state_floats(const AttnArgs &a) { return (size_t)(a.Bt * a.H) * a.K * a.V; }
 
-// 64 columns a workgroup (states of more than 128 rows have registers for no more), unless
-// 128 leave more than half the CUs one and none two (2048 tokens of heads of 128, us with 64
-// and 128: 160 sequences and heads 130, 108; 192: 132, 110; 224: 139, 116; of 4096 tokens
-// 128: 151, 218; 320: 390, 422; float32, 160: 637, 476).  Not in bf16 gradients (192
-// workgroups of the three recurrences: 104, 111; 216: 102, 102; float32 636, 459).
+// 64 or 128 columns a workgroup: 128 form the pairs half as often, 64 make twice the
+// workgroups.  (us with 64 and 128, bf16, heads of 128, by sequences times heads.)  64 up to
+// 128 of those (4096 tokens of 128: 180, 254; 2048 of 132: 126, 126), 128 above (2048 tokens of
+// 160: 132, 126; 192: 135, 129; 224: 145, 144; 4096 of 192: 267, 253; float32, 1024 of 160:
+// 327, 241), in bf16 also where the chip holds them twice over and more (4096 of 260: 393, 379;
+// 320: 464, 410; 512: 614, 521; 1024: 1219, 1028; 1024 of 260: 109, 110; 512: 161, 139), with
+// 64 state rows, whose pairs cost less, from 384 on (2048 of 320: 159, 166; 448: 202, 181).
+// States of more than 128 rows have registers for 64 only; bf16 gradients take them too (192
+// workgroups of the three recurrences: 122, 122; 216: 127, 124; float32, 192: 323, 229).
 // Segments, three or more, where at most half the CUs would have a workgroup, though keys
 // and values are read and the states formed twice.  bf16: up to two workgroups a CU, of 256
-// tokens or more (1 x 65536 tokens of 16 heads: 1, 4, 8, 16, 32 segments 1867, 743, 445,
-// 415, 430 us; 1 x 2048: 1, 4, 8, 16: 65, 40, 33, 36; 1 x 512 of 8 heads, 1 and 2: 19 and 25;
-// 4 sequences of 32 heads, 256 workgroups, 1 and 2: 151 and 225).  float32, whose matrix
-// instructions take 16 times as long: 64 tokens (2 x 256 of 4 heads, 1, 2, 4 segments: 44, 41,
-// 28; 2 x 160 of 6 heads of 64, 1 and 2: 17 and 20), and one workgroup a CU, since LDS holds
-// no more, unless that makes fewer than three (1 x 2048 of 16 heads, 8 and 16: 74 and 82;
-// gradients, 1, 4, 5: 317, 212, 179).
+// tokens or more (1 x 65536 tokens of 16 heads: 1, 4, 8, 16, 32 segments 2412, 892, 532,
+// 452, 456 us; 1 x 2048: 1, 4, 8, 16: 81, 45, 35, 38; 1 x 512 of 8 heads, 1 and 2: 24 and 28;
+// 4 sequences of 32 heads, 256 workgroups, 1, 2, 4: 180, 205, 221; gradients of 4 x 2048 tokens
+// of 16 heads, 384 workgroups, 1 to 4: 121, 137, 151, 147, of 2 x 4096 153, 168, 168, 146).
+// float32, whose matrix instructions take 16 times as long: 64 tokens (2 x 256 of 4 heads, 1,
+// 2, 4 segments: 45, 42, 28; 2 x 160 of 6 heads of 64, 1 and 2: 17 and 20), and one workgroup
+// a CU, since LDS holds no more, unless that makes fewer than three (1 x 2048 of 16 heads, 8
+// and 16: 77 and 84; gradients, 1, 4, 5: 322, 221, 184).
 AttnLayout layout_of(const AttnArgs &a, int jobs) {
     AttnLayout l;
     const int64_t wide = jobs > 1 && a.K > a.V ? a.K : a.V;
     const int64_t rows = a.Bt * a.H * jobs, half = rows * ((wide + 127) / 128);
     const int64_t narrow = jobs > 1 && a.V < a.K ? a.V : a.K;    // the fewest state rows
-    l.v_cols = wide > 64 && narrow <= 128 && half > 128 && half <= 256 && !(a.bf16 && jobs > 1)
-                   ? 128 : 64;
+    const bool many = a.bf16 && half > (a.K > 64 ? 256 : 384);
+    l.v_cols = wide > 64 && narrow <= 128 && half > 128 && (half <= 256 || many) &&
+                       !(a.bf16 && jobs > 1) ? 128 : 64;
     const int64_t groups = rows * ((wide + l.v_cols - 1) / l.v_cols);
     const int64_t most = a.T / (a.bf16 ? 256 : 64);
     int64_t seg = groups > 0 && groups <= 128 ? 512 / groups : 1;
