@@ -114,10 +114,12 @@ __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint8_t *__res
 // A wavefront takes NT tiles of 16 outputs over its share of the inputs, 64 at a time;
 // the shares of a workgroup's wavefronts are added through LDS, in order.  Rows and codes
 // are loaded into the wavefront's own part of LDS, whole lines at a time and three steps
-// ahead (64 rows, 5120 inputs, 2560 outputs: 14 us; one step ahead, 22): read straight into
-// operands, 16 rows 16 bytes at a time, they came at 11 bytes a cycle and CU (26 us).  What
-// bounds it is the reading of x, once for every 16 or 32 outputs, out of the L2 caches (48
-// rows: 79 MB in some 8 us); the codes' 6.6 MB alone would take 1.5.
+// ahead (64 rows, 5120 inputs, 2560 outputs: 13 us; one step ahead, 22 where three took 14):
+// read straight into operands, 16 rows 16 bytes at a time, they came at 11 bytes a cycle and CU
+// (26 us).  What bounds it is latency: a wavefront's share is a chain of steps (20 of 5120
+// inputs), each a trip to L2 or memory that three steps cover in part.  x is read once for
+// every 16 or 32 outputs (48 rows of 5120 for 2560: 39 MB in some 8 us, far below what the L2
+// caches give); the codes' 6.6 MB alone would take 1.5.
 //
 // 8 inputs of one row: as they lie in LDS, and as operands in the codes' order (0 4 1 5 2 6 3 7).
 template <typename T>
@@ -357,7 +359,8 @@ __global__ __launch_bounds__(256) void w4_linear_kernel(const W4Args a) {
 // matrix instruction whose 16 rows are mostly empty.  The rows lie in LDS, bf16 ones in
 // the codes' order, so that two products take one instruction; a lane reads 16 codes
 // at a time (8 bytes, of one group), all of a slab's before the first is used, and
-// its partial sums of 24 x are taken off as above.  10576 x 2560, one row: 7.1 us in a
+// its partial sums of 24 x are taken off as above (float32 rows take codes one at a time: 2
+// rows, whole calls, 11.9 us for bf16's 9.6).  10576 x 2560, one row: 7.1 us in a
 // profile, of which 14.4 MB would take 3.0 at a copy's rate (661 workgroups of one slab
 // each: the start of the launch and one trip to memory and back).
 constexpr int kSlab = 4096;     // inputs that LDS holds at a time
@@ -500,14 +503,17 @@ __global__ __launch_bounds__(256) void w4_rows_kernel(const W4Args a) {
     }
 }
 
-// One or two tiles of outputs: two halve the reading of x, but also the workgroups, so they
-// are taken where one each would not be on the chip at once (48 rows x 5120 x 2560, 160
-// workgroups: 13.0 us with one, 17.4 with two; 64 x 1664 x 32768, 2048: 63 and 48).
+// One or two tiles of outputs (16 or 32): two halve the reading of x, but also the workgroups,
+// so they are taken where one each would be more than a workgroup a CU (rows x inputs x
+// outputs, us with one and two tiles of outputs; bf16: 64 x 8192 x 1024, 128 workgroups of
+// one: 10.7, 14.4; 32 x 5120 x 2560, 160: 9.9, 13.0; 64 x 5120 x 2560, 320: 13.8, 13.0; 32 x 5120
+// x 5120, 320: 14.1, 13.1; 3 x 1664 x 32768, 2048: 15.6, 12.6; 64 x 1664 x 32768, 4096: 47.7,
+// 37.1; float32: 64 x 8192 x 1024, 256: 19.0, 23.8; 16 x 5120 x 2560, 160: 13.0, 16.4; 32 x
+// 5120 x 2560, 320: 19.1, 16.7; 64 x 1664 x 32768, 8192: 112.5, 78.3).
 template <typename T, int RT>
 void launch_tiles(const W4Args &a, hipStream_t st) {
-    constexpr int kLds = 4 * 4 * (16 * RT * 64 * sizeof(T) + 1024);
     const int64_t tiles = (a.outputs + 15) / 16, parts = (a.rows + 16 * RT - 1) / (16 * RT);
-    if (tiles * parts <= 256 * (160 * 1024 / kLds))
+    if (tiles * parts <= 256)
         w4_linear_kernel<T, RT, 1>
             <<<dim3((uint32_t)tiles, (uint32_t)parts), 256, 0, st>>>(a);
     else
@@ -523,12 +529,15 @@ void launch_rows(const W4Args &a, hipStream_t st) {
 // matrix instructions 9.5 and 9.6; with 4 rows 12.2 and 9.9).  A wavefront there takes four
 // outputs where that leaves two workgroups a CU, else two (6592 x 8192: 9.5 us, with four
 // 12.2).
-// More rows in tiles of 16, one or two a workgroup (bf16; rows x inputs x outputs, us with
-// one and two): two halve the reading of codes and fill what they read of x (20 x 1664 x
-// 32768: 22.6, 19.8; 64 x 2560 x 10576: 25.5, 21.0; 128 x 5120 x 5120: 31.6, 28.6), unless a
-// tile of few would stay empty (48 x 5120 x 2560: 10.5, 13.2; x 5120: 14.9, 17.9) or CUs idle
-// (32 x 8192 x 1024, 128 workgroups of one: 10.7, 13.0).  float32 always in single ones: three
-// terms of two tiles leave a CU one workgroup (32 x 1664 x 32768: 40.7, 48.0).
+// More rows in tiles of 16 rows, one or two a workgroup (bf16; rows x inputs x outputs, us with
+// one and two tiles of rows): two halve the reading of codes and fill what they read of x (20
+// x 1664 x 32768: 22.6, 19.8; 64 x 2560 x 10576: 25.5, 21.0; 128 x 5120 x 5120: 31.6, 28.6; with
+// a fifth, seventh or ninth tile half of whose pair stays empty too: 80 x 2560 x 10576: 28.8,
+// 25.9; 112: 38.0, 36.1; 144: 44.5, 41.6; x 5120 x 2560: 14.3, 13.6; 19.8, 18.0; 20.0, 19.1),
+// unless that is one of four (48 x 5120 x 2560: 10.3, 13.0; x 2560 x 10576: 20.0, 19.8; x 5120 x
+// 5120: 14.9, 17.9) or CUs would idle (32 x 8192 x 1024, 128 workgroups of one: 10.7, 13.0).
+// float32 always in single ones: three terms of two tiles leave a CU one workgroup (32 x 1664 x
+// 32768: 40.7, 48.0).
 template <typename T>
 void launch_linear(const W4Args &a, hipStream_t st) {
     if (a.rows <= 2) {
