@@ -362,7 +362,9 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float *__restrict_
 // of 1024: 262 us on a workgroup, 205), a workgroup in up to 4 (4 x 2048 tokens of 2048
 // channels, gradients, 4 accesses on a wavefront: 149 us, 1 on a workgroup: 54); what is
 // longer on 1024 lanes (8 x 4096 x 5120, one group, float32 gradients: 713 us with 2
-// accesses, 1905 with registers for 4).
+// accesses, 1905 with registers for 4).  Single channels are 2 or 4 bytes a lane and leave lanes
+// idle (8 x 4096 tokens, bf16, gated, 40 groups of 129 on 256 lanes each: 1035 us, one of 5121:
+// 444, where groups of 128 take 210; gradients of 4 x 2048: 313, 1007 and 87).
 struct NormShape {
     int vec, vpt, tpr;
 };

@@ -17,15 +17,20 @@
 // Per 16 columns of a bf16 state of 128 rows a chunk of 32 tokens takes 44 matrix
 // instructions of 16 x 16 x 32 and each wavefront 16 more for the pairs; bytes bound it
 // below (8 x 4096 tokens of 40 heads of 128: 1.34 GB, 280 us at a copy's rate).  Reached:
-// 381 us there (3.5 TB/s; matrix instructions 31% of the cycles, vector ones 34%), 128
-// sequences and heads of 4096 tokens 151 (3.6 TB/s), 1 x 65536 tokens of 16 heads, in two
-// passes, 404; gradients of 4 x 2048 tokens of 16 heads 108 (235 MB, 49 at a copy's rate).
+// 414 us there (3.3 TB/s; matrix instructions 28% of the cycles, vector ones 41%), 128
+// sequences and heads of 4096 tokens 181 (3.0 TB/s), 1 x 65536 tokens of 16 heads, in two
+// passes, 454; gradients of 4 x 2048 tokens of 16 heads 131 (235 MB, 49 at a copy's rate).
 // What bounds it is that a wavefront's chunk is a chain (operands out of LDS, products,
-// rounding, products) which two wavefronts a SIMD do not cover, and whole workgroups over
-// CUs (640 of them on 512 places).  Tried and slower than 390 us: chunks of 64 tokens
-// through registers (636), eight wavefronts of 16 columns (405), pairs shared through LDS
-// behind a second barrier (437), interleaving by hand (425 of 422 then), three workgroups a
-// CU (1140, spills).
+// splitting, products): with two wavefronts a SIMD the time of a chunk, 4500 cycles in those
+// gradients, is about the sum of what both issue (350 vector instructions of 4 cycles, 60
+// matrix ones of 16).  The long one's outputs pass comes near a copy's rate as well (4.8 TB/s):
+// its two slices of 64 columns read q and k 1.6 times.  Tried with bf16 and slower, while
+// operands were one term and 8 x 4096 took 390: chunks of 64 tokens through registers (636),
+// eight wavefronts of 16 columns (405), pairs shared through LDS behind a second barrier
+// (437), interleaving by hand (425 of 422 then), three workgroups a CU (1140, spills); since,
+// for 121 in the gradients: the terms' difference by matrix instructions (118 to 120, but 188
+// for 129 with 128 columns), by dot products (126), accumulators of its own for lo (129).
+// None of it was tried with float32.
 
 #include <float.h>
 
@@ -282,7 +287,7 @@ __device__ __forceinline__ f32x4 mma_weighted(f32x4 a, f32x4 b, f32x4 c) {
 
 // Accumulators as an operand (the state against q, the pairs' weights against the values):
 // for bf16 two terms, hi cut and lo rounded, which leave at most 2^-15 of each element, so that an
-// output is rounded to bf16 once, where it is stored.  (One term, 2^-9 of each element twice
+// output is rounded to bf16 once, where it is stored.  (One term, 2^-8 of each element twice
 // over, was 0.0023 of the outputs' norm off where that one rounding is 0.0017, at, us with one
 // term and with two: 8 x 4096 tokens of 40 heads of 128 396 and 436, 1 x 65536 of 16 406 and
 // 438, gradients of 4 x 2048 of 16 100 and 121.)
