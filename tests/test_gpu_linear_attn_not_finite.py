@@ -104,3 +104,26 @@ def test_cut_over_time(name, bad, io):
             assert_near(got[m][:, at + 1:], want[m][:, at + 1:], bar, m)
         keep = [t for t in range(n) if t != at]
         assert_near(got["dq"][:, keep], want["dq"][:, keep], bar, "dq")
+
+
+@pytest.mark.parametrize("io", TYPES)
+@pytest.mark.parametrize("Bt,K", [(40, 64), (40, 128), (65, 128)])
+@pytest.mark.parametrize("at", [0, 17, 40, 44])
+def test_prompts_of_many_sequences(at, Bt, K, io):
+    """Workgroups of 128 columns (65 sequences: in bf16 alone): a bad k, v or q leaves the tokens
+    before it, other heads, other sequences and, in v, other columns."""
+    V, n = 128, 45
+    lay = ssd.linear_attn_layout(ssd.AttnDims(Bt, n, H, H, K, V, 0, 0, 0, 0, 0, 0,
+                                              1 if io == "bf16" else 0, 1.0))
+    assert lay.fwd_cols == (128 if Bt == 40 or io == "bf16" else 64)
+    c, kw = attn_inputs(4, Bt, n, H, H, K, V, TYPES[io], init=True)
+    y, _ = ssd.ssd_linear_attn_fwd(**c, **kw)
+    bar = 2 * attn_bar(TYPES[io], n + 2 * max(K, V) + 64)
+    for i, name in enumerate("kvq"):
+        d = {m: t.clone() for m, t in c.items()}
+        d[name][1, at, 2, 3] = BAD[(i + at) % 3]
+        got, _ = ssd.ssd_linear_attn_fwd(**d, **kw)
+        tokens, columns = slice(at, at + 1 if name == "q" else n), 3 if name == "v" else slice(None)
+        same_but(got[:2], y[:2], [2], tokens, columns, bar, name)
+        assert torch.equal(got[2:], y[2:])
+        assert not torch.isfinite(got[1, tokens, 2, columns]).any()
